@@ -25,11 +25,27 @@ STATUS = {0: "SUCCESS", 1: "INVALID_VALUE", 2: "NOT_SUPPORTED", 3: "NOT_INITIALI
 EXPORTS = ["gemm_create", "gemm_destroy", "gemm_set_stream", "gemm_run", "gemm_run_noalloc", "gemm_run_mx",
            "gemm_quantize_mx", "gemm_check_args", "gemm_query_policy", "gemm_set_policy",
            "gemm_lds_probe", "gemm_hw_probe", "gemm_policy_count", "gemm_policy_name", "gemm_version",
-           "gemm_status_string", "gemm_syrk", "gemm_syr2k", "gemm_symm", "gemm_trmm", "gemm_trsm"]
+           "gemm_status_string", "gemm_syrk", "gemm_syr2k", "gemm_symm", "gemm_trmm", "gemm_trsm",
+           "gemm_run_act", "gemm_run_dact", "gemm_act_mx", "gemm_act_grad_mx", "gemm_layernorm",
+           "gemm_layernorm_grad"]
 
 LOWER, UPPER = 0, 1
 LEFT, RIGHT = 0, 1
 NON_UNIT, UNIT = 0, 1
+
+# activations by name (gemm_act_t), how the activation's argument is kept, element types
+ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+Z_NONE, Z_BF16, Z_MX = 0, 1, 2
+TYPE_BF16, TYPE_F32 = 0, 1
+
+
+class Epilogue(ctypes.Structure):
+    """gemm_epilogue_t"""
+    _fields_ = [("act", ctypes.c_int), ("bias_type", ctypes.c_int), ("bias", ctypes.c_void_p),
+                ("residual", ctypes.c_void_p), ("ld_residual", ctypes.c_int64), ("beta", ctypes.c_float),
+                ("z_kind", ctypes.c_int), ("z", ctypes.c_void_p), ("ld_z", ctypes.c_int64),
+                ("z_scales", ctypes.c_void_p), ("ld_z_scales", ctypes.c_int64)]
+
 
 _lib = None
 
@@ -101,10 +117,20 @@ def load_library():
     lib.gemm_symm.argtypes = [vp, i32, i32, i64, i64, f32, vp, i64, vp, i64, f32, vp, i64, i32]
     lib.gemm_trmm.argtypes = [vp, i32, i32, i32, i32, i64, i64, f32, vp, i64, vp, i64, vp, i64, i32]
     lib.gemm_trsm.argtypes = [vp, i32, i32, i32, i32, i64, i64, f32, vp, i64, vp, i64, i32]
+    lib.gemm_run_act.argtypes = [vp, i32, i32, i64, i64, i64, f32, vp, i64, vp, i64, ctypes.POINTER(Epilogue), vp, i64,
+                                 i32]
+    lib.gemm_run_dact.argtypes = [vp, i32, i32, i64, i64, i64, f32, vp, i64, vp, i64, i32, i32, vp, i64, vp, i64, vp,
+                                  vp, i64, i32]
+    lib.gemm_act_mx.argtypes = [vp, i64, i64, i32, vp, i64, vp, i64, vp, i64, vp, i64]
+    lib.gemm_act_grad_mx.argtypes = [vp, i64, i64, i32, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, i64]
+    lib.gemm_layernorm.argtypes = [vp, i64, i64, vp, i64, i32, vp, vp, i32, f32, vp, i64, i32, vp, vp]
+    lib.gemm_layernorm_grad.argtypes = [vp, i64, i64, vp, i64, i32, vp, i64, i32, vp, vp, vp, i32, vp, i64, vp, i64,
+                                        vp, vp]
     for fn in ["gemm_create", "gemm_destroy", "gemm_set_stream", "gemm_run", "gemm_run_noalloc", "gemm_check_args",
                "gemm_query_policy", "gemm_set_policy", "gemm_lds_probe", "gemm_hw_probe", "gemm_policy_count",
                "gemm_run_mx", "gemm_quantize_mx", "gemm_syrk", "gemm_syr2k", "gemm_symm", "gemm_trmm",
-               "gemm_trsm"]:
+               "gemm_trsm", "gemm_run_act", "gemm_run_dact", "gemm_act_mx", "gemm_act_grad_mx", "gemm_layernorm",
+               "gemm_layernorm_grad"]:
         getattr(lib, fn).restype = i32
     _lib = lib
     return lib
@@ -149,9 +175,104 @@ def _ptr(t) -> int:
 
 
 def _ld(t) -> int:
-    # row-major with unit column stride: the leading dimension is the row stride
-    assert t.dim() == 2 and t.stride(1) == 1, "operands must be row-major 2-D views"
-    return int(t.stride(0))
+    # row-major with unit column stride: the leading dimension is the row stride (a matrix of
+    # one row or without elements has any)
+    assert t.dim() == 2 and (t.stride(1) == 1 or t.shape[1] <= 1 or t.shape[0] == 0), \
+        "operands must be row-major 2-D views"
+    return int(t.stride(0)) if t.shape[0] > 1 else max(int(t.stride(0)), int(t.shape[1]), 1)
+
+
+# ---- argument checks of the MLP-block operators: what the C-ABI cannot see of a tensor
+
+def _ld0(t) -> int:
+    return 0 if t is None else _ld(t)
+
+
+def _act(name: str) -> int:
+    try:
+        return ACTS[name]
+    except KeyError:
+        raise ValueError(f"act is one of {', '.join(ACTS)}: got {name!r}") from None
+
+
+def _type(t) -> int:
+    import torch
+    if t.dtype == torch.bfloat16:
+        return TYPE_BF16
+    if t.dtype == torch.float32:
+        return TYPE_F32
+    raise ValueError(f"bfloat16 or float32 is wanted: got {t.dtype}")
+
+
+def _bf16(t, name):
+    if _type(t) != TYPE_BF16:
+        raise ValueError(f"{name} has to be bfloat16: got {t.dtype}")
+
+
+def _vec(t, n, name, f32=False):
+    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} has to be a contiguous vector of {n} values: got {tuple(t.shape)}")
+    if _type(t) != TYPE_F32 and f32:
+        raise ValueError(f"{name} has to be float32: got {t.dtype}")
+
+
+def _same(t, like, name, dtype=False):
+    if t.shape != like.shape or (dtype and t.dtype != like.dtype):
+        raise ValueError(f"{name} has to be {tuple(like.shape)}" + (f" {like.dtype}" if dtype else "") +
+                         f": got {tuple(t.shape)} {t.dtype}")
+
+
+def _weights(gamma, beta, n) -> int:
+    kinds = set()
+    for t, name in ((gamma, "gamma"), (beta, "beta")):
+        if t is not None:
+            _vec(t, n, name)
+            kinds.add(_type(t))
+    if len(kinds) > 1:
+        raise ValueError("gamma and beta have to be of one type")
+    return kinds.pop() if kinds else TYPE_F32
+
+
+def _z(z, scales, M, N, mx=False):
+    """(kind, pointer, stride, scale pointer, scale stride) of a kept activation argument."""
+    import torch
+    if z.shape != (M, N):
+        raise ValueError(f"z has to be {(M, N)}: got {tuple(z.shape)}")
+    if scales is None:
+        if mx:
+            raise ValueError("codes need their scales")
+        _bf16(z, "z without scales")
+        return Z_BF16, z.data_ptr(), _ld(z), None, 0
+    if z.dtype not in (torch.float8_e4m3fn, torch.uint8) or scales.dtype != torch.uint8:
+        raise ValueError("8-bit z: float8_e4m3fn or uint8 codes with uint8 scales")
+    if scales.shape != (M, (N + 31) // 32):
+        raise ValueError(f"z_scales has to be {(M, (N + 31) // 32)}: got {tuple(scales.shape)}")
+    return Z_MX, z.data_ptr(), _ld(z), scales.data_ptr(), _ld(scales)
+
+
+def _k_of(A, B, transA, transB, M, N) -> int:
+    m, k = (A.shape[1], A.shape[0]) if transA else A.shape
+    n, k2 = B.shape if transB else (B.shape[1], B.shape[0])
+    if m != M or n != N or k != k2:
+        raise ValueError(f"op(A) {(m, k)} times op(B) {(k2, n)} is not C's {(M, N)}")
+    return k
+
+
+def _in_out(A, B, C) -> int:
+    import torch
+    if A.dtype != B.dtype or A.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+        raise ValueError(f"A and B have to be bfloat16 or float8_e4m3fn: got {A.dtype}, {B.dtype}")
+    f32 = _type(C) == TYPE_F32
+    if A.dtype == torch.bfloat16:
+        return BF16_F32 if f32 else BF16_BF16
+    return E4M3_F32 if f32 else E4M3_BF16
+
+
+def _on(device, *tensors):
+    """Every tensor (None: absent) lives on the handle's device."""
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"tensors of cuda:{device} are wanted: got one on {t.device}")
 
 
 class Gemm:
@@ -364,6 +485,125 @@ class Gemm:
         if st != 0:
             raise GemmError("gemm_trsm", st)
         return B
+
+    # ---------------------------------------------------------------- MLP-block operators
+
+    def run_act(self, A, B, C, transA: int = 0, transB: int = 0, alpha: float = 1.0, act: str = "none", bias=None,
+                residual=None, beta: float = 1.0, z=None, z_scales=None):
+        """C <- act(Z) + beta*residual with Z = alpha*op(A)*op(B) + bias (gemm_run_act).
+
+        A and B bf16 or float8_e4m3fn, C bf16 or float32, bias (N values) bf16 or float32,
+        residual of C's type (C itself allowed).  Z is left in `z`: bf16, or with z_scales
+        (uint8 [M][ceil(N/32)]) block-scaled E4M3 codes (float8_e4m3fn or uint8)."""
+        M, N = C.shape
+        ep = Epilogue(_act(act))
+        if bias is not None:
+            _vec(bias, N, "bias")
+            ep.bias, ep.bias_type = bias.data_ptr(), _type(bias)
+        if residual is not None:
+            _same(residual, C, "residual", dtype=True)
+            ep.residual, ep.ld_residual, ep.beta = residual.data_ptr(), _ld(residual), beta
+        if z is not None:
+            ep.z_kind, ep.z, ep.ld_z, ep.z_scales, ep.ld_z_scales = _z(z, z_scales, M, N)
+        K = _k_of(A, B, transA, transB, M, N)
+        _on(self.device, A, B, C, bias, residual, z, z_scales)
+        self._bind(C)
+        st = self.lib.gemm_run_act(self.handle, int(transA), int(transB), M, N, K, alpha, A.data_ptr(), _ld(A),
+                                   B.data_ptr(), _ld(B), ctypes.byref(ep), C.data_ptr(), _ld(C), _in_out(A, B, C))
+        if st != 0:
+            raise GemmError("gemm_run_act", st)
+        return C
+
+    def run_dact(self, A, B, C, z, z_scales=None, transA: int = 0, transB: int = 0, alpha: float = 1.0,
+                 act: str = "none", dbias=None):
+        """C <- (alpha*op(A)*op(B)) * act'(z); dbias (float32, N values) its column sums
+        (gemm_run_dact).  z as run_act or act_mx left it."""
+        M, N = C.shape
+        kind, zp, ldz, sp, lds = _z(z, z_scales, M, N)
+        if dbias is not None:
+            _vec(dbias, N, "dbias", f32=True)
+        K = _k_of(A, B, transA, transB, M, N)
+        _on(self.device, A, B, C, z, z_scales, dbias)
+        self._bind(C)
+        st = self.lib.gemm_run_dact(self.handle, int(transA), int(transB), M, N, K, alpha, A.data_ptr(), _ld(A),
+                                    B.data_ptr(), _ld(B), _act(act), kind, zp, ldz, sp, lds, _ptr(dbias),
+                                    C.data_ptr(), _ld(C), _in_out(A, B, C))
+        if st != 0:
+            raise GemmError("gemm_run_dact", st)
+        return C
+
+    def act_mx(self, z, out, codes, scales, act: str = "none"):
+        """out <- act(z) and z's block-scaled E4M3 checkpoint (gemm_act_mx); z and out bf16."""
+        M, N = z.shape
+        _bf16(z, "z")
+        _same(out, z, "out", dtype=True)
+        _, qp, ldq, sp, lds = _z(codes, scales, M, N, mx=True)
+        _on(self.device, z, out, codes, scales)
+        self._bind(z)
+        st = self.lib.gemm_act_mx(self.handle, M, N, _act(act), z.data_ptr(), _ld(z), out.data_ptr(), _ld(out), qp,
+                                  ldq, sp, lds)
+        if st != 0:
+            raise GemmError("gemm_act_mx", st)
+        return out
+
+    def act_grad_mx(self, codes, scales, act: str = "none", dh=None, dz=None, dbias=None, h=None):
+        """From the checkpoint: dz <- dh * act'(z), dbias (float32) its column sums, h <- act(z)
+        (gemm_act_grad_mx); dh, dz and h bf16, each output optional."""
+        M, N = codes.shape
+        _, qp, ldq, sp, lds = _z(codes, scales, M, N, mx=True)
+        for t, name in ((dh, "dh"), (dz, "dz"), (h, "h")):
+            if t is not None:
+                _bf16(t, name)
+                _same(t, codes, name)
+        if dbias is not None:
+            _vec(dbias, N, "dbias", f32=True)
+        _on(self.device, codes, scales, dh, dz, dbias, h)
+        self._bind(codes)
+        st = self.lib.gemm_act_grad_mx(self.handle, M, N, _act(act), qp, ldq, sp, lds, _ptr(dh), _ld0(dh), _ptr(dz),
+                                       _ld0(dz), _ptr(dbias), _ptr(h), _ld0(h))
+        if st != 0:
+            raise GemmError("gemm_act_grad_mx", st)
+        return dz
+
+    def layernorm(self, x, y, gamma=None, beta=None, eps: float = 1e-5, mean=None, rstd=None):
+        """y <- layer norm of x's rows, times gamma plus beta (gemm_layernorm); mean and rstd
+        (float32, one per row) receive the statistics."""
+        M, N = x.shape
+        _same(y, x, "y")
+        wt = _weights(gamma, beta, N)
+        for t, name in ((mean, "mean"), (rstd, "rstd")):
+            if t is not None:
+                _vec(t, M, name, f32=True)
+        _on(self.device, x, y, gamma, beta, mean, rstd)
+        self._bind(x)
+        st = self.lib.gemm_layernorm(self.handle, M, N, x.data_ptr(), _ld(x), _type(x), _ptr(gamma), _ptr(beta), wt,
+                                     eps, y.data_ptr(), _ld(y), _type(y), _ptr(mean), _ptr(rstd))
+        if st != 0:
+            raise GemmError("gemm_layernorm", st)
+        return y
+
+    def layernorm_grad(self, dy, x, mean, rstd, dx, gamma=None, dgamma=None, dbeta=None, residual=None):
+        """dx <- the gradient of layernorm at x (+ residual), dgamma and dbeta (float32) those
+        of its weights (gemm_layernorm_grad)."""
+        M, N = x.shape
+        _same(dy, x, "dy")
+        _same(dx, x, "dx", dtype=True)
+        if residual is not None:
+            _same(residual, x, "residual", dtype=True)
+        _vec(mean, M, "mean", f32=True)
+        _vec(rstd, M, "rstd", f32=True)
+        for t, name in ((dgamma, "dgamma"), (dbeta, "dbeta")):
+            if t is not None:
+                _vec(t, N, name, f32=True)
+        wt = _weights(gamma, None, N)
+        _on(self.device, dy, x, mean, rstd, dx, gamma, dgamma, dbeta, residual)
+        self._bind(x)
+        st = self.lib.gemm_layernorm_grad(self.handle, M, N, dy.data_ptr(), _ld(dy), _type(dy), x.data_ptr(), _ld(x),
+                                          _type(x), mean.data_ptr(), rstd.data_ptr(), _ptr(gamma), wt, _ptr(residual),
+                                          _ld0(residual), dx.data_ptr(), _ld(dx), _ptr(dgamma), _ptr(dbeta))
+        if st != 0:
+            raise GemmError("gemm_layernorm_grad", st)
+        return dx
 
     def query_policy(self, M, N, K, transA=0, transB=0, dtype=BF16_BF16, A_ptr=0, lda=None,
                      B_ptr=0, ldb=None, C_ptr=0, ldc=None) -> str:

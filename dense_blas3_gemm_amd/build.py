@@ -26,7 +26,8 @@ BUILD = os.path.join(PKG, "_build")
 SOURCES = [("api.cpp", "api", []), ("policy.cpp", "policy", []), ("kernel_simt.hip", "kernel_simt", []),
            ("lds_probe.hip", "lds_probe", []), ("hw_probe.hip", "hw_probe", []),
            ("quantize_mx.hip", "quantize_mx", []),
-           ("blas3.cpp", "blas3", []), ("blas3_kernels.hip", "blas3_kernels", [])] + [
+           ("blas3.cpp", "blas3", []), ("blas3_kernels.hip", "blas3_kernels", []),
+           ("mlp.cpp", "mlp", []), ("act_mx.hip", "act_mx", []), ("layernorm.hip", "layernorm", [])] + [
     ("kernel_mfma.hip", f"kernel_mfma_{ta}{tb}", [f"-DDBGEMM_DMA_TA={ta}", f"-DDBGEMM_DMA_TB={tb}"])
     for ta in (0, 1) for tb in (0, 1)] + [
     ("kernel_mfma_dma.hip", f"kernel_mfma_dma_{ta}{tb}_p{part}",
@@ -114,9 +115,9 @@ def build(verbose: bool = False, incremental: bool = False) -> str:
 SAN_BUILD = os.path.join(PKG, "_build_san")
 SAN_OUT = os.path.join(SAN_BUILD, "libdbgemm_san.so")
 # The host-logic translation units (argument checks, policy choice, split and stream-K
-# sizing, the BLAS3 drivers) with AddressSanitizer and UndefinedBehaviorSanitizer on the
+# sizing, the BLAS3 and MLP-block drivers) with AddressSanitizer and UndefinedBehaviorSanitizer on the
 # host side only, linked with the kernels' objects of the regular build.
-SAN_SOURCES = ("api.cpp", "policy.cpp", "blas3.cpp")
+SAN_SOURCES = ("api.cpp", "policy.cpp", "blas3.cpp", "mlp.cpp")
 SAN_FLAGS = ["-O1", "-g", "-fPIC", "-std=c++17", f"--offload-arch={ARCH}", "-fno-omit-frame-pointer",
              "-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=undefined", "-fno-gpu-sanitize",
              "-Xarch_host", "-fno-sanitize-recover=undefined", "-Xclang", "-target-feature", "-Xclang",

@@ -1,0 +1,170 @@
+// Elementwise kernels of the MLP-block operators: the activation that leaves its argument
+// behind in block-scaled E4M3, the backward pass that reads it, the epilogue of a product
+// held in fp32, and the column sums that they share (bias gradients).
+//
+// Rows are walked by workgroups of 256 threads, 8 columns to a thread: a thread keeps its
+// columns over the rows that its workgroup takes, so a column sum is one register per
+// column, written once per thread as a partial row and added up by a second launch in a
+// fixed order (no atomics: the same bits every run).
+#include "epilogue.h"
+
+namespace dbgemm {
+namespace {
+
+constexpr int kThreads = 256;
+
+// Threads along the columns (a power of two, whole blocks of 32 columns: 4 threads) and rows
+// of threads of a workgroup, and the grid.
+struct RowGrid {
+  dim3 grid, block;
+  int parts;  // rows of threads over the whole grid along the rows
+};
+RowGrid row_grid(int64_t rows, int64_t cols, int64_t max_row_wgs, int max_parts) {
+  const int64_t chunks = (cols + 31) / 32 * 4;
+  unsigned tx = 4;
+  while (tx < (unsigned)kThreads && (int64_t)tx < chunks) tx *= 2;
+  const unsigned ty = kThreads / tx;
+  const int64_t gx = (chunks + tx - 1) / tx;
+  int64_t gy = (rows + ty - 1) / ty;
+  const int64_t cap = max_row_wgs / gx > 1 ? max_row_wgs / gx : 1;
+  if (gy > cap) gy = cap;
+  if (gy > 65535) gy = 65535;
+  if (max_parts > 0 && gy > max_parts / (int64_t)ty) gy = max_parts / (int64_t)ty > 1 ? max_parts / (int64_t)ty : 1;
+  if (gy < 1) gy = 1;
+  return {dim3((unsigned)gx, (unsigned)gy), dim3(tx, ty), (int)(gy * ty)};
+}
+
+// this thread's partial column sums, one row of `part` per row of threads
+__device__ __forceinline__ void put_partial(float* part, int64_t cols, int64_t n, const float (&cs)[8]) {
+  if (!part || n >= cols) return;
+  const int64_t p = (int64_t)blockIdx.y * blockDim.y + threadIdx.y;
+  ep_store8<false>(part + p * cols + n, cols - n < 8 ? (int)(cols - n) : 8, cs);
+}
+
+// Epilogue of a product in fp32 (the path of operands that the fused kernels do not take).
+__global__ __launch_bounds__(kThreads) void ep_rows_kernel(GemmEpArgs a, int64_t ldw) {
+  const int64_t k = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  if (k >= ((int64_t)a.N + 31) / 32 * 4) return;  // four lanes leave together
+  const int n = (int)(k * 8);
+  float cs[8] = {};
+  for (int64_t m = (int64_t)blockIdx.y * blockDim.y + threadIdx.y; m < a.M; m += (int64_t)gridDim.y * blockDim.y) {
+    float w[8];
+    const int nv = a.N - n < 8 ? (a.N > n ? a.N - n : 0) : 8;
+    ep_load8(a.ws + m * ldw + n, nv, w);
+    ep_apply8<false>(a, w, m, n, true, cs);
+  }
+  put_partial(a.ep.colsum, a.N, n, cs);
+}
+
+// Sums of the partial rows: 64 columns to a workgroup, the rows dealt to 16 waves, their sums
+// added in wave order.  blockIdx.y: which of the two sets of columns of a row.
+__global__ __launch_bounds__(1024) void colsum_kernel(const float* src, int parts, int64_t ld, int64_t cols,
+                                                      float* out0, float* out1, int accumulate) {
+  __shared__ float s[16][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t n = (int64_t)blockIdx.x * 64 + lane;
+  float* out = blockIdx.y ? out1 : out0;
+  if (!out) return;
+  src += blockIdx.y * cols;
+  float v = 0.f;
+  if (n < cols)
+    for (int p = wave; p < parts; p += 16) v += src[(int64_t)p * ld + n];
+  s[wave][lane] = v;
+  __syncthreads();
+  if (wave == 0 && n < cols) {
+    float t = accumulate ? out[n] : 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) t += s[i][lane];
+    out[n] = t;
+  }
+}
+
+__global__ __launch_bounds__(kThreads) void act_mx_kernel(int64_t rows, int64_t cols, int act, const uint16_t* z,
+                                                          int64_t ldz, uint16_t* h, int64_t ldh, uint8_t* q,
+                                                          int64_t ldq, uint8_t* sc, int64_t ldsc) {
+  const int64_t k = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  if (k >= (cols + 31) / 32 * 4) return;
+  const int64_t n = k * 8;
+  const int nv = cols - n < 8 ? (cols > n ? (int)(cols - n) : 0) : 8;
+  for (int64_t m = (int64_t)blockIdx.y * blockDim.y + threadIdx.y; m < rows; m += (int64_t)gridDim.y * blockDim.y) {
+    float v[8];
+    ep_load8(z + m * ldz + n, nv, v);
+    ep_store_mx(v, nv, (n & 31) == 0, q + m * ldq + n, sc + m * ldsc + (n >> 5));
+    ep_with_act(act, [&](auto ac) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = ep_act<decltype(ac)::value>(v[i]);
+    });
+    ep_store8<false>(h + m * ldh + n, nv, v);
+  }
+}
+
+__global__ __launch_bounds__(kThreads) void act_grad_mx_kernel(int64_t rows, int64_t cols, int act, const uint8_t* q,
+                                                               int64_t ldq, const uint8_t* sc, int64_t ldsc,
+                                                               const uint16_t* dh, int64_t lddh, uint16_t* dz,
+                                                               int64_t lddz, uint16_t* h, int64_t ldh, float* part) {
+  const int64_t k = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  const int64_t n = k * 8;
+  if (n >= cols) return;
+  const int nv = cols - n < 8 ? (int)(cols - n) : 8;
+  float cs[8] = {};
+  for (int64_t m = (int64_t)blockIdx.y * blockDim.y + threadIdx.y; m < rows; m += (int64_t)gridDim.y * blockDim.y) {
+    float z[8];
+    ep_load_mx(q + m * ldq + n, nv, sc[m * ldsc + (n >> 5)], z);
+    if (dh) {
+      float d[8];
+      ep_load8(dh + m * lddh + n, nv, d);
+      ep_with_act(act, [&](auto ac) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) d[i] *= ep_slope<decltype(ac)::value>(z[i]);
+      });
+#pragma unroll
+      for (int i = 0; i < 8; ++i) cs[i] += i < nv ? d[i] : 0.f;
+      if (dz) ep_store8<false>(dz + m * lddz + n, nv, d);
+    }
+    if (h) {
+      ep_with_act(act, [&](auto ac) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) z[i] = ep_act<decltype(ac)::value>(z[i]);
+      });
+      ep_store8<false>(h + m * ldh + n, nv, z);
+    }
+  }
+  put_partial(part, cols, n, cs);
+}
+
+}  // namespace
+
+hipError_t launch_ep_rows(const GemmEpArgs& a, int64_t ldw, int max_parts, int* parts, hipStream_t s) {
+  const RowGrid g = row_grid(a.M, a.N, 2048, a.ep.colsum ? max_parts : 0);
+  *parts = g.parts;
+  hipLaunchKernelGGL(ep_rows_kernel, g.grid, g.block, 0, s, a, ldw);
+  return hipGetLastError();
+}
+
+hipError_t launch_colsum(const float* src, int parts, int64_t ld, int64_t cols, float* out0, float* out1,
+                         int accumulate, hipStream_t s) {
+  if (cols == 0) return hipSuccess;
+  hipLaunchKernelGGL(colsum_kernel, dim3((unsigned)((cols + 63) / 64), out1 ? 2 : 1), dim3(1024), 0, s, src, parts, ld,
+                     cols, out0, out1, accumulate);
+  return hipGetLastError();
+}
+
+hipError_t launch_act_mx(int64_t rows, int64_t cols, int act, const void* z, int64_t ldz, void* h, int64_t ldh,
+                         uint8_t* q, int64_t ldq, uint8_t* sc, int64_t ldsc, hipStream_t s) {
+  const RowGrid g = row_grid(rows, cols, 4096, 0);
+  hipLaunchKernelGGL(act_mx_kernel, g.grid, g.block, 0, s, rows, cols, act, (const uint16_t*)z, ldz, (uint16_t*)h, ldh,
+                     q, ldq, sc, ldsc);
+  return hipGetLastError();
+}
+
+hipError_t launch_act_grad_mx(int64_t rows, int64_t cols, int act, const uint8_t* q, int64_t ldq, const uint8_t* sc,
+                              int64_t ldsc, const void* dh, int64_t lddh, void* dz, int64_t lddz, void* h,
+                              int64_t ldh, float* colsum, int max_parts, int* parts, hipStream_t s) {
+  const RowGrid g = row_grid(rows, cols, 2048, colsum ? max_parts : 0);
+  *parts = g.parts;
+  hipLaunchKernelGGL(act_grad_mx_kernel, g.grid, g.block, 0, s, rows, cols, act, q, ldq, sc, ldsc,
+                     (const uint16_t*)dh, lddh, (uint16_t*)dz, lddz, (uint16_t*)h, ldh, colsum);
+  return hipGetLastError();
+}
+
+}  // namespace dbgemm

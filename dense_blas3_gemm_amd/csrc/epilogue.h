@@ -1,0 +1,273 @@
+// Device side of the epilogues and of the activations: the functions and their slopes, and
+// what is done with eight consecutive columns of a product (or of a stored activation).
+// Included by kernel translation units only.
+#pragma once
+
+#include <type_traits>
+
+#include "e4m3_codec.h"
+#include "mlp_internal.h"
+
+namespace dbgemm {
+namespace {
+
+// Vectors at element alignment: global memory takes 8- and 16-byte accesses at any address,
+// so an odd leading dimension needs no path of its own.
+typedef unsigned short ep_u16x8 __attribute__((ext_vector_type(8)));
+typedef float ep_f32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int ep_u32x2 __attribute__((ext_vector_type(2)));
+typedef ep_u16x8 ep_u16x8_u __attribute__((aligned(2)));
+typedef ep_f32x4 ep_f32x4_u __attribute__((aligned(4)));
+typedef ep_u32x2 ep_u32x2_u __attribute__((aligned(1)));
+
+__device__ __forceinline__ float ep_bf16f(uint16_t b) { return __builtin_bit_cast(float, (uint32_t)b << 16); }
+__device__ __forceinline__ uint16_t ep_f32bf(float v) {
+  return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
+}
+
+// 8 elements at p, the first nv of them valid (the others read as zeros).
+__device__ __forceinline__ void ep_load8(const uint16_t* p, int nv, float (&v)[8]) {
+  if (nv == 8) {
+    const ep_u16x8 w = *(const ep_u16x8_u*)p;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = ep_bf16f(w[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < nv ? ep_bf16f(p[i]) : 0.f;
+  }
+}
+__device__ __forceinline__ void ep_load8(const float* p, int nv, float (&v)[8]) {
+  if (nv == 8) {
+    const ep_f32x4 a = *(const ep_f32x4_u*)p, b = *(const ep_f32x4_u*)(p + 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = a[i];
+      v[4 + i] = b[i];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < nv ? p[i] : 0.f;
+  }
+}
+// 8 elements of a matrix of either type
+__device__ __forceinline__ void ep_load8(const void* p, int64_t idx, int f32, int nv, float (&v)[8]) {
+  if (f32)
+    ep_load8((const float*)p + idx, nv, v);
+  else
+    ep_load8((const uint16_t*)p + idx, nv, v);
+}
+
+// The whole-vector stores of large outputs are non-temporal (NT): the kernel does not read
+// them again.
+template <bool NT>
+__device__ __forceinline__ void ep_store8(uint16_t* p, int nv, const float (&v)[8]) {
+  if (nv == 8) {
+    ep_u16x8 w;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = ep_f32bf(v[i]);
+    if constexpr (NT)
+      __builtin_nontemporal_store(w, (ep_u16x8_u*)p);
+    else
+      *(ep_u16x8_u*)p = w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < nv) p[i] = ep_f32bf(v[i]);
+  }
+}
+template <bool NT>
+__device__ __forceinline__ void ep_store8(float* p, int nv, const float (&v)[8]) {
+  if (nv == 8) {
+    const ep_f32x4 a = {v[0], v[1], v[2], v[3]}, b = {v[4], v[5], v[6], v[7]};
+    if constexpr (NT) {
+      __builtin_nontemporal_store(a, (ep_f32x4_u*)p);
+      __builtin_nontemporal_store(b, (ep_f32x4_u*)(p + 4));
+    } else {
+      *(ep_f32x4_u*)p = a;
+      *(ep_f32x4_u*)(p + 4) = b;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < nv) p[i] = v[i];
+  }
+}
+template <bool NT>
+__device__ __forceinline__ void ep_store8(void* p, int64_t idx, int f32, int nv, const float (&v)[8]) {
+  if (f32)
+    ep_store8<NT>((float*)p + idx, nv, v);
+  else
+    ep_store8<NT>((uint16_t*)p + idx, nv, v);
+}
+
+// ---- activations.  logistic(v) = 1 / (1 + 2^(-v log2 e)) with the hardware's exponential
+// and reciprocal (1 ulp each): 2^inf = inf and 1 / inf = 0, so both ends saturate.
+__device__ __forceinline__ float ep_logistic2(float neg_v_log2e) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(neg_v_log2e));
+}
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kGeluC0 = 0.7978845608028654f;  // sqrt(2 / pi)
+constexpr float kGeluC1 = 0.044715f;
+
+// 1 - Phi(|z|) = erfc(|z| / sqrt 2) / 2 by the rational form of Abramowitz and Stegun 7.1.26
+// (|error of erf| <= 1.5e-7, the size of an fp32 unit), and e = exp(-z^2 / 2).
+__device__ __forceinline__ float ep_gauss_tail(float z, float& e) {
+  const float x = __builtin_fabsf(z);
+  e = __builtin_amdgcn_exp2f(-0.5f * kLog2e * z * z);
+  const float t = __builtin_amdgcn_rcpf(1.0f + 0.3275911f * 0.70710678118f * x);
+  const float p =
+      t * (0.254829592f + t * (-0.284496736f + t * (1.421413741f + t * (-1.453152027f + t * 1.061405429f))));
+  return 0.5f * p * e;
+}
+
+template <int ACT>
+__device__ __forceinline__ float ep_act(float z) {
+  if constexpr (ACT == ACT_RELU) {
+    return z < 0.f ? 0.f : z;  // NaN stays NaN
+  } else if constexpr (ACT == ACT_GELU) {
+    float e;
+    const float q = ep_gauss_tail(z, e);
+    return z * (z < 0.f ? q : 1.0f - q);
+  } else if constexpr (ACT == ACT_GELU_TANH) {
+    // (1 + tanh u) / 2 = logistic(2u)
+    return z * ep_logistic2(z * (-2.f * kGeluC0 * kLog2e - 2.f * kGeluC0 * kGeluC1 * kLog2e * z * z));
+  } else if constexpr (ACT == ACT_SILU) {
+    return z * ep_logistic2(-kLog2e * z);
+  } else {
+    return z;
+  }
+}
+
+template <int ACT>
+__device__ __forceinline__ float ep_slope(float z) {
+  if constexpr (ACT == ACT_RELU) {
+    return z > 0.f ? 1.f : (z == z ? 0.f : z);
+  } else if constexpr (ACT == ACT_GELU) {
+    float e;
+    const float q = ep_gauss_tail(z, e);
+    return (z < 0.f ? q : 1.0f - q) + z * (0.3989422804014327f * e);
+  } else if constexpr (ACT == ACT_GELU_TANH) {
+    const float s = ep_logistic2(z * (-2.f * kGeluC0 * kLog2e - 2.f * kGeluC0 * kGeluC1 * kLog2e * z * z));
+    // past |z| = 64 the second term is 0 (s is 0 or 1); clamped so that z^2 stays finite
+    const float c = __builtin_fminf(__builtin_fmaxf(z, -64.f), 64.f);
+    return s + c * (s * (1.f - s)) * (2.f * kGeluC0 + 6.f * kGeluC0 * kGeluC1 * c * c);
+  } else if constexpr (ACT == ACT_SILU) {
+    const float s = ep_logistic2(-kLog2e * z);
+    return s * (1.f + z * (1.f - s));
+  } else {
+    return 1.f;
+  }
+}
+
+// f(integral_constant<int, act>) for the run-time act (uniform over the launch)
+template <class F>
+__device__ __forceinline__ void ep_with_act(int act, F&& f) {
+  switch (act) {
+    case ACT_RELU: f(std::integral_constant<int, ACT_RELU>{}); break;
+    case ACT_GELU: f(std::integral_constant<int, ACT_GELU>{}); break;
+    case ACT_GELU_TANH: f(std::integral_constant<int, ACT_GELU_TANH>{}); break;
+    case ACT_SILU: f(std::integral_constant<int, ACT_SILU>{}); break;
+    default: break;
+  }
+}
+
+// Eight values of a row to E4M3 codes: the four neighbouring lanes that hold one block of
+// 32 columns (columns n & ~31 .. + 31) run this together, each with its eight (the invalid
+// ones zero).  Stores the first nv codes at q and, from the block's first lane when it has
+// any column, the scale byte at s.
+__device__ __forceinline__ void ep_store_mx(const float (&v)[8], int nv, bool first, uint8_t* q, uint8_t* s) {
+  float amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) amax = __builtin_fmaxf(amax, __builtin_fabsf(v[i]));  // NaN does not set it
+  amax = __builtin_fmaxf(amax, __shfl_xor(amax, 1));
+  amax = __builtin_fmaxf(amax, __shfl_xor(amax, 2));
+  const int e = mx_scale(amax);
+  const float inv = mx_inv(e);
+  const uint32_t lo = e4m3x4_from_f32(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
+  const uint32_t hi = e4m3x4_from_f32(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv);
+  if (first && nv > 0) *s = (uint8_t)e;
+  if (nv == 8) {
+    *(ep_u32x2_u*)q = (ep_u32x2){lo, hi};
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < nv) q[i] = (uint8_t)((i < 4 ? lo : hi) >> (8 * (i & 3)));
+  }
+}
+
+// Eight values from their codes (the first nv valid) and their block's scale byte.
+__device__ __forceinline__ void ep_load_mx(const uint8_t* q, int nv, uint32_t scale, float (&v)[8]) {
+  uint32_t lo = 0, hi = 0;
+  if (nv == 8) {
+    const ep_u32x2 w = *(const ep_u32x2_u*)q;
+    lo = w[0];
+    hi = w[1];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < nv) (i < 4 ? lo : hi) |= (uint32_t)q[i] << (8 * (i & 3));
+  }
+  const float f = scale == 255u ? __builtin_nanf("") : __builtin_bit_cast(float, scale == 0u ? 0x00400000u : scale << 23);
+  v[0] = __builtin_amdgcn_cvt_f32_fp8((int)lo, 0) * f;
+  v[1] = __builtin_amdgcn_cvt_f32_fp8((int)lo, 1) * f;
+  v[2] = __builtin_amdgcn_cvt_f32_fp8((int)lo, 2) * f;
+  v[3] = __builtin_amdgcn_cvt_f32_fp8((int)lo, 3) * f;
+  v[4] = __builtin_amdgcn_cvt_f32_fp8((int)hi, 0) * f;
+  v[5] = __builtin_amdgcn_cvt_f32_fp8((int)hi, 1) * f;
+  v[6] = __builtin_amdgcn_cvt_f32_fp8((int)hi, 2) * f;
+  v[7] = __builtin_amdgcn_cvt_f32_fp8((int)hi, 3) * f;
+}
+
+// The epilogue of columns [n, n + 8) of row m (n a multiple of 8), w = alpha * product.  All
+// four lanes of a block of 32 columns call it together; one without a row or column to do
+// passes live = false.  grad: the unrounded results are added to cs[0 .. 7].
+template <bool NT>
+__device__ __forceinline__ void ep_apply8(const GemmEpArgs& a, float (&w)[8], int64_t m, int n, bool live,
+                                          float (&cs)[8]) {
+  const EpArgs& e = a.ep;
+  const int left = a.N - n;
+  const int nv = live ? (left < 8 ? (left > 0 ? left : 0) : 8) : 0;
+  if (e.grad) {
+    if (nv == 0) return;
+    float z[8];
+    if (e.z_kind == Z_MX)
+      ep_load_mx((const uint8_t*)e.Z + m * e.ldz + n, nv, e.S[m * e.lds + (n >> 5)], z);
+    else
+      ep_load8((const uint16_t*)e.Z + m * e.ldz + n, nv, z);
+    ep_with_act(e.act, [&](auto ac) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] *= ep_slope<decltype(ac)::value>(z[i]);
+    });
+#pragma unroll
+    for (int i = 0; i < 8; ++i) cs[i] += i < nv ? w[i] : 0.f;
+  } else {
+    if (e.bias) {
+      float b[8];
+      ep_load8(e.bias, n, e.bias_f32, nv, b);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] += b[i];
+    }
+    if (e.z_kind == Z_MX) {
+      float z[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) z[i] = i < nv ? w[i] : 0.f;
+      ep_store_mx(z, nv, (n & 31) == 0, (uint8_t*)e.Z + m * e.ldz + n, e.S + m * e.lds + (n >> 5));
+    }
+    if (nv == 0) return;
+    if (e.z_kind == Z_BF16) ep_store8<NT>((uint16_t*)e.Z + m * e.ldz + n, nv, w);
+    ep_with_act(e.act, [&](auto ac) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = ep_act<decltype(ac)::value>(w[i]);
+    });
+    if (e.R) {
+      float r[8];
+      ep_load8(e.R, m * e.ldr + n, a.c_kind == C_F32, nv, r);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] += e.beta * r[i];
+    }
+  }
+  ep_store8<NT>(a.C, m * a.ldc + n, a.c_kind == C_F32, nv, w);
+}
+
+}  // namespace
+}  // namespace dbgemm

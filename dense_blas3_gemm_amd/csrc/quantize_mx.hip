@@ -14,19 +14,6 @@ namespace {
 
 __device__ inline float bf16f(uint16_t b) { return __builtin_bit_cast(float, (uint32_t)b << 16); }
 
-// UE8M0 scale byte of a group with largest magnitude amax (0 for an all-zero group).
-__device__ inline int mx_scale(float amax) {
-  if (!(amax > 0.0f)) return 0;
-  int ex;  // floor(log2(amax)); amax is a bf16 value, normal or subnormal in fp32
-  const uint32_t ab = __builtin_bit_cast(uint32_t, amax);
-  if ((ab >> 23) != 0u)
-    ex = (int)(ab >> 23) - 127;
-  else
-    ex = -126 - (__builtin_clz(ab) - 8 - 1) - 1;  // subnormal: 2^-149 * mantissa
-  const int e = ex - 8 + 127;
-  return e < 0 ? 0 : (e > 254 ? 254 : e);
-}
-
 // Four lanes per 32-element group, 8 elements (16 bytes of bf16) each: a wave reads 1 KiB of
 // a row and writes 512 bytes of codes, both contiguous.  The group's amax is reduced over its
 // four neighbouring lanes, and its first lane writes the scale byte.
@@ -66,8 +53,7 @@ __global__ __launch_bounds__(256) void quantize_mx_kernel(int64_t rows, int64_t 
     amax = __builtin_fmaxf(amax, __shfl_xor(amax, 2));
     const int e = mx_scale(amax);
     if (k % 4 == 0) scales[r * ld_scales + b] = (uint8_t)e;
-    // x / 2^(e-127) = x * 2^(127-e): exact (the results stay below 512 in magnitude)
-    const float inv = e == 254 ? 0x1p-127f : __builtin_bit_cast(float, (uint32_t)(254 - e) << 23);
+    const float inv = mx_inv(e);
     uint8_t* d = dst + r * ld_dst + c0;
     if (n == 8 && ((uintptr_t)d & 7u) == 0) {
       // the conversion instruction after saturating to +-448: the same codes as e4m3_from_f32

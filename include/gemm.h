@@ -358,6 +358,106 @@ gemm_status_t gemm_trsm(gemm_handle_t h, int side, int uplo, int transA, int dia
                         int64_t N, float alpha, const void* A, int64_t lda, void* B, int64_t ldb,
                         int dtype);
 
+/* ---------------------------------------------------------------------------------
+ * The operators of a transformer's MLP block, around its products: the product with a
+ * bias, an activation and a residual in its epilogue, the product that runs back through
+ * the activation, the activation's argument kept in 8 bits for the backward pass, and
+ * layer norm.  Row-major matrices with row strides ("ld", in elements), device pointers
+ * owned by the caller, everything enqueued on the handle's stream; nothing is allocated.
+ * Sums, statistics and everything up to the last rounding are fp32.  Column sums (bias and
+ * norm-weight gradients) are added in a fixed order: the same bits every run.
+ * The calls use the handle's workspace (partial sums, split products), so like split-K
+ * GEMMs, calls of one handle must not overlap on the device; NOT_SUPPORTED where a call
+ * needs a workspace that the handle could not allocate or that is too small for it.
+ * Unless said otherwise outputs must not overlap inputs.  Any alignment and any size is
+ * taken; 16-byte aligned pointers and strides are fastest.  INVALID_VALUE for a bad size,
+ * stride, type or flag or a missing pointer; on an error nothing is written.
+ *
+ * Activations, z the argument, s(v) = 1 / (1 + exp(-v)), Phi the normal distribution:
+ *   NONE z; RELU max(z, 0) (its slope is 0 at z = 0); GELU z Phi(z); GELU_TANH
+ *   z (1 + tanh(u)) / 2 with u = sqrt(2/pi) (z + 0.044715 z^3); SILU z s(z).
+ * --------------------------------------------------------------------------------- */
+typedef enum {
+  GEMM_ACT_NONE = 0,
+  GEMM_ACT_RELU = 1,
+  GEMM_ACT_GELU = 2,
+  GEMM_ACT_GELU_TANH = 3,
+  GEMM_ACT_SILU = 4
+} gemm_act_t;
+/* how the activation's argument Z is kept: not at all, as bf16, or as block-scaled E4M3
+ * (gemm_quantize_mx's format and rule: E4M3 codes [rows][ld >= cols] and one UE8M0 byte per
+ * 32 columns [rows][ld >= ceil(cols/32)]) */
+typedef enum { GEMM_Z_NONE = 0, GEMM_Z_BF16 = 1, GEMM_Z_MX = 2 } gemm_z_t;
+typedef enum { GEMM_TYPE_BF16 = 0, GEMM_TYPE_F32 = 1 } gemm_type_t;
+
+/* The epilogue of gemm_run_act; zeroed memory is the empty one. */
+typedef struct {
+  int act;              /* gemm_act_t */
+  int bias_type;        /* gemm_type_t of bias */
+  const void* bias;     /* N values, or NULL */
+  const void* residual; /* R, M x N of C's type with row stride ld_residual, or NULL */
+  int64_t ld_residual;
+  float beta;           /* factor of R; with beta == 0 R is not read */
+  int z_kind;           /* gemm_z_t: what is written of Z */
+  void* z;              /* Z_BF16: bf16 M x N; Z_MX: the codes */
+  int64_t ld_z;
+  uint8_t* z_scales;    /* Z_MX */
+  int64_t ld_z_scales;
+} gemm_epilogue_t;
+
+/* Z <- alpha * op(A) * op(B) + bias (bias[n] to every row);  C <- act(Z) + beta * R.
+ * Operands as in gemm_run; dtype GEMM_BF16_F32, GEMM_BF16_BF16, GEMM_E4M3_BF16 or
+ * GEMM_E4M3_F32.  Z is written (ep->z_kind) from its fp32 value, for the backward pass.
+ * R may be C itself (same pointer and stride): C <- act(Z) + beta * C.  K == 0 or alpha ==
+ * 0: the product is 0 and the epilogue runs all the same.  gemm_set_policy does not apply. */
+gemm_status_t gemm_run_act(gemm_handle_t h, int transA, int transB, int64_t M, int64_t N, int64_t K, float alpha,
+                           const void* A, int64_t lda, const void* B, int64_t ldb, const gemm_epilogue_t* ep,
+                           void* C, int64_t ldc, int dtype);
+
+/* D <- (alpha * op(A) * op(B)) * act'(Z), element by element;  C <- D (bf16 or fp32, the
+ * dtypes of gemm_run_act);  dbias[n] <- sum over the rows of D (fp32, from D's unrounded
+ * values), or dbias NULL.  With A = dY and op(B) = W^T of the product behind the activation,
+ * C is the gradient of Z and dbias that of the bias added into Z.  Z (M x N) as
+ * gemm_run_act or gemm_act_mx left it: z_kind GEMM_Z_BF16 or GEMM_Z_MX (z_scales unused for
+ * bf16).  M == 0: dbias is set to zeros. */
+gemm_status_t gemm_run_dact(gemm_handle_t h, int transA, int transB, int64_t M, int64_t N, int64_t K, float alpha,
+                            const void* A, int64_t lda, const void* B, int64_t ldb, int act, int z_kind,
+                            const void* z, int64_t ld_z, const uint8_t* z_scales, int64_t ld_z_scales, float* dbias,
+                            void* C, int64_t ldc, int dtype);
+
+/* The activation with its 8-bit checkpoint: out <- act(z) (bf16, from the bf16 z itself)
+ * and z's codes and scales, in one pass over z. */
+gemm_status_t gemm_act_mx(gemm_handle_t h, int64_t rows, int64_t cols, int act, const void* z, int64_t ld_z, void* out,
+                          int64_t ld_out, void* codes, int64_t ld_codes, uint8_t* scales, int64_t ld_scales);
+
+/* The backward pass from the checkpoint, z^ the codes' values:  dz <- dout * act'(z^) (bf16),
+ * dbias[n] <- sum over the rows of that (fp32, unrounded values);  out <- act(z^) (bf16), the
+ * activation again, for the gradient of the weight behind it.  Each of dz, dbias and out may
+ * be NULL, not all; dout (bf16) is given exactly when dz or dbias is.  dz may be dout (same
+ * stride).  rows == 0: dbias is set to zeros. */
+gemm_status_t gemm_act_grad_mx(gemm_handle_t h, int64_t rows, int64_t cols, int act, const void* codes,
+                               int64_t ld_codes, const uint8_t* scales, int64_t ld_scales, const void* dout,
+                               int64_t ld_dout, void* dz, int64_t ld_dz, float* dbias, void* out, int64_t ld_out);
+
+/* Layer norm of each row:  mu = mean(x), r = 1 / sqrt(mean((x - mu)^2) + eps),
+ * y <- (x - mu) * r * gamma + beta.  x and y bf16 or fp32 each; gamma and beta (cols values
+ * of weight_type) may be NULL (1 and 0).  mean and rstd receive mu and r (one fp32 per row)
+ * for the gradient, or are NULL.  eps finite and >= 0.  y may be x (same type and stride). */
+gemm_status_t gemm_layernorm(gemm_handle_t h, int64_t rows, int64_t cols, const void* x, int64_t ld_x, int x_type,
+                             const void* gamma, const void* beta, int weight_type, float eps, void* y, int64_t ld_y,
+                             int y_type, float* mean, float* rstd);
+
+/* Its gradient, with n = (x - mean) * rstd and g = dy * gamma:
+ *   dx <- rstd * (g - mean(g) - n * mean(g * n)) + residual,
+ *   dgamma <- sum over the rows of dy * n,  dbeta <- sum over the rows of dy  (fp32).
+ * dy has y's type, dx and residual x's.  residual (the gradient that reaches x past the norm)
+ * may be NULL and may be dx itself (same stride); gamma, dgamma and dbeta may be NULL.
+ * rows == 0: dgamma and dbeta are set to zeros. */
+gemm_status_t gemm_layernorm_grad(gemm_handle_t h, int64_t rows, int64_t cols, const void* dy, int64_t ld_dy,
+                                  int y_type, const void* x, int64_t ld_x, int x_type, const float* mean,
+                                  const float* rstd, const void* gamma, int weight_type, const void* residual,
+                                  int64_t ld_residual, void* dx, int64_t ld_dx, float* dgamma, float* dbeta);
+
 #ifdef __cplusplus
 }
 #endif

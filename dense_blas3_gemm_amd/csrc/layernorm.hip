@@ -24,6 +24,310 @@ __device__ __forceinline__ float wave_sum(float v) {
   for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
   return v;
 }
+
+// Eight elements of a row as they come from memory; the loads of the next rows are in flight
+// in this form while a row is worked on.
+template <class T>
+struct Raw8;
+template <>
+struct Raw8<uint16_t> {
+  ep_u16x8 w;
+  __device__ __forceinline__ void load(const uint16_t* p) { w = *(const ep_u16x8_u*)p; }
+  __device__ __forceinline__ void set(int i, uint16_t v) { w[i] = v; }
+  __device__ __forceinline__ float get(int i) const { return ep_bf16f(w[i]); }
+};
+template <>
+struct Raw8<float> {
+  ep_f32x4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = *(const ep_f32x4_u*)p;
+    b = *(const ep_f32x4_u*)(p + 4);
+  }
+  __device__ __forceinline__ void set(int i, float v) { (i < 4 ? a : b)[i & 3] = v; }
+  __device__ __forceinline__ float get(int i) const { return i < 4 ? a[i & 3] : b[i & 3]; }
+};
+// the first nv (<= 8) elements at p, zeros behind them
+template <class T>
+__device__ __forceinline__ void raw_load(Raw8<T>& r, const T* p, int nv) {
+  if (nv >= 8) {
+    r.load(p);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r.set(i, i < nv ? p[i] : T(0));
+  }
+}
+
+// ---- the row kernels.  A team of blockDim.x threads (whole waves) holds a row in registers:
+// thread t its columns 8 (t + c blockDim.x) .. + 7 for c < CPT.  blockDim.y teams make up a
+// workgroup, and a workgroup walks the rows with R rows per team at a time: one exchange over
+// the waves of a team serves R rows, the weights stay in registers, and the next R rows'
+// loads are issued before the present rows' sums are waited for.  Wide rows (CPT = 4) have no
+// registers for either: the weights are read where they are used and the rows one by one.
+struct Team {
+  int t, T, waves, wave;  // thread and wave within the team
+  int first_wave;         // the team's first wave within the workgroup
+  __device__ Team()
+      : t(threadIdx.x), T(blockDim.x), waves(blockDim.x >> 6), wave(threadIdx.x >> 6),
+        first_wave(threadIdx.y * (blockDim.x >> 6)) {}
+};
+
+// Sums over the team of V values per thread, the same in every thread.  s: 2 x 16 x V floats,
+// its two halves used in turn: the barrier of the use between two of one half keeps them
+// apart.  Every team of the workgroup calls it together.
+template <int V>
+__device__ __forceinline__ void team_sum(const Team& m, float (&v)[V], float* s, int& half) {
+#pragma unroll
+  for (int i = 0; i < V; ++i) v[i] = wave_sum(v[i]);
+  if (m.waves == 1) return;  // (uniform over the workgroup)
+  float* h = s + half * 16 * V;
+  half ^= 1;
+  if ((m.t & 63) == 0)
+#pragma unroll
+    for (int i = 0; i < V; ++i) h[(m.first_wave + m.wave) * V + i] = v[i];
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < V; ++i) v[i] = 0.f;
+  for (int w = 0; w < m.waves; ++w)
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] += h[(m.first_wave + w) * V + i];
+}
+
+// Forward: reads x once, writes y once.  Bound by those bytes.
+template <class X, class Y, int CPT, int R, int MAXT>
+__global__ __launch_bounds__(MAXT) void layernorm_kernel(NormArgs a) {
+  constexpr bool kWide = CPT >= 4;
+  __shared__ float s[2 * 16 * R];
+  const Team m;
+  int half = 0;
+  const X* x = (const X*)a.x;
+  Y* y = (Y*)a.y;
+  int col[CPT], nv[CPT];
+  float g[kWide ? 1 : CPT][8], b[kWide ? 1 : CPT][8];
+  auto weights = [&](int c, float (&gc)[8], float (&bc)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      gc[i] = 1.f;
+      bc[i] = 0.f;
+    }
+    if (a.gamma) ep_load8(a.gamma, col[c], a.w_kind, nv[c], gc);
+    if (a.beta) ep_load8(a.beta, col[c], a.w_kind, nv[c], bc);
+  };
+#pragma unroll
+  for (int c = 0; c < CPT; ++c) {
+    col[c] = 8 * (m.t + c * m.T);
+    nv[c] = min(max(a.cols - col[c], 0), 8);
+    if constexpr (!kWide) weights(c, g[c], b[c]);
+  }
+  const int64_t step = (int64_t)gridDim.x * blockDim.y * R;
+  const int64_t mine = ((int64_t)blockIdx.x * blockDim.y + threadIdx.y) * R;
+  Raw8<X> in[R][CPT];
+  auto load = [&](int64_t r) {
+#pragma unroll
+    for (int j = 0; j < R; ++j)
+#pragma unroll
+      for (int c = 0; c < CPT; ++c) raw_load(in[j][c], x + (r + j) * a.ldx + col[c], r + j < a.rows ? nv[c] : 0);
+  };
+  if constexpr (!kWide) load(mine);
+  const float n = (float)a.cols;
+  // (the workgroup's teams run the same number of rounds: they share the barriers)
+  for (int64_t r0 = (int64_t)blockIdx.x * blockDim.y * R; r0 < a.rows; r0 += step) {
+    const int64_t r = r0 + (mine - (int64_t)blockIdx.x * blockDim.y * R);
+    float v[R][CPT][8], mu[R], q[R];
+    if constexpr (kWide) load(r);
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      mu[j] = 0.f;
+#pragma unroll
+      for (int c = 0; c < CPT; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          v[j][c][i] = in[j][c].get(i);
+          mu[j] += v[j][c][i];
+        }
+    }
+    if constexpr (!kWide)
+      if (r0 + step < a.rows) load(r + step);
+    team_sum<R>(m, mu, s, half);
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      mu[j] /= n;  // (a constant row's mean is exact)
+      q[j] = 0.f;
+#pragma unroll
+      for (int c = 0; c < CPT; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          v[j][c][i] -= mu[j];
+          q[j] += i < nv[c] ? v[j][c][i] * v[j][c][i] : 0.f;
+        }
+    }
+    team_sum<R>(m, q, s, half);
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      if (r + j >= a.rows) continue;
+      const float rs = 1.0f / __builtin_sqrtf(q[j] / n + a.eps);
+#pragma unroll
+      for (int c = 0; c < CPT; ++c) {
+        if (nv[c] == 0) continue;
+        if constexpr (kWide) weights(c, g[0], b[0]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[j][c][i] = v[j][c][i] * rs * g[kWide ? 0 : c][i] + b[kWide ? 0 : c][i];
+        ep_store8<true>(y + (r + j) * a.ldy + col[c], nv[c], v[j][c]);
+      }
+      if (m.t == 0) {
+        if (a.mean) a.mean[r + j] = mu[j];
+        if (a.rstd) a.rstd[r + j] = rs;
+      }
+    }
+  }
+}
+
+// Gradient: reads x, dy (and dr) once, writes dx once; SUMS: a thread adds up dgamma and dbeta
+// of its columns over all rows of its team, the teams of a workgroup are added through LDS,
+// and each workgroup leaves one partial row.
+template <class X, class Y, int CPT, int R, int MAXT, bool SUMS>
+__global__ __launch_bounds__(MAXT) void layernorm_grad_kernel(NormArgs a) {
+  constexpr bool kWide = CPT >= 4;
+  static_assert(!(kWide && SUMS), "no registers for the sums of a wide row");
+  constexpr bool kAhead = !kWide && (CPT == 1 || MAXT <= 512);  // the next rows' loads ahead
+  __shared__ float s[2 * 16 * 2 * R];
+  const Team m;
+  int half = 0;
+  const X* x = (const X*)a.x;
+  const Y* dy = (const Y*)a.dy;
+  X* dx = (X*)a.y;
+  int col[CPT], nv[CPT];
+  float gam[kWide ? 1 : CPT][8], dg[SUMS ? CPT : 1][8] = {}, db[SUMS ? CPT : 1][8] = {};
+  auto weights = [&](int c, float (&gc)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) gc[i] = 1.f;
+    if (a.gamma) ep_load8(a.gamma, col[c], a.w_kind, nv[c], gc);
+  };
+#pragma unroll
+  for (int c = 0; c < CPT; ++c) {
+    col[c] = 8 * (m.t + c * m.T);
+    nv[c] = min(max(a.cols - col[c], 0), 8);
+    if constexpr (!kWide) weights(c, gam[c]);
+  }
+  const int64_t step = (int64_t)gridDim.x * blockDim.y * R;
+  const int64_t mine = ((int64_t)blockIdx.x * blockDim.y + threadIdx.y) * R;
+  Raw8<X> xin[R][CPT];
+  Raw8<Y> gin[R][CPT];
+  float mu[R], rs[R];
+  auto load = [&](int64_t r) {
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      const bool live = r + j < a.rows;
+      mu[j] = live ? a.mean[r + j] : 0.f;
+      rs[j] = live ? a.rstd[r + j] : 0.f;
+#pragma unroll
+      for (int c = 0; c < CPT; ++c) {
+        raw_load(xin[j][c], x + (r + j) * a.ldx + col[c], live ? nv[c] : 0);
+        raw_load(gin[j][c], dy + (r + j) * a.lddy + col[c], live ? nv[c] : 0);
+      }
+    }
+  };
+  if constexpr (kAhead) load(mine);
+  const float n = (float)a.cols;
+  for (int64_t r0 = (int64_t)blockIdx.x * blockDim.y * R; r0 < a.rows; r0 += step) {
+    const int64_t r = r0 + (mine - (int64_t)blockIdx.x * blockDim.y * R);
+    // (a wide row's xh and g are formed twice instead of being held)
+    float xh[R][kWide ? 1 : CPT][8], g[R][kWide ? 1 : CPT][8], c12[2 * R], rr[R];
+    if constexpr (!kAhead) load(r);
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      float c1 = 0.f, c2 = 0.f;
+      rr[j] = rs[j];
+#pragma unroll
+      for (int c = 0; c < CPT; ++c) {
+        if constexpr (kWide) weights(c, gam[0]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          // (a column past the row has dy = 0 and adds nothing)
+          const float d = gin[j][c].get(i);
+          const float xn = (xin[j][c].get(i) - mu[j]) * rs[j], gn = d * gam[kWide ? 0 : c][i];
+          c1 += gn;
+          c2 += gn * xn;
+          if constexpr (!kWide) {
+            xh[j][c][i] = xn;
+            g[j][c][i] = gn;
+          }
+          if constexpr (SUMS) {
+            dg[c][i] += d * xn;
+            db[c][i] += d;
+          }
+        }
+      }
+      c12[2 * j] = c1;
+      c12[2 * j + 1] = c2;
+    }
+    Raw8<X> res[R][kWide ? 1 : CPT];
+    if constexpr (!kWide) {
+      if (a.dr) {
+#pragma unroll
+        for (int j = 0; j < R; ++j)
+#pragma unroll
+          for (int c = 0; c < CPT; ++c)
+            raw_load(res[j][c], (const X*)a.dr + (r + j) * a.lddr + col[c], r + j < a.rows ? nv[c] : 0);
+      }
+    }
+    if constexpr (kAhead)
+      if (r0 + step < a.rows) load(r + step);
+    team_sum<2 * R>(m, c12, s, half);
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      if (r + j >= a.rows) continue;
+      const float c1 = c12[2 * j] / n, c2 = c12[2 * j + 1] / n;
+#pragma unroll
+      for (int c = 0; c < CPT; ++c) {
+        if (nv[c] == 0) continue;
+        if constexpr (kWide) {
+          weights(c, gam[0]);
+          if (a.dr) raw_load(res[j][0], (const X*)a.dr + (r + j) * a.lddr + col[c], nv[c]);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            xh[j][0][i] = (xin[j][c].get(i) - mu[j]) * rs[j];
+            g[j][0][i] = gin[j][c].get(i) * gam[0][i];
+          }
+        }
+        const int k = kWide ? 0 : c;
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          v[i] = rr[j] * (g[j][k][i] - c1 - xh[j][k][i] * c2);
+          if (a.dr) v[i] += res[j][k].get(i);
+        }
+        ep_store8<true>(dx + (r + j) * a.ldy + col[c], nv[c], v);
+      }
+    }
+  }
+  if constexpr (SUMS) {
+    // the teams' sums, one set of eight columns at a time: team y > 0 leaves its own in LDS
+    // and team 0 adds them in order
+    __shared__ float t8[8 * 1024];
+    float* out = a.part + (int64_t)blockIdx.x * 2 * a.cols;
+    auto put = [&](float (&v)[8], int c, int set) {
+      if (blockDim.y > 1) {
+        __syncthreads();
+        if (threadIdx.y > 0)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) t8[i * 1024 + threadIdx.y * m.T + m.t] = v[i];
+        __syncthreads();
+        if (threadIdx.y == 0)
+          for (unsigned k = 1; k < blockDim.y; ++k)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] += t8[i * 1024 + k * m.T + m.t];
+      }
+      if (threadIdx.y == 0 && nv[c] > 0) ep_store8<false>(out + (int64_t)set * a.cols + col[c], nv[c], v);
+    };
+#pragma unroll
+    for (int c = 0; c < CPT; ++c) {
+      put(dg[c], c, 0);
+      put(db[c], c, 1);
+    }
+  }
+}
+
+// ---- rows too wide for the registers of a workgroup
 // Sums of two values over a workgroup of 256 threads, the same in every thread.
 __device__ __forceinline__ void group_sum(float& u, float& v, float (*s)[2]) {
   u = wave_sum(u);
@@ -91,40 +395,138 @@ __global__ __launch_bounds__(256) void layernorm_dx_kernel(NormArgs a) {
   }
 }
 
-// Partial sums of dgamma and dbeta: a thread to a column, workgroup row y takes rows y, y +
-// gridDim.y, ...
+// Partial sums of dgamma and dbeta: a thread to eight columns, workgroup row y takes rows y,
+// y + gridDim.y, ...
+template <class X, class Y>
 __global__ __launch_bounds__(256) void layernorm_dw_kernel(NormArgs a) {
-  const int i = blockIdx.x * 256 + threadIdx.x;
-  if (i >= a.cols) return;
-  float dg = 0.f, db = 0.f;
+  const int col = 8 * (blockIdx.x * 256 + threadIdx.x);
+  if (col >= a.cols) return;
+  const int nv = min(a.cols - col, 8);
+  float dg[8] = {}, db[8] = {};
+#pragma unroll 2
   for (int64_t r = blockIdx.y; r < a.rows; r += gridDim.y) {
-    const float dy = ln_load(a.dy, r * a.lddy + i, a.y_kind);
-    dg += dy * ((ln_load(a.x, r * a.ldx + i, a.x_kind) - a.mean[r]) * a.rstd[r]);
-    db += dy;
+    Raw8<X> x;
+    Raw8<Y> d;
+    raw_load(x, (const X*)a.x + r * a.ldx + col, nv);
+    raw_load(d, (const Y*)a.dy + r * a.lddy + col, nv);
+    const float mu = a.mean[r], rs = a.rstd[r];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      dg[i] += d.get(i) * ((x.get(i) - mu) * rs);
+      db[i] += d.get(i);
+    }
   }
-  a.part[((int64_t)blockIdx.y * 2) * a.cols + i] = dg;
-  a.part[((int64_t)blockIdx.y * 2 + 1) * a.cols + i] = db;
+  float* out = a.part + (int64_t)blockIdx.y * 2 * a.cols + col;
+  ep_store8<false>(out, nv, dg);
+  ep_store8<false>(out + a.cols, nv, db);
 }
 
-}  // namespace
+// Threads of a team for rows of `cols` columns at `cpt` chunks of 8 to a thread: whole waves.
+unsigned team_threads(int64_t cols, int cpt) { return (unsigned)((cols + 512 * cpt - 1) / (512 * cpt)) * 64; }
 
-hipError_t launch_layernorm(const NormArgs& a, hipStream_t s) {
+template <class X, class Y, int CPT, int R, int MAXT>
+hipError_t fwd(const NormArgs& a, hipStream_t s) {
+  constexpr unsigned wg = 256, per_cu = 1024;
+  const unsigned T = team_threads(a.cols, CPT);
+  const unsigned teams = T < wg ? wg / T : 1;
+  const int64_t need = (a.rows + (int64_t)teams * R - 1) / ((int64_t)teams * R);
+  const int64_t most = 256 * (per_cu / (T * teams) ? per_cu / (T * teams) : 1);
+  hipLaunchKernelGGL((layernorm_kernel<X, Y, CPT, R, MAXT>), dim3((unsigned)(need < most ? need : most)),
+                     dim3(T, teams), 0, s, a);
+  return hipGetLastError();
+}
+
+template <class X, class Y, int CPT, int R, int MAXT, bool SUMS>
+hipError_t grad(const NormArgs& a, int max_parts, int* parts, hipStream_t s) {
+  constexpr unsigned wg = 512;
+  const unsigned T = team_threads(a.cols, CPT);
+  unsigned teams = T < wg ? wg / T : 1;
+  while (teams > 1 && (int64_t)teams * R * 256 > a.rows) --teams;  // few rows: spread them over the CUs
+  const int64_t need = (a.rows + (int64_t)teams * R - 1) / ((int64_t)teams * R);
+  // With the weights' sums one workgroup to a CU: a partial row more per CU costs more (its
+  // write and its read) than a second workgroup's overlap gains, 128.4 against 136.6 us at
+  // 16384 x 5120.  Narrow rows (one chunk a thread, no spills at 128 registers) take two.
+  int64_t most = 256 * (SUMS && CPT > 1 ? 1 : 1024 / (T * teams) ? 1024 / (T * teams) : 1);
+  if (SUMS && most > max_parts) most = max_parts;
+  const unsigned n = (unsigned)(need < most ? need : most);
+  *parts = (int)n;
+  hipLaunchKernelGGL((layernorm_grad_kernel<X, Y, CPT, R, MAXT, SUMS>), dim3(n), dim3(T, teams), 0, s, a);
+  return hipGetLastError();
+}
+
+// Chunks per thread, rows at a time, by width and rows (MI355X, bf16): at 16384 x 5120 two
+// chunks (teams of 320 threads, three workgroups to a CU) take 59.6 us and one chunk 91.8-95;
+// at 65536 x 768 two rows at a time 39.8, one 43.5.  A few rows finish sooner with more
+// threads to each (1 x 5120: 3.4 against 3.9).
+template <class X, class Y>
+hipError_t fwd_xy(const NormArgs& a, hipStream_t s) {
+  if (a.cols <= 8192) {
+    if (a.rows <= 256) return fwd<X, Y, 1, 1, 1024>(a, s);
+    return a.cols <= 1024 ? fwd<X, Y, 2, 2, 512>(a, s) : fwd<X, Y, 2, 1, 512>(a, s);
+  }
+  if (a.cols <= 16384) return fwd<X, Y, 2, 1, 1024>(a, s);
+  if (a.cols <= 32768) return fwd<X, Y, 4, 1, 1024>(a, s);
   const unsigned g = (unsigned)(a.rows < 65536 ? a.rows : 65536);
   hipLaunchKernelGGL(layernorm_rows_kernel, dim3(g), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
-hipError_t launch_layernorm_grad(const NormArgs& a, int max_parts, int* parts, hipStream_t s) {
-  const unsigned g = (unsigned)(a.rows < 65536 ? a.rows : 65536);
-  // dx may overwrite dr: the weights' sums read neither
-  hipLaunchKernelGGL(layernorm_dx_kernel, dim3(g), dim3(256), 0, s, a);
-  *parts = 0;
-  if (a.part) {
-    *parts = (int)(a.rows < max_parts ? a.rows : max_parts);
-    hipLaunchKernelGGL(layernorm_dw_kernel, dim3((unsigned)((a.cols + 255) / 256), (unsigned)*parts), dim3(256), 0, s,
-                       a);
+// The same for the gradient: at 16384 x 5120 two chunks and two rows at a time take 128.4 us
+// with the sum of the partials, one row 157, one chunk 137; at 65536 x 768 one chunk and two
+// rows 109, two chunks 125.
+template <class X, class Y, bool SUMS>
+hipError_t grad_fit(const NormArgs& a, int max_parts, int* parts, hipStream_t s) {
+  constexpr int kBytes = sizeof(X) + sizeof(Y);  // (R as far as the registers go)
+  if (a.cols <= 1024) return grad<X, Y, 1, (kBytes > 4 ? 1 : 2), 1024, SUMS>(a, max_parts, parts, s);
+  if (a.cols <= 8192) {
+    if (a.rows <= 256) return grad<X, Y, 1, 1, 1024, SUMS>(a, max_parts, parts, s);
+    return grad<X, Y, 2, (kBytes > 6 ? 1 : 2), 512, SUMS>(a, max_parts, parts, s);
   }
+  return grad<X, Y, 2, 1, 1024, SUMS>(a, max_parts, parts, s);  // up to 16384
+}
+
+template <class X, class Y>
+hipError_t grad_xy(const NormArgs& a, int max_parts, int* parts, hipStream_t s) {
+  if (a.cols <= 16384)
+    return a.part ? grad_fit<X, Y, true>(a, max_parts, parts, s) : grad_fit<X, Y, false>(a, 0, parts, s);
+  // wider: dx and the weights' sums apart (the sums' registers would not fit beside the row)
+  NormArgs d = a;
+  d.part = nullptr;
+  hipError_t e;
+  if (a.cols <= 32768) {
+    int none = 0;
+    e = grad<X, Y, 4, 1, 1024, false>(d, 0, &none, s);
+  } else {
+    const unsigned g = (unsigned)(a.rows < 65536 ? a.rows : 65536);
+    hipLaunchKernelGGL(layernorm_dx_kernel, dim3(g), dim3(256), 0, s, d);
+    e = hipGetLastError();
+  }
+  *parts = 0;
+  if (e != hipSuccess || !a.part) return e;
+  const int64_t gx = (a.cols + 2047) / 2048;
+  int64_t gy = 2048 / gx;
+  if (gy > max_parts) gy = max_parts;
+  if (gy > a.rows) gy = a.rows;
+  if (gy < 1) gy = 1;
+  *parts = (int)gy;
+  hipLaunchKernelGGL((layernorm_dw_kernel<X, Y>), dim3((unsigned)gx, (unsigned)gy), dim3(256), 0, s, a);
   return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_layernorm(const NormArgs& a, hipStream_t s) {
+  if (a.x_kind == T_F32)
+    return a.y_kind == T_F32 ? fwd_xy<float, float>(a, s) : fwd_xy<float, uint16_t>(a, s);
+  return a.y_kind == T_F32 ? fwd_xy<uint16_t, float>(a, s) : fwd_xy<uint16_t, uint16_t>(a, s);
+}
+
+hipError_t launch_layernorm_grad(const NormArgs& a, int max_parts, int* parts, hipStream_t s) {
+  if (a.x_kind == T_F32)
+    return a.y_kind == T_F32 ? grad_xy<float, float>(a, max_parts, parts, s)
+                             : grad_xy<float, uint16_t>(a, max_parts, parts, s);
+  return a.y_kind == T_F32 ? grad_xy<uint16_t, float>(a, max_parts, parts, s)
+                           : grad_xy<uint16_t, uint16_t>(a, max_parts, parts, s);
 }
 
 }  // namespace dbgemm

@@ -46,13 +46,18 @@ __global__ __launch_bounds__(kThreads) void ep_rows_kernel(GemmEpArgs a, int64_t
   const int64_t k = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   if (k >= ((int64_t)a.N + 31) / 32 * 4) return;  // four lanes leave together
   const int n = (int)(k * 8);
-  float cs[8] = {};
-  for (int64_t m = (int64_t)blockIdx.y * blockDim.y + threadIdx.y; m < a.M; m += (int64_t)gridDim.y * blockDim.y) {
-    float w[8];
-    const int nv = a.N - n < 8 ? (a.N > n ? a.N - n : 0) : 8;
-    ep_load8(a.ws + m * ldw + n, nv, w);
-    ep_apply8<false>(a, w, m, n, true, cs);
-  }
+  const int nv = a.N - n < 8 ? (a.N > n ? a.N - n : 0) : 8;
+  float cs[8] = {}, b[8];
+  ep_bias8(a, n, nv, b);
+  ep_dispatch(a.ep, [&](auto gc, auto ac) {
+    for (int64_t m = (int64_t)blockIdx.y * blockDim.y + threadIdx.y; m < a.M; m += (int64_t)gridDim.y * blockDim.y) {
+      float w[8];
+      EpRaw r;
+      ep_fetch8<decltype(gc)::value>(a, m, n, nv, r);
+      ep_load8(a.ws + m * ldw + n, nv, w);
+      ep_finish8<false, decltype(gc)::value, decltype(ac)::value>(a, w, r, b, m, n, nv, cs);
+    }
+  });
   put_partial(a.ep.colsum, a.N, n, cs);
 }
 

@@ -565,6 +565,11 @@ hipError_t gemm_enqueue(const HandleView& hv, int transA, int transB, int64_t M,
   return unsupported ? hipErrorInvalidConfiguration : e;
 }
 
+Problem gemm_problem(int transA, int transB, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* B,
+                     int64_t ldb, const void* C, int64_t ldc, int dtype) {
+  return make_problem(transA, transB, M, N, K, A, lda, B, ldb, C, ldc, dtype);
+}
+
 bool gemm_fast_ok(int transA, int transB, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* B,
                   int64_t ldb, const void* C, int64_t ldc, int dtype) {
   return make_problem(transA, transB, M, N, K, A, lda, B, ldb, C, ldc, dtype).fast_ok;

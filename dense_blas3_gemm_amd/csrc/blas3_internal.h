@@ -45,6 +45,9 @@ struct GemmExtras {
 hipError_t gemm_enqueue(const HandleView& hv, int transA, int transB, int64_t M, int64_t N, int64_t K, float alpha,
                         const void* A, int64_t lda, const void* B, int64_t ldb, float beta, void* C, int64_t ldc,
                         int dtype, const GemmExtras& x);
+// gemm_run's problem for these arguments (what the tile policy is chosen by).
+Problem gemm_problem(int transA, int transB, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* B,
+                     int64_t ldb, const void* C, int64_t ldc, int dtype);
 // Whether the MFMA kernels take these operands (alignment, strides, spans).
 bool gemm_fast_ok(int transA, int transB, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* B,
                   int64_t ldb, const void* C, int64_t ldc, int dtype);

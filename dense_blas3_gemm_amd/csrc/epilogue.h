@@ -167,7 +167,7 @@ __device__ __forceinline__ void ep_with_act(int act, F&& f) {
     case ACT_GELU: f(std::integral_constant<int, ACT_GELU>{}); break;
     case ACT_GELU_TANH: f(std::integral_constant<int, ACT_GELU_TANH>{}); break;
     case ACT_SILU: f(std::integral_constant<int, ACT_SILU>{}); break;
-    default: break;
+    default: f(std::integral_constant<int, ACT_NONE>{}); break;
   }
 }
 
@@ -195,18 +195,8 @@ __device__ __forceinline__ void ep_store_mx(const float (&v)[8], int nv, bool fi
   }
 }
 
-// Eight values from their codes (the first nv valid) and their block's scale byte.
-__device__ __forceinline__ void ep_load_mx(const uint8_t* q, int nv, uint32_t scale, float (&v)[8]) {
-  uint32_t lo = 0, hi = 0;
-  if (nv == 8) {
-    const ep_u32x2 w = *(const ep_u32x2_u*)q;
-    lo = w[0];
-    hi = w[1];
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < nv) (i < 4 ? lo : hi) |= (uint32_t)q[i] << (8 * (i & 3));
-  }
+// Eight values from their codes (bytes of lo, then hi) and their block's scale byte.
+__device__ __forceinline__ void ep_codes8(uint32_t lo, uint32_t hi, uint32_t scale, float (&v)[8]) {
   const float f = scale == 255u ? __builtin_nanf("") : __builtin_bit_cast(float, scale == 0u ? 0x00400000u : scale << 23);
   v[0] = __builtin_amdgcn_cvt_f32_fp8((int)lo, 0) * f;
   v[1] = __builtin_amdgcn_cvt_f32_fp8((int)lo, 1) * f;
@@ -218,55 +208,142 @@ __device__ __forceinline__ void ep_load_mx(const uint8_t* q, int nv, uint32_t sc
   v[7] = __builtin_amdgcn_cvt_f32_fp8((int)hi, 3) * f;
 }
 
-// The epilogue of columns [n, n + 8) of row m (n a multiple of 8), w = alpha * product.  All
-// four lanes of a block of 32 columns call it together; one without a row or column to do
-// passes live = false.  grad: the unrounded results are added to cs[0 .. 7].
-template <bool NT>
-__device__ __forceinline__ void ep_apply8(const GemmEpArgs& a, float (&w)[8], int64_t m, int n, bool live,
-                                          float (&cs)[8]) {
-  const EpArgs& e = a.ep;
-  const int left = a.N - n;
-  const int nv = live ? (left < 8 ? (left > 0 ? left : 0) : 8) : 0;
-  if (e.grad) {
-    if (nv == 0) return;
-    float z[8];
-    if (e.z_kind == Z_MX)
-      ep_load_mx((const uint8_t*)e.Z + m * e.ldz + n, nv, e.S[m * e.lds + (n >> 5)], z);
-    else
-      ep_load8((const uint16_t*)e.Z + m * e.ldz + n, nv, z);
-    ep_with_act(e.act, [&](auto ac) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] *= ep_slope<decltype(ac)::value>(z[i]);
-    });
-#pragma unroll
-    for (int i = 0; i < 8; ++i) cs[i] += i < nv ? w[i] : 0.f;
+// the same from memory, the first nv codes valid
+__device__ __forceinline__ void ep_load_mx(const uint8_t* q, int nv, uint32_t scale, float (&v)[8]) {
+  uint32_t lo = 0, hi = 0;
+  if (nv == 8) {
+    const ep_u32x2 w = *(const ep_u32x2_u*)q;
+    lo = w[0];
+    hi = w[1];
   } else {
-    if (e.bias) {
-      float b[8];
-      ep_load8(e.bias, n, e.bias_f32, nv, b);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] += b[i];
+    for (int i = 0; i < 8; ++i)
+      if (i < nv) (i < 4 ? lo : hi) |= (uint32_t)q[i] << (8 * (i & 3));
+  }
+  ep_codes8(lo, hi, scale, v);
+}
+
+// The epilogue of columns [n, n + 8) of row m (n a multiple of 8) in two parts: ep_fetch8
+// issues the load of what the row brings (the residual, or Z for a gradient), ep_finish8 does
+// the rest, so that a caller can have the loads of several rows in flight.  nv: the valid
+// columns, 0 .. 8 (0: no row or column here).
+struct EpRaw {
+  uint32_t d[8];  // 8 bf16 in d[0..3], 8 fp32, or 8 codes in d[0..1] and their scale in d[2]
+};
+
+// d[0 .. W) <- W * 4 bytes at p, or (a part) the first nv elements of ES bytes, zeros behind
+template <int W, int ES>
+__device__ __forceinline__ void ep_raw(const void* p, int nv, EpRaw& r) {
+  typedef uint32_t vec __attribute__((ext_vector_type(W == 8 ? 4 : W)));
+  typedef vec vec_u __attribute__((aligned(ES)));
+  if (nv == 8) {
+    const vec v = *(const vec_u*)p;
+#pragma unroll
+    for (int i = 0; i < (W == 8 ? 4 : W); ++i) r.d[i] = v[i];
+    if constexpr (W == 8) {
+      const vec u = *(const vec_u*)((const char*)p + 16);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) r.d[4 + i] = u[i];
     }
-    if (e.z_kind == Z_MX) {
-      float z[8];
+  } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) z[i] = i < nv ? w[i] : 0.f;
-      ep_store_mx(z, nv, (n & 31) == 0, (uint8_t*)e.Z + m * e.ldz + n, e.S + m * e.lds + (n >> 5));
+    for (int i = 0; i < W; ++i) r.d[i] = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < nv) {
+        const uint32_t e = ES == 4 ? ((const uint32_t*)p)[i] : ES == 2 ? ((const uint16_t*)p)[i] : ((const uint8_t*)p)[i];
+        r.d[i * ES / 4] |= e << (8 * (i * ES % 4));
+      }
+  }
+}
+
+template <bool GRAD>
+__device__ __forceinline__ void ep_fetch8(const GemmEpArgs& a, int64_t m, int n, int nv, EpRaw& r) {
+  const EpArgs& e = a.ep;
+  if (nv == 0) return;
+  if constexpr (GRAD) {
+    if (e.z_kind == Z_MX) {
+      ep_raw<2, 1>((const uint8_t*)e.Z + m * e.ldz + n, nv, r);
+      r.d[2] = e.S[m * e.lds + (n >> 5)];
+    } else {
+      ep_raw<4, 2>((const uint16_t*)e.Z + m * e.ldz + n, nv, r);
+    }
+  } else if (e.R) {
+    if (a.c_kind == C_F32)
+      ep_raw<8, 4>((const float*)e.R + m * e.ldr + n, nv, r);
+    else
+      ep_raw<4, 2>((const uint16_t*)e.R + m * e.ldr + n, nv, r);
+  }
+}
+
+__device__ __forceinline__ void ep_raw_bf16(const EpRaw& r, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __builtin_bit_cast(float, r.d[i] << 16);
+    v[2 * i + 1] = __builtin_bit_cast(float, r.d[i] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ void ep_raw_f32(const EpRaw& r, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __builtin_bit_cast(float, r.d[i]);
+}
+
+// w = alpha * product, b = the bias of these columns (zeros without one).  The four lanes of a
+// block of 32 columns call it together.  A gradient's unrounded results are added to cs.
+template <bool NT, bool GRAD, int ACT>
+__device__ __forceinline__ void ep_finish8(const GemmEpArgs& a, float (&w)[8], const EpRaw& r, const float (&b)[8],
+                                           int64_t m, int n, int nv, float (&cs)[8]) {
+  const EpArgs& e = a.ep;
+  float v[8];
+  if constexpr (GRAD) {
+    if (nv == 0) return;
+    if (e.z_kind == Z_MX)
+      ep_codes8(r.d[0], r.d[1], r.d[2], v);
+    else
+      ep_raw_bf16(r, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      w[i] *= ep_slope<ACT>(v[i]);
+      cs[i] += i < nv ? w[i] : 0.f;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] += b[i];
+    if (e.z_kind == Z_MX) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = i < nv ? w[i] : 0.f;
+      ep_store_mx(v, nv, (n & 31) == 0, (uint8_t*)e.Z + m * e.ldz + n, e.S + m * e.lds + (n >> 5));
     }
     if (nv == 0) return;
     if (e.z_kind == Z_BF16) ep_store8<NT>((uint16_t*)e.Z + m * e.ldz + n, nv, w);
-    ep_with_act(e.act, [&](auto ac) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = ep_act<decltype(ac)::value>(w[i]);
-    });
+    for (int i = 0; i < 8; ++i) w[i] = ep_act<ACT>(w[i]);
     if (e.R) {
-      float r[8];
-      ep_load8(e.R, m * e.ldr + n, a.c_kind == C_F32, nv, r);
+      if (a.c_kind == C_F32)
+        ep_raw_f32(r, v);
+      else
+        ep_raw_bf16(r, v);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] += e.beta * r[i];
+      for (int i = 0; i < 8; ++i) w[i] += e.beta * v[i];
     }
   }
   ep_store8<NT>(a.C, m * a.ldc + n, a.c_kind == C_F32, nv, w);
+}
+
+// the bias of columns [n, n + 8)
+__device__ __forceinline__ void ep_bias8(const GemmEpArgs& a, int n, int nv, float (&b)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) b[i] = 0.f;
+  if (!a.ep.grad && a.ep.bias) ep_load8(a.ep.bias, n, a.ep.bias_f32, nv, b);
+}
+
+// f(bool_constant<grad>, integral_constant<int, act>) for the call's epilogue
+template <class F>
+__device__ __forceinline__ void ep_dispatch(const EpArgs& e, F&& f) {
+  if (e.grad)
+    ep_with_act(e.act, [&](auto ac) { f(std::true_type{}, ac); });
+  else
+    ep_with_act(e.act, [&](auto ac) { f(std::false_type{}, ac); });
 }
 
 }  // namespace

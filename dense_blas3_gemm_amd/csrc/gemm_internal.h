@@ -115,6 +115,14 @@ struct Policy {
   int a_kc_only;      // serves only A [M][K] (transA = 0)
 };
 
+// The table entries whose kernels are also built with an epilogue behind the product
+// (DBGEMM_EPILOGUE; see mlp_internal.h): the shape-driven choice's tiles, one per size.
+constexpr bool has_epilogue(int pipe, int in_mode, int BM, int BN, int BK, int MT, int k_contig_only, float eff) {
+  return eff > 0.f && MT == 16 && !k_contig_only &&
+         ((pipe == 2 && BM == 256 && ((in_mode == 0 && BK == 32) || (in_mode == 5 && BK == 128))) ||
+          (pipe == 1 && in_mode == 0 && BN <= 128) || (pipe == 0 && in_mode == 1 && BM <= 128));
+}
+
 // Launchers (one per kernel family).  They return hipSuccess or the launch error.
 hipError_t launch_simt(const GemmArgs& a, hipStream_t s);
 hipError_t launch_scale(const GemmArgs& a, hipStream_t s);  // C <- beta*C (K == 0 or alpha == 0)
@@ -182,6 +190,7 @@ struct Problem {
   bool blas3 = false;
   bool square_tiles = false;
   bool kband = false;  // per-tile K band (wave model: longest tiles first)
+  bool ep = false;     // an epilogue behind the product (has_epilogue)
 };
 // Stream-K plan of a ping-pong policy on a problem (the GemmArgs fields of that name);
 // tiles == 0: none (the grid is whole rounds, or the policy has no stream-K form).

@@ -21,9 +21,18 @@
 // The cross-wave wait is explicit (`s_waitcnt vmcnt` + `s_barrier`); within a wave the
 // compiler also orders each LDS read after the loads into the same ring slot.
 #include "mfma_common.h"
+#ifdef DBGEMM_EPILOGUE  // the kernels of products with an epilogue
+#include "epilogue_tile.h"
+#endif
 
 namespace dbgemm {
 namespace {
+
+#ifdef DBGEMM_EPILOGUE
+using KernelArgs = GemmEpArgs;
+#else
+using KernelArgs = GemmArgs;
+#endif
 
 // 64 lanes x 16 bytes from buffer `rsrc` at per-lane byte offset `voff` into LDS
 // bytes [lds_base, lds_base + 1024) (lane i -> lds_base + 16*i); an offset past the
@@ -91,7 +100,7 @@ struct Dma {
 };
 
 template <class C>
-__global__ __launch_bounds__(C::THREADS) void gemm_dma_kernel(GemmArgs a) {
+__global__ __launch_bounds__(C::THREADS) void gemm_dma_kernel(KernelArgs a) {
   using D = Dma<C>;
   // One LDS object per ring slot: the compiler tracks the loads into each slot on
   // its own, so its automatic waits before LDS reads wait for that slot only.
@@ -375,7 +384,12 @@ __global__ __launch_bounds__(C::THREADS) void gemm_dma_kernel(GemmArgs a) {
     store_partial<C>(a.ws + ((size_t)tile * a.splits + split) * (C::BM * C::BN), acc, t);
     return;
   }
+#ifdef DBGEMM_EPILOGUE
+  static_assert(C::WTM * C::BN * 4 <= C::STAGE_BYTES, "one row of waves' fp32 image fits a ring slot");
+  ep_tile<C, false>(a, acc, m0, n0, tm, wm, xb0, lane, t, (uint32_t)(uintptr_t)slot(std::integral_constant<int, 0>{}));
+#else
   store_tile<C>(a, acc, m0 + xa0, n0 + xb0, lane);
+#endif
 }
 
 // Split-K, second launch on the same stream: C <- alpha * (P_0 + ... + P_{S-1}) +
@@ -390,6 +404,68 @@ struct Reduce {
   static constexpr int CHUNKS = NP / CH;
   static_assert(NP % CH == 0, "whole chunks");
 };
+
+#ifdef DBGEMM_EPILOGUE
+
+// The same with an epilogue: workgroup (tile, i) adds the partials of fragment row i of every
+// row of waves, puts the WM x 16 rows together in LDS and runs the epilogue over them.
+template <class C>
+__global__ __launch_bounds__(C::THREADS) void split_reduce_ep_kernel(GemmEpArgs a) {
+  constexpr int ROWS = C::WM * 16, RB = C::BN * 4, CH = C::BN / 8, RPS = C::THREADS / CH, STEPS = ROWS / RPS;
+  static_assert(C::ACC == 4 && ROWS % RPS == 0 && RPS * RB <= ROWS * RB, "16x16 fragments, whole steps of rows");
+  __shared__ __attribute__((aligned(1024))) char lds[ROWS * RB];
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_char*)lds;
+  const int tile = blockIdx.x / C::FM, i = blockIdx.x % C::FM;
+  const int tm = tile / a.tiles_n, tn = tile % a.tiles_n;
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  const int wm = wave / C::WN, wn = wave % C::WN;
+  const int m0 = tm * C::BM, n0 = tn * C::BN;
+  // local row r of the strip is row (r / 16) WTM + 16 i + r % 16 of the tile
+  auto row_of = [&](int r) { return m0 + (r >> 4) * C::WTM + i * 16 + (r & 15); };
+  const int row = t / CH, ch = (t % CH) * 2, n = n0 + (t % CH) * 8;
+  const int nvc = min(max(a.N - n, 0), 8);
+  float cs[8] = {}, b[8];
+  ep_bias8(a, n, nvc, b);
+  const f32x4* src = (const f32x4*)(a.ws + (size_t)tile * a.splits * (C::BM * C::BN)) + i * C::FN * C::THREADS + t;
+  constexpr size_t stride = (size_t)C::FM * C::FN * C::THREADS;  // float4s per partial
+  ep_dispatch(a.ep, [&](auto gc, auto ac) {
+    constexpr bool GRAD = decltype(gc)::value;
+    EpRaw raw[STEPS];
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+      const int m = row_of(s * RPS + row);
+      ep_fetch8<GRAD>(a, m, n, m < a.M ? nvc : 0, raw[s]);
+    }
+    if (row_of(wm * 16) < a.M) {  // (this wave's rows past M hold no sums)
+      f32x4 v[C::FN];
+#pragma unroll
+      for (int j = 0; j < C::FN; ++j) v[j] = src[j * C::THREADS];
+#pragma unroll 4
+      for (int s = 1; s < a.splits; ++s)
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j) v[j] += src[s * stride + j * C::THREADS];
+#pragma unroll
+      for (int j = 0; j < C::FN; ++j) {
+        const int r = wm * 16 + lane % 16, chunk = ((wn * C::WTN + j * 16 + 4 * (lane / 16)) >> 2) ^ (r & 15);
+        *(__attribute__((address_space(3))) f32x4*)(uintptr_t)(lds0 + (uint32_t)(r * RB + chunk * 16)) =
+            (f32x4){a.alpha * v[j][0], a.alpha * v[j][1], a.alpha * v[j][2], a.alpha * v[j][3]};
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+      const int r = s * RPS + row, m = row_of(r);
+      const uint32_t at = lds0 + (uint32_t)(r * RB);
+      const f32x4 lo = *(__attribute__((address_space(3))) f32x4*)(uintptr_t)(at + ((ch ^ (r & 15)) * 16));
+      const f32x4 hi = *(__attribute__((address_space(3))) f32x4*)(uintptr_t)(at + (((ch + 1) ^ (r & 15)) * 16));
+      float w[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+      ep_finish8<false, GRAD, decltype(ac)::value>(a, w, raw[s], b, m, n, m < a.M ? nvc : 0, cs);
+    }
+  });
+  if (a.ep.grad && a.ep.colsum) ep_put_colsum<C::THREADS, C::BN>(a, cs, (int64_t)tm * C::FM + i, n0, t, lds0);
+}
+
+#else
 
 template <class C>
 __global__ __launch_bounds__(C::THREADS) void split_reduce_kernel(GemmArgs a) {
@@ -412,15 +488,21 @@ __global__ __launch_bounds__(C::THREADS) void split_reduce_kernel(GemmArgs a) {
     store_group<C>(a, v[c], c0 + c, tm * C::BM + wm * C::WTM, tn * C::BN + wn * C::WTN, lane);
 }
 
+#endif
+
 template <class C>
-hipError_t launch_cfg(const GemmArgs& a, hipStream_t s) {
+hipError_t launch_cfg(const KernelArgs& a, hipStream_t s) {
   const int ntiles = a.tiles_m * a.tiles_n;
   const unsigned by = a.batch_y > 1 ? (unsigned)a.batch_y : 1u, bz = a.batch_z > 1 ? (unsigned)a.batch_z : 1u;
   hipLaunchKernelGGL(gemm_dma_kernel<C>, dim3(grid_tiles(a), by, bz), dim3(C::THREADS), 0, s, a);
   if (a.splits > 1) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
+#ifdef DBGEMM_EPILOGUE
+    hipLaunchKernelGGL(split_reduce_ep_kernel<C>, dim3(ntiles * C::FM), dim3(C::THREADS), 0, s, a);
+#else
     hipLaunchKernelGGL(split_reduce_kernel<C>, dim3(ntiles * Reduce<C>::CHUNKS), dim3(C::THREADS), 0, s, a);
+#endif
   }
   return hipGetLastError();
 }
@@ -428,11 +510,35 @@ hipError_t launch_cfg(const GemmArgs& a, hipStream_t s) {
 // This file is compiled once per transpose case (DBGEMM_DMA_TA, DBGEMM_DMA_TB) and half of
 // the policy table (DBGEMM_DMA_PART: the entries on even or odd lines of policies.inc), so
 // the eight groups of kernel instantiations build in parallel.
-#if !defined(DBGEMM_DMA_TA) || !defined(DBGEMM_DMA_TB) || !defined(DBGEMM_DMA_PART)
+// With DBGEMM_EPILOGUE once per transpose case (few entries).
+#if !defined(DBGEMM_DMA_TA) || !defined(DBGEMM_DMA_TB) || \
+    (!defined(DBGEMM_DMA_PART) && !defined(DBGEMM_EPILOGUE))
 #error "compile with -DDBGEMM_DMA_TA=0|1 -DDBGEMM_DMA_TB=0|1 -DDBGEMM_DMA_PART=0|1"
 #endif
 
 }  // namespace
+
+#ifdef DBGEMM_EPILOGUE
+
+#define DBGEMM_DMA_CAT2(a, b) launch_mfma_dma_ep_##a##b
+#define DBGEMM_DMA_CAT(a, b) DBGEMM_DMA_CAT2(a, b)
+
+hipError_t DBGEMM_DMA_CAT(DBGEMM_DMA_TA, DBGEMM_DMA_TB)(const Policy& p, const GemmEpArgs& a, int* parts,
+                                                        hipStream_t s) {
+  // partial rows: one per row of tiles, or per strip of the second launch
+  *parts = a.splits > 1 ? a.tiles_m * (p.BM / p.WM / 16) : a.tiles_m;
+#define DBGEMM_SIMT(name, eff)
+#define DBGEMM_MFMA(name_, pipe_, in_, bm_, bn_, bk_, wm_, wn_, mt_, st_, grp_, rn_, xcd_, sw_, eff_)      \
+  if constexpr (pipe_ == 1 && has_epilogue(pipe_, in_, bm_, bn_, bk_, mt_, ((sw_) >> 3) & 1, eff_))        \
+    if (p.BM == bm_ && p.BN == bn_ && p.BK == bk_ && p.WM == wm_ && p.WN == wn_ && p.stages == st_)        \
+      return launch_cfg<Cfg<bm_, bn_, bk_, wm_, wn_, mt_, st_, in_, DBGEMM_DMA_TA != 0, DBGEMM_DMA_TB != 0>>(a, s);
+#include "policies.inc"
+#undef DBGEMM_SIMT
+#undef DBGEMM_MFMA
+  return hipErrorInvalidConfiguration;
+}
+
+#else
 
 #define DBGEMM_DMA_CAT2(a, b, c) launch_mfma_dma_##a##b##_p##c
 #define DBGEMM_DMA_CAT(a, b, c) DBGEMM_DMA_CAT2(a, b, c)
@@ -456,5 +562,7 @@ bool DBGEMM_DMA_CAT(DBGEMM_DMA_TA, DBGEMM_DMA_TB, DBGEMM_DMA_PART)(const Policy&
 #undef DBGEMM_MFMA
   return false;
 }
+
+#endif
 
 }  // namespace dbgemm

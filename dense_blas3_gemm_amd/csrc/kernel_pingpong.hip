@@ -42,9 +42,18 @@
 // widened with its block's scale code placed in the exponent field of the conversion's
 // scale operand.
 #include "mfma_common.h"
+#ifdef DBGEMM_EPILOGUE  // the kernels of products with an epilogue
+#include "epilogue_tile.h"
+#endif
 
 namespace dbgemm {
 namespace {
+
+#ifdef DBGEMM_EPILOGUE
+using KernelArgs = GemmEpArgs;
+#else
+using KernelArgs = GemmArgs;
+#endif
 
 typedef unsigned short u16x8 __attribute__((ext_vector_type(8)));
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
@@ -438,7 +447,7 @@ __device__ __forceinline__ void pp_store_tile_lds(const GemmArgs& a, const typen
 // other sk_tiles tiles).  Each workgroup runs its segments (a tile and a range [k0, k1) of
 // its K tiles) one after the other, each through the same two-group pipeline.
 template <class C, bool SK>
-__global__ __launch_bounds__(512) void gemm_pp_kernel(GemmArgs a) {
+__global__ __launch_bounds__(512) void gemm_pp_kernel(KernelArgs a) {
   using P = PingPong<C>;
   constexpr int S = P::S;
   __shared__ __attribute__((aligned(1024))) char lds[P::LDS_BYTES];
@@ -955,14 +964,26 @@ __global__ __launch_bounds__(512) void gemm_pp_kernel(GemmArgs a) {
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       __syncthreads();
     } else {
+#ifdef DBGEMM_EPILOGUE
+      ep_tile<C, true>(a, acc, m0, n0, tm, wm, xb0, lane, t, lds0);
+#else
       pp_store_tile_lds<C>(a, acc, m0, n0, grp, xb0, lane, t, lds0);
+#endif
       break;
     }
   }
 }
 
+#ifdef DBGEMM_EPILOGUE
 template <class C>
-hipError_t launch_pp(const GemmArgs& a, hipStream_t s) {
+hipError_t launch_pp(const KernelArgs& a, hipStream_t s) {
+  if (a.splits != 1 || a.sk_tiles > 0) return hipErrorInvalidConfiguration;
+  hipLaunchKernelGGL((gemm_pp_kernel<C, false>), dim3(grid_tiles(a)), dim3(C::THREADS), 0, s, a);
+  return hipGetLastError();
+}
+#else
+template <class C>
+hipError_t launch_pp(const KernelArgs& a, hipStream_t s) {
   if (a.splits != 1 || a.tri != TRI_NONE || a.kband != KBAND_NONE || a.dual) return hipErrorInvalidConfiguration;
   if constexpr (PingPong<C>::MXS) {
     // scale rows of whole dwords, at least one byte per 32-element block of K
@@ -987,6 +1008,7 @@ hipError_t launch_pp(const GemmArgs& a, hipStream_t s) {
   }
   return hipGetLastError();
 }
+#endif
 
 #if !defined(DBGEMM_DMA_TA) || !defined(DBGEMM_DMA_TB)
 #error "compile with -DDBGEMM_DMA_TA=0|1 -DDBGEMM_DMA_TB=0|1"
@@ -994,8 +1016,30 @@ hipError_t launch_pp(const GemmArgs& a, hipStream_t s) {
 
 }  // namespace
 
+#ifdef DBGEMM_EPILOGUE
+#define DBGEMM_PP_CAT2(a, b) launch_mfma_pp_ep_##a##b
+#else
 #define DBGEMM_PP_CAT2(a, b) launch_mfma_pp_##a##b
+#endif
 #define DBGEMM_PP_CAT(a, b) DBGEMM_PP_CAT2(a, b)
+
+#ifdef DBGEMM_EPILOGUE
+
+hipError_t DBGEMM_PP_CAT(DBGEMM_DMA_TA, DBGEMM_DMA_TB)(const Policy& p, const GemmEpArgs& a, int* parts,
+                                                       hipStream_t s) {
+  *parts = a.tiles_m;  // one partial row per row of tiles
+#define DBGEMM_SIMT(name, eff)
+#define DBGEMM_MFMA(name_, pipe_, in_, bm_, bn_, bk_, wm_, wn_, mt_, st_, grp_, rn_, xcd_, sw_, eff_)              \
+  if constexpr (pipe_ == 2 && has_epilogue(pipe_, in_, bm_, bn_, bk_, mt_, ((sw_) >> 3) & 1, eff_))                \
+    if (p.BM == bm_ && p.BN == bn_ && p.BK == bk_ && p.in_mode == in_)                                            \
+      return launch_pp<Cfg<bm_, bn_, bk_, wm_, wn_, mt_, st_, in_, DBGEMM_DMA_TA != 0, DBGEMM_DMA_TB != 0>>(a, s);
+#include "policies_pp.inc"
+#undef DBGEMM_SIMT
+#undef DBGEMM_MFMA
+  return hipErrorInvalidConfiguration;
+}
+
+#else
 
 // pipe 2 entries of the policy table; a tile edge whose M/N-contiguous rows would not be
 // a power of two of chunks is not instantiated for that transpose case (the policy code
@@ -1015,5 +1059,7 @@ hipError_t DBGEMM_PP_CAT(DBGEMM_DMA_TA, DBGEMM_DMA_TB)(const Policy& p, const Ge
 #undef DBGEMM_MFMA
   return hipErrorInvalidConfiguration;
 }
+
+#endif
 
 }  // namespace dbgemm

@@ -17,7 +17,8 @@ static_assert(GEMM_TYPE_BF16 == T_BF16 && GEMM_TYPE_F32 == T_F32, "the kernels' 
 
 namespace {
 
-// The workspace: partial column sums first, a product in fp32 behind them.
+// The workspace: partial column sums, or a split product's partial tiles, first; behind them a
+// product in fp32, or the column sums of a product with an epilogue.
 constexpr size_t kPartBytes = (size_t)64 << 20;
 constexpr int kMaxParts = 512;
 
@@ -104,6 +105,42 @@ gemm_status_t run_by_rows(const HandleView& v, GemmEpArgs a, int transA, int tra
   return GEMM_STATUS_SUCCESS;
 }
 
+// The product with its epilogue in the kernel that computes it; false when no such kernel
+// takes the operands.
+bool run_fused(const HandleView& v, GemmEpArgs a, int transA, int transB, int dtype, float* dbias, gemm_status_t* st) {
+  if (a.K == 0 || a.alpha == 0.f) return false;
+  Problem pr = gemm_problem(transA, transB, a.M, a.N, a.K, a.A, a.lda, a.B, a.ldb, a.C, a.ldc, dtype);
+  if (!pr.fast_ok) return false;
+  pr.ep = true;
+  int sp = 1;
+  const int64_t split_floats = v.ws ? (int64_t)(kPartBytes / sizeof(float)) : 0;
+  const Policy& p = policy_at(policy_select(pr, v.cu_count, split_floats, &sp));
+  if (p.kind != KIND_MFMA) return false;
+  a.in_fp8 = pr.in_fp8;
+  a.transA = transA;
+  a.transB = transB;
+  a.tiles_m = (a.M + p.BM - 1) / p.BM;
+  a.tiles_n = (a.N + p.BN - 1) / p.BN;
+  a.group = p.group;
+  a.raster_n = p.raster_n;
+  a.xcd = p.xcd;
+  a.swizzle = p.swizzle;
+  a.splits = sp;
+  a.kt_per_split = (int)split_kt(p, a.K, sp);
+  a.ws = sp > 1 ? (float*)v.ws : nullptr;
+  if (dbias) {
+    // at most one partial row per 16 rows of C
+    const int64_t most = ((int64_t)a.tiles_m * p.BM / 16) * a.N * (int64_t)sizeof(float);
+    if (!v.ws || v.ws_bytes < kPartBytes + (size_t)most) return false;
+    a.ep.colsum = (float*)((char*)v.ws + kPartBytes);
+  }
+  int parts = 0;
+  hipError_t e = launch_mfma_ep(p, a, &parts, v.stream);
+  if (e == hipSuccess && dbias) e = launch_colsum(a.ep.colsum, parts, a.N, a.N, dbias, nullptr, 0, v.stream);
+  *st = status(e);
+  return true;
+}
+
 gemm_status_t run_product(gemm_handle_t h, int transA, int transB, int64_t M, int64_t N, int64_t K, float alpha,
                           const void* A, int64_t lda, const void* B, int64_t ldb, void* C, int64_t ldc, int dtype,
                           const EpArgs& e, float* dbias) {
@@ -126,10 +163,28 @@ gemm_status_t run_product(gemm_handle_t h, int transA, int transB, int64_t M, in
   a.alpha = alpha;
   a.c_kind = (dtype == GEMM_BF16_F32 || dtype == GEMM_E4M3_F32) ? C_F32 : C_BF16;
   a.ep = e;
+  gemm_status_t st;
+  if (run_fused(v, a, transA, transB, dtype, dbias, &st)) return st;
   return run_by_rows(v, a, transA, transB, dtype, dbias);
 }
 
 }  // namespace
+
+namespace dbgemm {
+hipError_t launch_mfma_ep(const Policy& p, const GemmEpArgs& a, int* parts, hipStream_t s) {
+#define DBGEMM_EP_CASE(ab)                                                                       \
+  return p.pipe == 2   ? launch_mfma_pp_ep_##ab(p, a, parts, s)                                  \
+         : p.pipe == 1 ? launch_mfma_dma_ep_##ab(p, a, parts, s)                                 \
+                       : launch_mfma_staged_ep_##ab(p, a, parts, s)
+  switch (a.transA * 2 + a.transB) {
+    case 0: DBGEMM_EP_CASE(00);
+    case 1: DBGEMM_EP_CASE(01);
+    case 2: DBGEMM_EP_CASE(10);
+    default: DBGEMM_EP_CASE(11);
+  }
+#undef DBGEMM_EP_CASE
+}
+}  // namespace dbgemm
 
 extern "C" {
 

@@ -37,6 +37,20 @@ struct GemmEpArgs : GemmArgs {
   EpArgs ep;
 };
 
+// Products with an epilogue on the MFMA kernels: policy p (has_epilogue) on a, whose grid
+// fields are set; with ep.colsum set, *parts receives the partial rows it writes.
+hipError_t launch_mfma_ep(const Policy& p, const GemmEpArgs& a, int* parts, hipStream_t s);
+// one per kernel family and (transA, transB) case, each in its own object
+#define DBGEMM_EP_DECL(ab)                                                                               \
+  hipError_t launch_mfma_pp_ep_##ab(const Policy& p, const GemmEpArgs& a, int* parts, hipStream_t s);     \
+  hipError_t launch_mfma_dma_ep_##ab(const Policy& p, const GemmEpArgs& a, int* parts, hipStream_t s);    \
+  hipError_t launch_mfma_staged_ep_##ab(const Policy& p, const GemmEpArgs& a, int* parts, hipStream_t s);
+DBGEMM_EP_DECL(00)
+DBGEMM_EP_DECL(01)
+DBGEMM_EP_DECL(10)
+DBGEMM_EP_DECL(11)
+#undef DBGEMM_EP_DECL
+
 // ---- launchers (they return hipSuccess or the launch error)
 
 // Epilogue of a product held in fp32: a.ws is rows [0, M) of alpha * op(A) op(B) with row

@@ -58,6 +58,7 @@ int policy_find(const char* name) {
 bool policy_serves(const Policy& p, const Problem& pr) {
   if (p.kind == KIND_SIMT) return true;
   if (p.kind != KIND_MFMA || !pr.fast_ok) return false;
+  if (pr.ep && !has_epilogue(p.pipe, p.in_mode, p.BM, p.BN, p.BK, p.MT, p.k_contig_only, p.efficiency)) return false;
   if (p.k_contig_only && (pr.transA != 0 || pr.transB != 1)) return false;
   if (p.a_kc_only && pr.transA != 0) return false;
   if (pr.mx) return p.in_mode == 3 || ((p.in_mode == 4 || p.in_mode == 6) && pr.mx_words);

@@ -49,13 +49,12 @@ __global__ __launch_bounds__(kThreads) void ep_rows_kernel(GemmEpArgs a, int64_t
   const int nv = a.N - n < 8 ? (a.N > n ? a.N - n : 0) : 8;
   float cs[8] = {}, b[8];
   ep_bias8(a, n, nv, b);
-  ep_dispatch(a.ep, [&](auto gc, auto ac) {
+  ep_dispatch(a.ep, [&](auto gc, auto ac) EP_INLINE {
     for (int64_t m = (int64_t)blockIdx.y * blockDim.y + threadIdx.y; m < a.M; m += (int64_t)gridDim.y * blockDim.y) {
       float w[8];
-      EpRaw r;
-      ep_fetch8<decltype(gc)::value>(a, m, n, nv, r);
+      const EpRaw r = ep_fetch8<decltype(gc)::value, true>(a, m, n, nv);
       ep_load8(a.ws + m * ldw + n, nv, w);
-      ep_finish8<false, decltype(gc)::value, decltype(ac)::value>(a, w, r, b, m, n, nv, cs);
+      ep_finish8<false, decltype(gc)::value, decltype(ac)::value, true>(a, w, r, b, m, n, nv, cs);
     }
   });
   put_partial(a.ep.colsum, a.N, n, cs);
@@ -95,7 +94,7 @@ __global__ __launch_bounds__(kThreads) void act_mx_kernel(int64_t rows, int64_t 
     float v[8];
     ep_load8(z + m * ldz + n, nv, v);
     ep_store_mx(v, nv, (n & 31) == 0, q + m * ldq + n, sc + m * ldsc + (n >> 5));
-    ep_with_act(act, [&](auto ac) {
+    ep_with_act(act, [&](auto ac) EP_INLINE {
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = ep_act<decltype(ac)::value>(v[i]);
     });
@@ -118,7 +117,7 @@ __global__ __launch_bounds__(kThreads) void act_grad_mx_kernel(int64_t rows, int
     if (dh) {
       float d[8];
       ep_load8(dh + m * lddh + n, nv, d);
-      ep_with_act(act, [&](auto ac) {
+      ep_with_act(act, [&](auto ac) EP_INLINE {
 #pragma unroll
         for (int i = 0; i < 8; ++i) d[i] *= ep_slope<decltype(ac)::value>(z[i]);
       });
@@ -127,7 +126,7 @@ __global__ __launch_bounds__(kThreads) void act_grad_mx_kernel(int64_t rows, int
       if (dz) ep_store8<false>(dz + m * lddz + n, nv, d);
     }
     if (h) {
-      ep_with_act(act, [&](auto ac) {
+      ep_with_act(act, [&](auto ac) EP_INLINE {
 #pragma unroll
         for (int i = 0; i < 8; ++i) z[i] = ep_act<decltype(ac)::value>(z[i]);
       });

@@ -8,6 +8,9 @@
 #include "e4m3_codec.h"
 #include "mlp_internal.h"
 
+// Lambdas over an activation: called, their captured arrays would live in scratch memory.
+#define EP_INLINE __attribute__((always_inline))
+
 namespace dbgemm {
 namespace {
 
@@ -19,6 +22,9 @@ typedef unsigned int ep_u32x2 __attribute__((ext_vector_type(2)));
 typedef ep_u16x8 ep_u16x8_u __attribute__((aligned(2)));
 typedef ep_f32x4 ep_f32x4_u __attribute__((aligned(4)));
 typedef ep_u32x2 ep_u32x2_u __attribute__((aligned(1)));
+typedef unsigned int ep_u32x4 __attribute__((ext_vector_type(4)));
+typedef ep_u32x4 ep_u32x4_4 __attribute__((aligned(4)));
+typedef ep_u32x4 ep_u32x4_2 __attribute__((aligned(2)));
 
 __device__ __forceinline__ float ep_bf16f(uint16_t b) { return __builtin_bit_cast(float, (uint32_t)b << 16); }
 __device__ __forceinline__ uint16_t ep_f32bf(float v) {
@@ -58,8 +64,8 @@ __device__ __forceinline__ void ep_load8(const void* p, int64_t idx, int f32, in
 }
 
 // The whole-vector stores of large outputs are non-temporal (NT): the kernel does not read
-// them again.
-template <bool NT>
+// them again.  PART = false: nv is 8 or 0 (columns in whole eights), here and below.
+template <bool NT, bool PART = true>
 __device__ __forceinline__ void ep_store8(uint16_t* p, int nv, const float (&v)[8]) {
   if (nv == 8) {
     ep_u16x8 w;
@@ -69,13 +75,13 @@ __device__ __forceinline__ void ep_store8(uint16_t* p, int nv, const float (&v)[
       __builtin_nontemporal_store(w, (ep_u16x8_u*)p);
     else
       *(ep_u16x8_u*)p = w;
-  } else {
+  } else if constexpr (PART) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       if (i < nv) p[i] = ep_f32bf(v[i]);
   }
 }
-template <bool NT>
+template <bool NT, bool PART = true>
 __device__ __forceinline__ void ep_store8(float* p, int nv, const float (&v)[8]) {
   if (nv == 8) {
     const ep_f32x4 a = {v[0], v[1], v[2], v[3]}, b = {v[4], v[5], v[6], v[7]};
@@ -86,18 +92,18 @@ __device__ __forceinline__ void ep_store8(float* p, int nv, const float (&v)[8])
       *(ep_f32x4_u*)p = a;
       *(ep_f32x4_u*)(p + 4) = b;
     }
-  } else {
+  } else if constexpr (PART) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       if (i < nv) p[i] = v[i];
   }
 }
-template <bool NT>
+template <bool NT, bool PART = true>
 __device__ __forceinline__ void ep_store8(void* p, int64_t idx, int f32, int nv, const float (&v)[8]) {
   if (f32)
-    ep_store8<NT>((float*)p + idx, nv, v);
+    ep_store8<NT, PART>((float*)p + idx, nv, v);
   else
-    ep_store8<NT>((uint16_t*)p + idx, nv, v);
+    ep_store8<NT, PART>((uint16_t*)p + idx, nv, v);
 }
 
 // ---- activations.  logistic(v) = 1 / (1 + 2^(-v log2 e)) with the hardware's exponential
@@ -175,6 +181,7 @@ __device__ __forceinline__ void ep_with_act(int act, F&& f) {
 // 32 columns (columns n & ~31 .. + 31) run this together, each with its eight (the invalid
 // ones zero).  Stores the first nv codes at q and, from the block's first lane when it has
 // any column, the scale byte at s.
+template <bool PART = true>
 __device__ __forceinline__ void ep_store_mx(const float (&v)[8], int nv, bool first, uint8_t* q, uint8_t* s) {
   float amax = 0.f;
 #pragma unroll
@@ -188,7 +195,7 @@ __device__ __forceinline__ void ep_store_mx(const float (&v)[8], int nv, bool fi
   if (first && nv > 0) *s = (uint8_t)e;
   if (nv == 8) {
     *(ep_u32x2_u*)q = (ep_u32x2){lo, hi};
-  } else {
+  } else if constexpr (PART) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       if (i < nv) q[i] = (uint8_t)((i < 4 ? lo : hi) >> (8 * (i & 3)));
@@ -228,69 +235,83 @@ __device__ __forceinline__ void ep_load_mx(const uint8_t* q, int nv, uint32_t sc
 // the rest, so that a caller can have the loads of several rows in flight.  nv: the valid
 // columns, 0 .. 8 (0: no row or column here).
 struct EpRaw {
-  uint32_t d[8];  // 8 bf16 in d[0..3], 8 fp32, or 8 codes in d[0..1] and their scale in d[2]
+  ep_u32x4 lo, hi;  // 8 bf16 in lo, 8 fp32, or 8 codes in lo[0..1] and their scale in lo[2]
 };
 
-// d[0 .. W) <- W * 4 bytes at p, or (a part) the first nv elements of ES bytes, zeros behind
-template <int W, int ES>
-__device__ __forceinline__ void ep_raw(const void* p, int nv, EpRaw& r) {
-  typedef uint32_t vec __attribute__((ext_vector_type(W == 8 ? 4 : W)));
-  typedef vec vec_u __attribute__((aligned(ES)));
-  if (nv == 8) {
-    const vec v = *(const vec_u*)p;
+// nv elements of ES bytes at p as dwords [first, first + 4) of their row of W dwords, zeros
+// behind them
+template <int ES>
+__device__ __forceinline__ ep_u32x4 ep_raw_part(const void* p, int nv, int first) {
+  ep_u32x4 v = {0, 0, 0, 0};
 #pragma unroll
-    for (int i = 0; i < (W == 8 ? 4 : W); ++i) r.d[i] = v[i];
-    if constexpr (W == 8) {
-      const vec u = *(const vec_u*)((const char*)p + 16);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) r.d[4 + i] = u[i];
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < W; ++i) r.d[i] = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < nv) {
-        const uint32_t e = ES == 4 ? ((const uint32_t*)p)[i] : ES == 2 ? ((const uint16_t*)p)[i] : ((const uint8_t*)p)[i];
-        r.d[i * ES / 4] |= e << (8 * (i * ES % 4));
-      }
+  for (int i = 0; i < 16 / ES && i < 8; ++i) {
+    const int e = first * 4 / ES + i;
+    if (e < nv)
+      v[i * ES / 4] |= (ES == 4 ? ((const uint32_t*)p)[e] : ES == 2 ? ((const uint16_t*)p)[e] : ((const uint8_t*)p)[e])
+                       << (8 * (i * ES % 4));
   }
+  return v;
 }
 
-template <bool GRAD>
-__device__ __forceinline__ void ep_fetch8(const GemmEpArgs& a, int64_t m, int n, int nv, EpRaw& r) {
+template <bool GRAD, bool PART>
+__device__ __forceinline__ EpRaw ep_fetch8(const GemmEpArgs& a, int64_t m, int n, int nv) {
   const EpArgs& e = a.ep;
-  if (nv == 0) return;
+  EpRaw r;
+  r.lo = r.hi = (ep_u32x4){0, 0, 0, 0};
+  if (nv == 0) return r;
+  const bool whole = !PART || nv == 8;
   if constexpr (GRAD) {
     if (e.z_kind == Z_MX) {
-      ep_raw<2, 1>((const uint8_t*)e.Z + m * e.ldz + n, nv, r);
-      r.d[2] = e.S[m * e.lds + (n >> 5)];
-    } else {
-      ep_raw<4, 2>((const uint16_t*)e.Z + m * e.ldz + n, nv, r);
+      const uint8_t* p = (const uint8_t*)e.Z + m * e.ldz + n;
+      if (whole) {
+        const ep_u32x2 v = *(const ep_u32x2_u*)p;
+        r.lo = (ep_u32x4){v[0], v[1], 0, 0};
+      } else if constexpr (PART) {
+        r.lo = ep_raw_part<1>(p, nv, 0);
+      }
+      r.lo[2] = e.S[m * e.lds + (n >> 5)];
+      return r;
     }
-  } else if (e.R) {
-    if (a.c_kind == C_F32)
-      ep_raw<8, 4>((const float*)e.R + m * e.ldr + n, nv, r);
-    else
-      ep_raw<4, 2>((const uint16_t*)e.R + m * e.ldr + n, nv, r);
+  } else {
+    if (!e.R) return r;
+    if (a.c_kind == C_F32) {
+      const float* p = (const float*)e.R + m * e.ldr + n;
+      if (whole) {
+        r.lo = *(const ep_u32x4_4*)p;
+        r.hi = *(const ep_u32x4_4*)(p + 4);
+      } else if constexpr (PART) {
+        r.lo = ep_raw_part<4>(p, nv, 0);
+        r.hi = ep_raw_part<4>(p, nv, 4);
+      }
+      return r;
+    }
   }
+  const uint16_t* p = GRAD ? (const uint16_t*)e.Z + m * e.ldz + n : (const uint16_t*)e.R + m * e.ldr + n;
+  if (whole)
+    r.lo = *(const ep_u32x4_2*)p;
+  else if constexpr (PART)
+    r.lo = ep_raw_part<2>(p, nv, 0);
+  return r;
 }
 
 __device__ __forceinline__ void ep_raw_bf16(const EpRaw& r, float (&v)[8]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __builtin_bit_cast(float, r.d[i] << 16);
-    v[2 * i + 1] = __builtin_bit_cast(float, r.d[i] & 0xFFFF0000u);
+    v[2 * i] = __builtin_bit_cast(float, r.lo[i] << 16);
+    v[2 * i + 1] = __builtin_bit_cast(float, r.lo[i] & 0xFFFF0000u);
   }
 }
 __device__ __forceinline__ void ep_raw_f32(const EpRaw& r, float (&v)[8]) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = __builtin_bit_cast(float, r.d[i]);
+  for (int i = 0; i < 4; ++i) {
+    v[i] = __builtin_bit_cast(float, (uint32_t)r.lo[i]);
+    v[4 + i] = __builtin_bit_cast(float, (uint32_t)r.hi[i]);
+  }
 }
 
 // w = alpha * product, b = the bias of these columns (zeros without one).  The four lanes of a
 // block of 32 columns call it together.  A gradient's unrounded results are added to cs.
-template <bool NT, bool GRAD, int ACT>
+template <bool NT, bool GRAD, int ACT, bool PART>
 __device__ __forceinline__ void ep_finish8(const GemmEpArgs& a, float (&w)[8], const EpRaw& r, const float (&b)[8],
                                            int64_t m, int n, int nv, float (&cs)[8]) {
   const EpArgs& e = a.ep;
@@ -298,24 +319,24 @@ __device__ __forceinline__ void ep_finish8(const GemmEpArgs& a, float (&w)[8], c
   if constexpr (GRAD) {
     if (nv == 0) return;
     if (e.z_kind == Z_MX)
-      ep_codes8(r.d[0], r.d[1], r.d[2], v);
+      ep_codes8(r.lo[0], r.lo[1], r.lo[2], v);
     else
       ep_raw_bf16(r, v);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       w[i] *= ep_slope<ACT>(v[i]);
-      cs[i] += i < nv ? w[i] : 0.f;
+      cs[i] += !PART || i < nv ? w[i] : 0.f;
     }
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) w[i] += b[i];
     if (e.z_kind == Z_MX) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = i < nv ? w[i] : 0.f;
-      ep_store_mx(v, nv, (n & 31) == 0, (uint8_t*)e.Z + m * e.ldz + n, e.S + m * e.lds + (n >> 5));
+      for (int i = 0; i < 8; ++i) v[i] = (PART ? i < nv : nv > 0) ? w[i] : 0.f;
+      ep_store_mx<PART>(v, nv, (n & 31) == 0, (uint8_t*)e.Z + m * e.ldz + n, e.S + m * e.lds + (n >> 5));
     }
     if (nv == 0) return;
-    if (e.z_kind == Z_BF16) ep_store8<NT>((uint16_t*)e.Z + m * e.ldz + n, nv, w);
+    if (e.z_kind == Z_BF16) ep_store8<NT, PART>((uint16_t*)e.Z + m * e.ldz + n, nv, w);
 #pragma unroll
     for (int i = 0; i < 8; ++i) w[i] = ep_act<ACT>(w[i]);
     if (e.R) {
@@ -327,7 +348,7 @@ __device__ __forceinline__ void ep_finish8(const GemmEpArgs& a, float (&w)[8], c
       for (int i = 0; i < 8; ++i) w[i] += e.beta * v[i];
     }
   }
-  ep_store8<NT>(a.C, m * a.ldc + n, a.c_kind == C_F32, nv, w);
+  ep_store8<NT, PART>(a.C, m * a.ldc + n, a.c_kind == C_F32, nv, w);
 }
 
 // the bias of columns [n, n + 8)
@@ -341,9 +362,9 @@ __device__ __forceinline__ void ep_bias8(const GemmEpArgs& a, int n, int nv, flo
 template <class F>
 __device__ __forceinline__ void ep_dispatch(const EpArgs& e, F&& f) {
   if (e.grad)
-    ep_with_act(e.act, [&](auto ac) { f(std::true_type{}, ac); });
+    ep_with_act(e.act, [&](auto ac) EP_INLINE { f(std::true_type{}, ac); });
   else
-    ep_with_act(e.act, [&](auto ac) { f(std::false_type{}, ac); });
+    ep_with_act(e.act, [&](auto ac) EP_INLINE { f(std::false_type{}, ac); });
 }
 
 }  // namespace

@@ -224,8 +224,8 @@ __global__ __launch_bounds__(C::THREADS) void gemm_mfma_kernel(KernelArgs a) {
   }
 
 #ifdef DBGEMM_EPILOGUE
-  static_assert(C::WTM * C::BN * 4 <= C::STAGES * C::STAGE_BYTES, "one row of waves' fp32 image fits the LDS");
-  ep_tile<C, false>(a, acc, m0, n0, tm, wm, xb0, lane, t, (uint32_t)(uintptr_t)sm);
+  ep_tile<C, C::STAGES * C::STAGE_BYTES, false>(a, acc, m0 + xa0, n0 + xb0, tm * C::WM + wm, wave, lane,
+                                                (uint32_t)(uintptr_t)sm);
 #else
   store_tile<C>(a, acc, m0 + xa0, n0 + xb0, lane);
 #endif
@@ -261,7 +261,7 @@ hipError_t launch_trans(const KernelArgs& a, hipStream_t s) {
 
 hipError_t DBGEMM_ST_CAT(DBGEMM_DMA_TA, DBGEMM_DMA_TB)(const Policy& p, const GemmEpArgs& a, int* parts,
                                                        hipStream_t s) {
-  *parts = a.tiles_m;  // one partial row per row of tiles
+  *parts = a.tiles_m * p.WM;  // one partial row per row of waves
 #define DBGEMM_SIMT(name, eff)
 #define DBGEMM_MFMA(name_, pipe_, in_, bm_, bn_, bk_, wm_, wn_, mt_, st_, grp_, rn_, xcd_, sw_, eff_)      \
   if constexpr (pipe_ == 0 && has_epilogue(pipe_, in_, bm_, bn_, bk_, mt_, ((sw_) >> 3) & 1, eff_))        \

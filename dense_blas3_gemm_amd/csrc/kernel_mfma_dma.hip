@@ -385,8 +385,8 @@ __global__ __launch_bounds__(C::THREADS) void gemm_dma_kernel(KernelArgs a) {
     return;
   }
 #ifdef DBGEMM_EPILOGUE
-  static_assert(C::WTM * C::BN * 4 <= C::STAGE_BYTES, "one row of waves' fp32 image fits a ring slot");
-  ep_tile<C, false>(a, acc, m0, n0, tm, wm, xb0, lane, t, (uint32_t)(uintptr_t)slot(std::integral_constant<int, 0>{}));
+  ep_tile<C, C::STAGE_BYTES, false>(a, acc, m0 + xa0, n0 + xb0, tm * C::WM + wm, wave, lane,
+                                    (uint32_t)(uintptr_t)slot(std::integral_constant<int, 0>{}));
 #else
   store_tile<C>(a, acc, m0 + xa0, n0 + xb0, lane);
 #endif
@@ -423,18 +423,18 @@ __global__ __launch_bounds__(C::THREADS) void split_reduce_ep_kernel(GemmEpArgs 
   // local row r of the strip is row (r / 16) WTM + 16 i + r % 16 of the tile
   auto row_of = [&](int r) { return m0 + (r >> 4) * C::WTM + i * 16 + (r & 15); };
   const int row = t / CH, ch = (t % CH) * 2, n = n0 + (t % CH) * 8;
-  const int nvc = min(max(a.N - n, 0), 8);
+  const int nvc = n < a.N ? 8 : 0;  // (N in whole eights)
   float cs[8] = {}, b[8];
   ep_bias8(a, n, nvc, b);
   const f32x4* src = (const f32x4*)(a.ws + (size_t)tile * a.splits * (C::BM * C::BN)) + i * C::FN * C::THREADS + t;
   constexpr size_t stride = (size_t)C::FM * C::FN * C::THREADS;  // float4s per partial
-  ep_dispatch(a.ep, [&](auto gc, auto ac) {
+  ep_dispatch(a.ep, [&](auto gc, auto ac) EP_INLINE {
     constexpr bool GRAD = decltype(gc)::value;
     EpRaw raw[STEPS];
 #pragma unroll
     for (int s = 0; s < STEPS; ++s) {
       const int m = row_of(s * RPS + row);
-      ep_fetch8<GRAD>(a, m, n, m < a.M ? nvc : 0, raw[s]);
+      raw[s] = ep_fetch8<GRAD, false>(a, m, n, m < a.M ? nvc : 0);
     }
     if (row_of(wm * 16) < a.M) {  // (this wave's rows past M hold no sums)
       f32x4 v[C::FN];
@@ -459,7 +459,7 @@ __global__ __launch_bounds__(C::THREADS) void split_reduce_ep_kernel(GemmEpArgs 
       const f32x4 lo = *(__attribute__((address_space(3))) f32x4*)(uintptr_t)(at + ((ch ^ (r & 15)) * 16));
       const f32x4 hi = *(__attribute__((address_space(3))) f32x4*)(uintptr_t)(at + (((ch + 1) ^ (r & 15)) * 16));
       float w[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-      ep_finish8<false, GRAD, decltype(ac)::value>(a, w, raw[s], b, m, n, m < a.M ? nvc : 0, cs);
+      ep_finish8<false, GRAD, decltype(ac)::value, false>(a, w, raw[s], b, m, n, m < a.M ? nvc : 0, cs);
     }
   });
   if (a.ep.grad && a.ep.colsum) ep_put_colsum<C::THREADS, C::BN>(a, cs, (int64_t)tm * C::FM + i, n0, t, lds0);
@@ -525,8 +525,8 @@ hipError_t launch_cfg(const KernelArgs& a, hipStream_t s) {
 
 hipError_t DBGEMM_DMA_CAT(DBGEMM_DMA_TA, DBGEMM_DMA_TB)(const Policy& p, const GemmEpArgs& a, int* parts,
                                                         hipStream_t s) {
-  // partial rows: one per row of tiles, or per strip of the second launch
-  *parts = a.splits > 1 ? a.tiles_m * (p.BM / p.WM / 16) : a.tiles_m;
+  // partial rows: one per row of waves, or per strip of the second launch
+  *parts = a.tiles_m * (a.splits > 1 ? p.BM / p.WM / 16 : p.WM);
 #define DBGEMM_SIMT(name, eff)
 #define DBGEMM_MFMA(name_, pipe_, in_, bm_, bn_, bk_, wm_, wn_, mt_, st_, grp_, rn_, xcd_, sw_, eff_)      \
   if constexpr (pipe_ == 1 && has_epilogue(pipe_, in_, bm_, bn_, bk_, mt_, ((sw_) >> 3) & 1, eff_))        \

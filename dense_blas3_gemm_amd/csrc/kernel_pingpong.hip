@@ -965,7 +965,7 @@ __global__ __launch_bounds__(512) void gemm_pp_kernel(KernelArgs a) {
       __syncthreads();
     } else {
 #ifdef DBGEMM_EPILOGUE
-      ep_tile<C, true>(a, acc, m0, n0, tm, wm, xb0, lane, t, lds0);
+      ep_tile<C, P::LDS_BYTES, true>(a, acc, m0 + xa0, n0 + xb0, tm * C::WM + wm, wave, lane, lds0);
 #else
       pp_store_tile_lds<C>(a, acc, m0, n0, grp, xb0, lane, t, lds0);
 #endif
@@ -1027,7 +1027,7 @@ hipError_t launch_pp(const KernelArgs& a, hipStream_t s) {
 
 hipError_t DBGEMM_PP_CAT(DBGEMM_DMA_TA, DBGEMM_DMA_TB)(const Policy& p, const GemmEpArgs& a, int* parts,
                                                        hipStream_t s) {
-  *parts = a.tiles_m;  // one partial row per row of tiles
+  *parts = a.tiles_m * p.WM;  // one partial row per row of waves
 #define DBGEMM_SIMT(name, eff)
 #define DBGEMM_MFMA(name_, pipe_, in_, bm_, bn_, bk_, wm_, wn_, mt_, st_, grp_, rn_, xcd_, sw_, eff_)              \
   if constexpr (pipe_ == 2 && has_epilogue(pipe_, in_, bm_, bn_, bk_, mt_, ((sw_) >> 3) & 1, eff_))                \

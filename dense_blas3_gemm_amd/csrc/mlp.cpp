@@ -108,7 +108,7 @@ gemm_status_t run_by_rows(const HandleView& v, GemmEpArgs a, int transA, int tra
 // The product with its epilogue in the kernel that computes it; false when no such kernel
 // takes the operands.
 bool run_fused(const HandleView& v, GemmEpArgs a, int transA, int transB, int dtype, float* dbias, gemm_status_t* st) {
-  if (a.K == 0 || a.alpha == 0.f) return false;
+  if (a.K == 0 || a.alpha == 0.f || a.N % 8 != 0) return false;
   Problem pr = gemm_problem(transA, transB, a.M, a.N, a.K, a.A, a.lda, a.B, a.ldb, a.C, a.ldc, dtype);
   if (!pr.fast_ok) return false;
   pr.ep = true;

@@ -48,6 +48,9 @@ class Epilogue(ctypes.Structure):
 
 
 _lib = None
+# set when the library is loaded: device index -> raw handle of torch's current stream there,
+# and the native part of the binding (with torch only)
+_RAW_STREAM, _NATIVE = [], []
 
 
 class GemmError(RuntimeError):
@@ -83,7 +86,9 @@ def load_library():
     if not os.path.exists(LIB_PATH):
         raise RuntimeError(f"{LIB_PATH} is missing: build it with `python -m dense_blas3_gemm_amd.build`")
     try:
-        import torch  # noqa: F401  (maps torch's HIP runtime before the library's)
+        import torch  # (maps torch's HIP runtime before the library's)
+        _RAW_STREAM[:] = [getattr(torch._C, "_cuda_getCurrentRawStream", None) or
+                          (lambda index: torch.cuda.current_stream(index).cuda_stream)]
     except ImportError:
         pass
     lib = ctypes.CDLL(LIB_PATH)
@@ -132,8 +137,23 @@ def load_library():
                "gemm_trsm", "gemm_run_act", "gemm_run_dact", "gemm_act_mx", "gemm_act_grad_mx", "gemm_layernorm",
                "gemm_layernorm_grad"]:
         getattr(lib, fn).restype = i32
+    if _RAW_STREAM:
+        _load_native()
     _lib = lib
     return lib
+
+
+def _load_native():
+    """Loads the native part of the binding on the library just loaded; raises if it is missing."""
+    path = os.path.join(PKG, "_binding.so")
+    if not os.path.exists(path):
+        raise RuntimeError(f"{path} is missing: build it with `python -m dense_blas3_gemm_amd.build`")
+    import importlib.util
+    spec = importlib.util.spec_from_file_location(__name__ + "._binding", path)
+    native = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(native)
+    native.bind(LIB_PATH)
+    _NATIVE[:] = [native]
 
 
 def version() -> str:
@@ -164,10 +184,11 @@ def _current_stream(device) -> int:
     """Raw hipStream_t of torch's current stream on `device` (the cheap accessor when
     this torch has it)."""
     import torch
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    if raw is not None:
-        return int(raw(device.index if device.index is not None else torch.cuda.current_device()))
-    return torch.cuda.current_stream(device).cuda_stream
+    return _raw_stream(device.index if device.index is not None else torch.cuda.current_device())
+
+
+def _raw_stream(index: int) -> int:
+    return int(_RAW_STREAM[0](index))
 
 
 def _ptr(t) -> int:
@@ -180,99 +201,6 @@ def _ld(t) -> int:
     assert t.dim() == 2 and (t.stride(1) == 1 or t.shape[1] <= 1 or t.shape[0] == 0), \
         "operands must be row-major 2-D views"
     return int(t.stride(0)) if t.shape[0] > 1 else max(int(t.stride(0)), int(t.shape[1]), 1)
-
-
-# ---- argument checks of the MLP-block operators: what the C-ABI cannot see of a tensor
-
-def _ld0(t) -> int:
-    return 0 if t is None else _ld(t)
-
-
-def _act(name: str) -> int:
-    try:
-        return ACTS[name]
-    except KeyError:
-        raise ValueError(f"act is one of {', '.join(ACTS)}: got {name!r}") from None
-
-
-def _type(t) -> int:
-    import torch
-    if t.dtype == torch.bfloat16:
-        return TYPE_BF16
-    if t.dtype == torch.float32:
-        return TYPE_F32
-    raise ValueError(f"bfloat16 or float32 is wanted: got {t.dtype}")
-
-
-def _bf16(t, name):
-    if _type(t) != TYPE_BF16:
-        raise ValueError(f"{name} has to be bfloat16: got {t.dtype}")
-
-
-def _vec(t, n, name, f32=False):
-    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
-        raise ValueError(f"{name} has to be a contiguous vector of {n} values: got {tuple(t.shape)}")
-    if _type(t) != TYPE_F32 and f32:
-        raise ValueError(f"{name} has to be float32: got {t.dtype}")
-
-
-def _same(t, like, name, dtype=False):
-    if t.shape != like.shape or (dtype and t.dtype != like.dtype):
-        raise ValueError(f"{name} has to be {tuple(like.shape)}" + (f" {like.dtype}" if dtype else "") +
-                         f": got {tuple(t.shape)} {t.dtype}")
-
-
-def _weights(gamma, beta, n) -> int:
-    kinds = set()
-    for t, name in ((gamma, "gamma"), (beta, "beta")):
-        if t is not None:
-            _vec(t, n, name)
-            kinds.add(_type(t))
-    if len(kinds) > 1:
-        raise ValueError("gamma and beta have to be of one type")
-    return kinds.pop() if kinds else TYPE_F32
-
-
-def _z(z, scales, M, N, mx=False):
-    """(kind, pointer, stride, scale pointer, scale stride) of a kept activation argument."""
-    import torch
-    if z.shape != (M, N):
-        raise ValueError(f"z has to be {(M, N)}: got {tuple(z.shape)}")
-    if scales is None:
-        if mx:
-            raise ValueError("codes need their scales")
-        _bf16(z, "z without scales")
-        return Z_BF16, z.data_ptr(), _ld(z), None, 0
-    if z.dtype not in (torch.float8_e4m3fn, torch.uint8) or scales.dtype != torch.uint8:
-        raise ValueError("8-bit z: float8_e4m3fn or uint8 codes with uint8 scales")
-    if scales.shape != (M, (N + 31) // 32):
-        raise ValueError(f"z_scales has to be {(M, (N + 31) // 32)}: got {tuple(scales.shape)}")
-    return Z_MX, z.data_ptr(), _ld(z), scales.data_ptr(), _ld(scales)
-
-
-def _k_of(A, B, transA, transB, M, N) -> int:
-    m, k = (A.shape[1], A.shape[0]) if transA else A.shape
-    n, k2 = B.shape if transB else (B.shape[1], B.shape[0])
-    if m != M or n != N or k != k2:
-        raise ValueError(f"op(A) {(m, k)} times op(B) {(k2, n)} is not C's {(M, N)}")
-    return k
-
-
-def _in_out(A, B, C) -> int:
-    import torch
-    if A.dtype != B.dtype or A.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
-        raise ValueError(f"A and B have to be bfloat16 or float8_e4m3fn: got {A.dtype}, {B.dtype}")
-    f32 = _type(C) == TYPE_F32
-    if A.dtype == torch.bfloat16:
-        return BF16_F32 if f32 else BF16_BF16
-    return E4M3_F32 if f32 else E4M3_BF16
-
-
-def _on(device, *tensors):
-    """Every tensor (None: absent) lives on the handle's device."""
-    for t in tensors:
-        if t is not None and t.get_device() != device:
-            raise ValueError(f"tensors of cuda:{device} are wanted: got one on {t.device}")
 
 
 class Gemm:
@@ -487,29 +415,25 @@ class Gemm:
         return B
 
     # ---------------------------------------------------------------- MLP-block operators
+    # (csrc/binding.cpp reads and checks the tensors: ValueError for a bad one)
+
+    def _follow(self):
+        """Binds the handle to torch's current stream of its device; the handle's address."""
+        stream = _RAW_STREAM[0](self.device)
+        if stream != self._stream:
+            self.set_stream(stream)
+        h = self.handle
+        return (h.value or 0) if h is not None else 0  # (closed: NOT_INITIALIZED)
 
     def run_act(self, A, B, C, transA: int = 0, transB: int = 0, alpha: float = 1.0, act: str = "none", bias=None,
                 residual=None, beta: float = 1.0, z=None, z_scales=None):
         """C <- act(Z) + beta*residual with Z = alpha*op(A)*op(B) + bias (gemm_run_act).
 
         A and B bf16 or float8_e4m3fn, C bf16 or float32, bias (N values) bf16 or float32,
-        residual of C's type (C itself allowed).  Z is left in `z`: bf16, or with z_scales
-        (uint8 [M][ceil(N/32)]) block-scaled E4M3 codes (float8_e4m3fn or uint8)."""
-        M, N = C.shape
-        ep = Epilogue(_act(act))
-        if bias is not None:
-            _vec(bias, N, "bias")
-            ep.bias, ep.bias_type = bias.data_ptr(), _type(bias)
-        if residual is not None:
-            _same(residual, C, "residual", dtype=True)
-            ep.residual, ep.ld_residual, ep.beta = residual.data_ptr(), _ld(residual), beta
-        if z is not None:
-            ep.z_kind, ep.z, ep.ld_z, ep.z_scales, ep.ld_z_scales = _z(z, z_scales, M, N)
-        K = _k_of(A, B, transA, transB, M, N)
-        _on(self.device, A, B, C, bias, residual, z, z_scales)
-        self._bind(C)
-        st = self.lib.gemm_run_act(self.handle, int(transA), int(transB), M, N, K, alpha, A.data_ptr(), _ld(A),
-                                   B.data_ptr(), _ld(B), ctypes.byref(ep), C.data_ptr(), _ld(C), _in_out(A, B, C))
+        residual of C's type (C itself allowed); act one of ACTS.  Z is left in `z`: bf16, or
+        with z_scales (uint8 [M][ceil(N/32)]) block-scaled E4M3 codes (float8_e4m3fn or uint8)."""
+        st = _NATIVE[0].run_act(self._follow(), self.device, A, B, C, transA, transB, alpha, act, bias, residual, beta,
+                                z, z_scales)
         if st != 0:
             raise GemmError("gemm_run_act", st)
         return C
@@ -518,30 +442,14 @@ class Gemm:
                  act: str = "none", dbias=None):
         """C <- (alpha*op(A)*op(B)) * act'(z); dbias (float32, N values) its column sums
         (gemm_run_dact).  z as run_act or act_mx left it."""
-        M, N = C.shape
-        kind, zp, ldz, sp, lds = _z(z, z_scales, M, N)
-        if dbias is not None:
-            _vec(dbias, N, "dbias", f32=True)
-        K = _k_of(A, B, transA, transB, M, N)
-        _on(self.device, A, B, C, z, z_scales, dbias)
-        self._bind(C)
-        st = self.lib.gemm_run_dact(self.handle, int(transA), int(transB), M, N, K, alpha, A.data_ptr(), _ld(A),
-                                    B.data_ptr(), _ld(B), _act(act), kind, zp, ldz, sp, lds, _ptr(dbias),
-                                    C.data_ptr(), _ld(C), _in_out(A, B, C))
+        st = _NATIVE[0].run_dact(self._follow(), self.device, A, B, C, z, z_scales, transA, transB, alpha, act, dbias)
         if st != 0:
             raise GemmError("gemm_run_dact", st)
         return C
 
     def act_mx(self, z, out, codes, scales, act: str = "none"):
         """out <- act(z) and z's block-scaled E4M3 checkpoint (gemm_act_mx); z and out bf16."""
-        M, N = z.shape
-        _bf16(z, "z")
-        _same(out, z, "out", dtype=True)
-        _, qp, ldq, sp, lds = _z(codes, scales, M, N, mx=True)
-        _on(self.device, z, out, codes, scales)
-        self._bind(z)
-        st = self.lib.gemm_act_mx(self.handle, M, N, _act(act), z.data_ptr(), _ld(z), out.data_ptr(), _ld(out), qp,
-                                  ldq, sp, lds)
+        st = _NATIVE[0].act_mx(self._follow(), self.device, z, out, codes, scales, act)
         if st != 0:
             raise GemmError("gemm_act_mx", st)
         return out
@@ -549,18 +457,7 @@ class Gemm:
     def act_grad_mx(self, codes, scales, act: str = "none", dh=None, dz=None, dbias=None, h=None):
         """From the checkpoint: dz <- dh * act'(z), dbias (float32) its column sums, h <- act(z)
         (gemm_act_grad_mx); dh, dz and h bf16, each output optional."""
-        M, N = codes.shape
-        _, qp, ldq, sp, lds = _z(codes, scales, M, N, mx=True)
-        for t, name in ((dh, "dh"), (dz, "dz"), (h, "h")):
-            if t is not None:
-                _bf16(t, name)
-                _same(t, codes, name)
-        if dbias is not None:
-            _vec(dbias, N, "dbias", f32=True)
-        _on(self.device, codes, scales, dh, dz, dbias, h)
-        self._bind(codes)
-        st = self.lib.gemm_act_grad_mx(self.handle, M, N, _act(act), qp, ldq, sp, lds, _ptr(dh), _ld0(dh), _ptr(dz),
-                                       _ld0(dz), _ptr(dbias), _ptr(h), _ld0(h))
+        st = _NATIVE[0].act_grad_mx(self._follow(), self.device, codes, scales, act, dh, dz, dbias, h)
         if st != 0:
             raise GemmError("gemm_act_grad_mx", st)
         return dz
@@ -568,16 +465,7 @@ class Gemm:
     def layernorm(self, x, y, gamma=None, beta=None, eps: float = 1e-5, mean=None, rstd=None):
         """y <- layer norm of x's rows, times gamma plus beta (gemm_layernorm); mean and rstd
         (float32, one per row) receive the statistics."""
-        M, N = x.shape
-        _same(y, x, "y")
-        wt = _weights(gamma, beta, N)
-        for t, name in ((mean, "mean"), (rstd, "rstd")):
-            if t is not None:
-                _vec(t, M, name, f32=True)
-        _on(self.device, x, y, gamma, beta, mean, rstd)
-        self._bind(x)
-        st = self.lib.gemm_layernorm(self.handle, M, N, x.data_ptr(), _ld(x), _type(x), _ptr(gamma), _ptr(beta), wt,
-                                     eps, y.data_ptr(), _ld(y), _type(y), _ptr(mean), _ptr(rstd))
+        st = _NATIVE[0].layernorm(self._follow(), self.device, x, y, gamma, beta, eps, mean, rstd)
         if st != 0:
             raise GemmError("gemm_layernorm", st)
         return y
@@ -585,22 +473,8 @@ class Gemm:
     def layernorm_grad(self, dy, x, mean, rstd, dx, gamma=None, dgamma=None, dbeta=None, residual=None):
         """dx <- the gradient of layernorm at x (+ residual), dgamma and dbeta (float32) those
         of its weights (gemm_layernorm_grad)."""
-        M, N = x.shape
-        _same(dy, x, "dy")
-        _same(dx, x, "dx", dtype=True)
-        if residual is not None:
-            _same(residual, x, "residual", dtype=True)
-        _vec(mean, M, "mean", f32=True)
-        _vec(rstd, M, "rstd", f32=True)
-        for t, name in ((dgamma, "dgamma"), (dbeta, "dbeta")):
-            if t is not None:
-                _vec(t, N, name, f32=True)
-        wt = _weights(gamma, None, N)
-        _on(self.device, dy, x, mean, rstd, dx, gamma, dgamma, dbeta, residual)
-        self._bind(x)
-        st = self.lib.gemm_layernorm_grad(self.handle, M, N, dy.data_ptr(), _ld(dy), _type(dy), x.data_ptr(), _ld(x),
-                                          _type(x), mean.data_ptr(), rstd.data_ptr(), _ptr(gamma), wt, _ptr(residual),
-                                          _ld0(residual), dx.data_ptr(), _ld(dx), _ptr(dgamma), _ptr(dbeta))
+        st = _NATIVE[0].layernorm_grad(self._follow(), self.device, dy, x, mean, rstd, dx, gamma, dgamma, dbeta,
+                                       residual)
         if st != 0:
             raise GemmError("gemm_layernorm_grad", st)
         return dx

@@ -82,6 +82,29 @@ def _compile(entry, incremental: bool = False) -> str:
     return obj
 
 
+BINDING = os.path.join(PKG, "_binding.so")
+
+
+def _build_binding(incremental: bool = False) -> None:
+    """The native part of the Python binding (csrc/binding.cpp): host code against torch's and
+    Python's headers."""
+    src = os.path.join(CSRC, "binding.cpp")
+    if incremental and not _stale("binding.cpp", BINDING):
+        return
+    import sysconfig
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cmd = ["g++", "-O2", "-fPIC", "-shared", "-std=c++17", "-Wall", "-Wno-cast-function-type",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", "-I", INCLUDE, "-isystem",
+           os.path.join(root, "include"), "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"], src, "-o", BINDING + ".tmp", "-L", os.path.join(root, "lib"),
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-ldl"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for binding.cpp:\n{r.stderr}")
+    os.replace(BINDING + ".tmp", BINDING)
+
+
 def _write_build_info() -> None:
     """Records the source state the library was built from (git describe, when the tree is
     a git checkout) beside it; bench.py reports it."""
@@ -102,7 +125,9 @@ def build(verbose: bool = False, incremental: bool = False) -> str:
     # the slowest translation units first, so that they start at once
     order = sorted(SOURCES, key=lambda e: not e[0].startswith("kernel_mfma"))
     with cf.ThreadPoolExecutor(max_workers=min(len(SOURCES), os.cpu_count() or 8)) as ex:
+        binding = ex.submit(_build_binding, incremental)
         objs = list(ex.map(lambda e: _compile(e, incremental), order))
+        binding.result()
     tmp = OUT + ".tmp"
     cmd = [HIPCC, "-shared", "-fPIC", f"--offload-arch={ARCH}", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -78,54 +78,6 @@ __device__ __forceinline__ void pp_load_to_lds_dword(uint32_t lds_base, uint32_t
       : "memory");
 }
 
-// N copies of 1 KiB from one buffer into the LDS blocks at l, l + 1024, ... in one
-// statement (M0 saved once, written before each load, one wait state after each write).
-// TAIL only changes the statement's text (a ragged-K tile), so that the compiler keeps the
-// full-tile and the ragged-tile forms apart instead of merging them with per-copy selects.
-template <int N, bool TAIL>
-__device__ __forceinline__ void pp_copies(uint32_t l, const uint32_t (&o)[N], __amdgpu_buffer_rsrc_t r) {
-  uint32_t saved;
-  if constexpr (N == 1) {
-    asm volatile(
-        "s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_dwordx4 %2, %3, 0 offen lds\n\t"
-        "s_mov_b32 m0, %0 ; %4"
-        : "=&s"(saved)
-        : "s"(l), "v"(o[0]), "s"(r), "i"(TAIL ? 1 : 0)
-        : "memory");
-  } else if constexpr (N == 2) {
-    asm volatile(
-        "s_mov_b32 %0, m0\n\t"
-        "s_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_dwordx4 %2, %4, 0 offen lds\n\t"
-        "s_add_u32 m0, m0, 0x400\n\ts_nop 0\n\tbuffer_load_dwordx4 %3, %4, 0 offen lds\n\t"
-        "s_mov_b32 m0, %0 ; %5"
-        : "=&s"(saved)
-        : "s"(l), "v"(o[0]), "v"(o[1]), "s"(r), "i"(TAIL ? 1 : 0)
-        : "memory");
-  } else if constexpr (N == 3) {
-    asm volatile(
-        "s_mov_b32 %0, m0\n\t"
-        "s_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_dwordx4 %2, %5, 0 offen lds\n\t"
-        "s_add_u32 m0, m0, 0x400\n\ts_nop 0\n\tbuffer_load_dwordx4 %3, %5, 0 offen lds\n\t"
-        "s_add_u32 m0, m0, 0x400\n\ts_nop 0\n\tbuffer_load_dwordx4 %4, %5, 0 offen lds\n\t"
-        "s_mov_b32 m0, %0 ; %6"
-        : "=&s"(saved)
-        : "s"(l), "v"(o[0]), "v"(o[1]), "v"(o[2]), "s"(r), "i"(TAIL ? 1 : 0)
-        : "memory");
-  } else {
-    static_assert(N == 4, "1 to 4 copies per statement");
-    asm volatile(
-        "s_mov_b32 %0, m0\n\t"
-        "s_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_dwordx4 %2, %6, 0 offen lds\n\t"
-        "s_add_u32 m0, m0, 0x400\n\ts_nop 0\n\tbuffer_load_dwordx4 %3, %6, 0 offen lds\n\t"
-        "s_add_u32 m0, m0, 0x400\n\ts_nop 0\n\tbuffer_load_dwordx4 %4, %6, 0 offen lds\n\t"
-        "s_add_u32 m0, m0, 0x400\n\ts_nop 0\n\tbuffer_load_dwordx4 %5, %6, 0 offen lds\n\t"
-        "s_mov_b32 m0, %0 ; %7"
-        : "=&s"(saved)
-        : "s"(l), "v"(o[0]), "v"(o[1]), "v"(o[2]), "v"(o[3]), "s"(r), "i"(TAIL ? 1 : 0)
-        : "memory");
-  }
-}
-
 // Waits for this wave's LDS reads only (its copies stay in flight), then the barrier.
 __device__ __forceinline__ void pp_wait_lds_barrier() {
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
@@ -135,10 +87,6 @@ template <int N>
 __device__ __forceinline__ void pp_wait_vm_barrier() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(N) : "memory");
 }
-
-// E4M3 bytes in LDS, widened to bf16 after each fragment read (with or without block scales)
-template <class C>
-constexpr bool pp_e8 = C::IN == IN_E4M3_LDS || C::IN == IN_MX_LDS;
 
 template <class C>
 struct PingPong {
@@ -192,70 +140,6 @@ struct PingPong {
   // E4M3 fragment is 8 bytes, one read either way)
   static constexpr int A_RD = (C::A_KC || E8) ? 1 : 2, B_RD = (C::B_KC || E8) ? 1 : 2;
 };
-
-// XOR swizzle of the 16-byte chunk index of LDS row r.  bf16 tiles use the shared layout
-// (swz).  E4M3 tiles are read 8 bytes per lane; measured conflict-free with the LDS bank
-// counter on gfx950: K-contiguous rows (ds_read_b64) xor by (r >> 2) for 64-byte rows and
-// (r >> 1) for 128-byte rows, M/N-contiguous rows (ds_read_b64_tr_b8) by the row itself.
-template <class C, bool KC, int CPR>
-__device__ __forceinline__ int pp_swz(int r) {
-  if constexpr (pp_e8<C>) {
-    if constexpr (KC)
-      return (r >> (CPR == 4 ? 2 : 1)) & (CPR - 1);
-    else
-      return r & (CPR - 1);
-  } else {
-    return swz<KC, false, CPR, C::MT>(r);
-  }
-}
-
-// Byte offset, inside one operand tile in LDS, of this lane's part of fragment read h of
-// the MT-row block starting at x0 (M or N index) and K step starting at kbase: the
-// addresses that load_frag computes for bf16 tiles in the XOR-swizzled layout, and the
-// 8-byte reads of E4M3 tiles (lane l: row or column l % 16, K values 8 (l / 16) .. + 7).
-template <class C, bool KC, int RB>
-__device__ __forceinline__ uint32_t pp_frag_off(int x0, int kbase, int lane, int h) {
-  constexpr int CPR = RB / 16;
-  if constexpr (pp_e8<C>) {
-    if constexpr (KC) {
-      const int r = x0 + lane % 16;
-      const int kb = kbase + (lane / 16) * 8;  // bytes = elements
-      return (uint32_t)(r * RB + ((((kb >> 4) ^ pp_swz<C, true, CPR>(r)) << 4) | (kb & 15)));
-    } else {
-      // ds_read_b64_tr_b8: within each group of 16 lanes, lane t gives row t / 2 of eight and
-      // the 8 bytes at column (t % 2) * 8 of a 16-column block; lane i receives column i
-      const int g = lane >> 4, t = lane & 15;
-      const int k = kbase + g * 8 + t / 2;
-      const int xb = x0 + (t % 2) * 8;
-      return (uint32_t)(k * RB + ((((xb >> 4) ^ pp_swz<C, false, CPR>(k)) << 4) | (xb & 15)));
-    }
-  } else if constexpr (KC) {
-    const int r = x0 + lane % C::MT;
-    const int c = (kbase + (lane / C::MT) * C::KPL) * 2 / 16;
-    return (uint32_t)(r * RB + ((c ^ swz<true, false, CPR, C::MT>(r)) << 4));
-  } else {
-    const int g = lane >> 4, s = lane & 15;
-    const int coloff = (C::MT == 32) ? 16 * (g & 1) : 0;
-    const int kgrp = (C::MT == 32) ? (g >> 1) : g;
-    const int xb = (x0 + coloff + (s % 4) * 4) * 2;
-    const int k = kbase + kgrp * C::KPL + h * 4 + s / 4;
-    return (uint32_t)(k * RB + ((((xb >> 4) ^ swz<false, false, CPR, C::MT>(k)) << 4) | (xb & 15)));
-  }
-}
-
-// 8 E4M3 values (bytes in K order) -> 8 bf16 values times `scale`, with the gfx950 packed
-// conversion: exact at unit scale (every E4M3 number, subnormals included, is a bf16
-// number).  The conversion takes its scale as a UE8M0 code: only the exponent field (bits
-// 23-30) of the operand counts, sign and mantissa are ignored, code 0 scales by 2^-127 and
-// code 255 gives NaN (measured on gfx950, and pinned by the block-scaled GPU tests, which
-// compare with a kernel that passes 2^(e - 127) as a float).
-__device__ __forceinline__ bf16x8 pp_widen8(i32x2 v, float scale = 1.0f) {
-  const int w0 = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[0], scale, false));
-  const int w1 = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[0], scale, true));
-  const int w2 = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[1], scale, false));
-  const int w3 = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[1], scale, true));
-  return __builtin_bit_cast(bf16x8, (i32x4){w0, w1, w2, w3});
-}
 
 // Stream-K: bound on the tries of an owner's wait for one partial (each try sleeps a few
 // hundred cycles after a device-scope load, about a microsecond, so the bound is a few

@@ -27,7 +27,8 @@ SOURCES = [("api.cpp", "api", []), ("policy.cpp", "policy", []), ("kernel_simt.h
            ("lds_probe.hip", "lds_probe", []), ("hw_probe.hip", "hw_probe", []),
            ("quantize_mx.hip", "quantize_mx", []),
            ("blas3.cpp", "blas3", []), ("blas3_kernels.hip", "blas3_kernels", []),
-           ("mlp.cpp", "mlp", []), ("act_mx.hip", "act_mx", []), ("layernorm.hip", "layernorm", [])] + [
+           ("mlp.cpp", "mlp", []), ("act_mx.hip", "act_mx", []), ("layernorm.hip", "layernorm", []),
+           ("kernel_skinny.hip", "kernel_skinny", [])] + [
     ("kernel_mfma.hip", f"kernel_mfma_{ta}{tb}", [f"-DDBGEMM_DMA_TA={ta}", f"-DDBGEMM_DMA_TB={tb}"])
     for ta in (0, 1) for tb in (0, 1)] + [
     ("kernel_mfma_dma.hip", f"kernel_mfma_dma_{ta}{tb}_p{part}",

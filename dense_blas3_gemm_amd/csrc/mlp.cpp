@@ -111,14 +111,19 @@ bool run_fused(const HandleView& v, GemmEpArgs a, int transA, int transB, int dt
   if (a.K == 0 || a.alpha == 0.f || a.N % 8 != 0) return false;
   Problem pr = gemm_problem(transA, transB, a.M, a.N, a.K, a.A, a.lda, a.B, a.ldb, a.C, a.ldc, dtype);
   if (!pr.fast_ok) return false;
+  a.in_fp8 = pr.in_fp8;
+  a.transA = transA;
+  a.transB = transB;
+  if (a.M <= skinny_rows(a.in_fp8, transA, transB)) {
+    a.ep.colsum = dbias;
+    *st = status(launch_skinny(a, v.stream));
+    return true;
+  }
   pr.ep = true;
   int sp = 1;
   const int64_t split_floats = v.ws ? (int64_t)(kPartBytes / sizeof(float)) : 0;
   const Policy& p = policy_at(policy_select(pr, v.cu_count, split_floats, &sp));
   if (p.kind != KIND_MFMA) return false;
-  a.in_fp8 = pr.in_fp8;
-  a.transA = transA;
-  a.transB = transB;
   a.tiles_m = (a.M + p.BM - 1) / p.BM;
   a.tiles_n = (a.N + p.BN - 1) / p.BN;
   a.group = p.group;

@@ -51,6 +51,11 @@ DBGEMM_EP_DECL(10)
 DBGEMM_EP_DECL(11)
 #undef DBGEMM_EP_DECL
 
+// Products of a few rows (at most skinny_rows), N a multiple of 8, operands as the MFMA kernels
+// take them; ep.colsum, when set, receives the column sums themselves.
+int skinny_rows(int in_fp8, int transA, int transB);
+hipError_t launch_skinny(const GemmEpArgs& a, hipStream_t s);
+
 // ---- launchers (they return hipSuccess or the launch error)
 
 // Epilogue of a product held in fp32: a.ws is rows [0, M) of alpha * op(A) op(B) with row

@@ -25,7 +25,9 @@ RowGrid row_grid(int64_t rows, int64_t cols, int64_t max_row_wgs, int max_parts)
   while (tx < (unsigned)kThreads && (int64_t)tx < chunks) tx *= 2;
   const unsigned ty = kThreads / tx;
   const int64_t gx = (chunks + tx - 1) / tx;
-  int64_t gy = (rows + ty - 1) / ty;
+  // with partial rows, eight rows to a thread at least: a partial row is written and read again
+  const int64_t each = (int64_t)ty * (max_parts > 0 ? 8 : 1);
+  int64_t gy = (rows + each - 1) / each;
   const int64_t cap = max_row_wgs / gx > 1 ? max_row_wgs / gx : 1;
   if (gy > cap) gy = cap;
   if (gy > 65535) gy = 65535;
@@ -60,27 +62,37 @@ __global__ __launch_bounds__(kThreads) void ep_rows_kernel(GemmEpArgs a, int64_t
   put_partial(a.ep.colsum, a.N, n, cs);
 }
 
-// Sums of the partial rows: 64 columns to a workgroup, the rows dealt to 16 waves, their sums
-// added in wave order.  blockIdx.y: which of the two sets of columns of a row.
-__global__ __launch_bounds__(1024) void colsum_kernel(const float* src, int parts, int64_t ld, int64_t cols,
-                                                      float* out0, float* out1, int accumulate) {
-  __shared__ float s[16][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t n = (int64_t)blockIdx.x * 64 + lane;
+// Sums of the partial rows: 64 columns to a workgroup, four to a thread, the rows dealt to 64
+// groups of 16 lanes, whose sums are added in order through LDS.  blockIdx.y: which of the two
+// sets of columns of a row.
+constexpr int kSumGroups = 64;
+__global__ __launch_bounds__(16 * kSumGroups) void colsum_kernel(const float* src, int parts, int64_t ld, int64_t cols,
+                                                                 float* out0, float* out1, int accumulate) {
+  __shared__ float s[kSumGroups][64 + 4];
   float* out = blockIdx.y ? out1 : out0;
   if (!out) return;
-  src += blockIdx.y * cols;
-  float v = 0.f;
-  if (n < cols)
-    for (int p = wave; p < parts; p += 16) v += src[(int64_t)p * ld + n];
-  s[wave][lane] = v;
-  __syncthreads();
-  if (wave == 0 && n < cols) {
-    float t = accumulate ? out[n] : 0.f;
+  const int l = threadIdx.x & 15, g = threadIdx.x >> 4;
+  const int64_t n = (int64_t)blockIdx.x * 64 + l * 4;
+  const float* p = src + blockIdx.y * cols + n;
+  ep_f32x4 v = {0.f, 0.f, 0.f, 0.f};
+  if (n + 4 <= cols) {
+#pragma unroll 4
+    for (int r = g; r < parts; r += kSumGroups) v += *(const ep_f32x4_u*)(p + (int64_t)r * ld);
+  } else {
+    for (int r = g; r < parts; r += kSumGroups)
 #pragma unroll
-    for (int i = 0; i < 16; ++i) t += s[i][lane];
-    out[n] = t;
+      for (int i = 0; i < 4; ++i)
+        if (n + i < cols) v[i] += p[(int64_t)r * ld + i];
   }
+  *(ep_f32x4*)&s[g][l * 4] = v;
+  __syncthreads();
+  // 16 threads to a column: four groups each, then over the 16
+  const int c = threadIdx.x >> 4;
+  float t = s[4 * l][c] + s[4 * l + 1][c] + s[4 * l + 2][c] + s[4 * l + 3][c];
+#pragma unroll
+  for (int o = 1; o < 16; o <<= 1) t += __shfl_xor(t, o);
+  const int64_t m = (int64_t)blockIdx.x * 64 + c;
+  if (l == 0 && m < cols) out[m] = accumulate ? out[m] + t : t;
 }
 
 __global__ __launch_bounds__(kThreads) void act_mx_kernel(int64_t rows, int64_t cols, int act, const uint16_t* z,
@@ -102,6 +114,8 @@ __global__ __launch_bounds__(kThreads) void act_mx_kernel(int64_t rows, int64_t 
   }
 }
 
+// Backward from the checkpoint, kAhead rows of a thread at a time: their loads go out together.
+constexpr int kAhead = 4;
 __global__ __launch_bounds__(kThreads) void act_grad_mx_kernel(int64_t rows, int64_t cols, int act, const uint8_t* q,
                                                                int64_t ldq, const uint8_t* sc, int64_t ldsc,
                                                                const uint16_t* dh, int64_t lddh, uint16_t* dz,
@@ -110,29 +124,52 @@ __global__ __launch_bounds__(kThreads) void act_grad_mx_kernel(int64_t rows, int
   const int64_t n = k * 8;
   if (n >= cols) return;
   const int nv = cols - n < 8 ? (int)(cols - n) : 8;
+  const int64_t step = (int64_t)gridDim.y * blockDim.y;
   float cs[8] = {};
-  for (int64_t m = (int64_t)blockIdx.y * blockDim.y + threadIdx.y; m < rows; m += (int64_t)gridDim.y * blockDim.y) {
-    float z[8];
-    ep_load_mx(q + m * ldq + n, nv, sc[m * ldsc + (n >> 5)], z);
-    if (dh) {
-      float d[8];
-      ep_load8(dh + m * lddh + n, nv, d);
-      ep_with_act(act, [&](auto ac) EP_INLINE {
+  ep_with_act(act, [&](auto ac) EP_INLINE {
+    constexpr int ACT = decltype(ac)::value;
+    for (int64_t m0 = (int64_t)blockIdx.y * blockDim.y + threadIdx.y; m0 < rows; m0 += kAhead * step) {
+      ep_u32x4 codes[kAhead], d[kAhead];  // codes and scale, dh
 #pragma unroll
-        for (int i = 0; i < 8; ++i) d[i] *= ep_slope<decltype(ac)::value>(z[i]);
-      });
+      for (int j = 0; j < kAhead; ++j) {
+        const int64_t m = m0 + j * step;
+        const bool live = m < rows;
+        codes[j] = d[j] = (ep_u32x4){0, 0, 0, 0};
+        if (live && nv == 8) {
+          const ep_u32x2 w = *(const ep_u32x2_u*)(q + m * ldq + n);
+          codes[j] = (ep_u32x4){w[0], w[1], sc[m * ldsc + (n >> 5)], 0};
+          if (dh) d[j] = *(const ep_u32x4_2*)(dh + m * lddh + n);
+        } else if (live) {
+          codes[j] = ep_raw_part<1>(q + m * ldq + n, nv, 0);
+          codes[j][2] = sc[m * ldsc + (n >> 5)];
+          if (dh) d[j] = ep_raw_part<2>(dh + m * lddh + n, nv, 0);
+        }
+      }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) cs[i] += i < nv ? d[i] : 0.f;
-      if (dz) ep_store8<false>(dz + m * lddz + n, nv, d);
+      for (int j = 0; j < kAhead; ++j) {
+        const int64_t m = m0 + j * step;
+        if (m >= rows) break;
+        float z[8], g[8];
+        ep_codes8(codes[j][0], codes[j][1], codes[j][2], z);
+        if (dh) {
+          EpRaw r;
+          r.lo = d[j];
+          ep_raw_bf16(r, g);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            g[i] *= ep_slope<ACT>(z[i]);
+            cs[i] += i < nv ? g[i] : 0.f;
+          }
+          if (dz) ep_store8<true>(dz + m * lddz + n, nv, g);
+        }
+        if (h) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) z[i] = ep_act<ACT>(z[i]);
+          ep_store8<true>(h + m * ldh + n, nv, z);
+        }
+      }
     }
-    if (h) {
-      ep_with_act(act, [&](auto ac) EP_INLINE {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) z[i] = ep_act<decltype(ac)::value>(z[i]);
-      });
-      ep_store8<false>(h + m * ldh + n, nv, z);
-    }
-  }
+  });
   put_partial(part, cols, n, cs);
 }
 
@@ -148,7 +185,7 @@ hipError_t launch_ep_rows(const GemmEpArgs& a, int64_t ldw, int max_parts, int* 
 hipError_t launch_colsum(const float* src, int parts, int64_t ld, int64_t cols, float* out0, float* out1,
                          int accumulate, hipStream_t s) {
   if (cols == 0) return hipSuccess;
-  hipLaunchKernelGGL(colsum_kernel, dim3((unsigned)((cols + 63) / 64), out1 ? 2 : 1), dim3(1024), 0, s, src, parts, ld,
+  hipLaunchKernelGGL(colsum_kernel, dim3((unsigned)((cols + 63) / 64), out1 ? 2 : 1), dim3(16 * kSumGroups), 0, s, src, parts, ld,
                      cols, out0, out1, accumulate);
   return hipGetLastError();
 }

@@ -2,7 +2,7 @@
 // behind in block-scaled E4M3, the backward pass that reads it, the epilogue of a product
 // held in fp32, and the column sums that they share (bias gradients).
 //
-// Rows are walked by workgroups of 256 threads, 8 columns to a thread: a thread keeps its
+// Rows are walked by workgroups of up to 256 threads, 8 columns to a thread: a thread keeps its
 // columns over the rows that its workgroup takes, so a column sum is one register per
 // column, written once per thread as a partial row and added up by a second launch in a
 // fixed order (no atomics: the same bits every run).
@@ -13,42 +13,55 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Threads along the columns (a power of two, whole blocks of 32 columns: 4 threads) and rows
-// of threads of a workgroup, and the grid.
+// Threads along the columns (whole blocks of 32 columns: 4 neighbouring threads), rows of
+// threads of a workgroup, and the grid: at most max_wgs workgroups.  With partial rows (at most
+// max_parts, one per row of workgroups) a workgroup takes 16 rows or more, as long as that
+// leaves 128 workgroups: a partial row is written and read again.
 struct RowGrid {
   dim3 grid, block;
-  int parts;  // rows of threads over the whole grid along the rows
 };
-RowGrid row_grid(int64_t rows, int64_t cols, int64_t max_row_wgs, int max_parts) {
+RowGrid row_grid(int64_t rows, int64_t cols, int64_t max_wgs, int max_parts) {
   const int64_t chunks = (cols + 31) / 32 * 4;
-  unsigned tx = 4;
-  while (tx < (unsigned)kThreads && (int64_t)tx < chunks) tx *= 2;
-  const unsigned ty = kThreads / tx;
-  const int64_t gx = (chunks + tx - 1) / tx;
-  // with partial rows, eight rows to a thread at least: a partial row is written and read again
-  const int64_t each = (int64_t)ty * (max_parts > 0 ? 8 : 1);
-  int64_t gy = (rows + each - 1) / each;
-  const int64_t cap = max_row_wgs / gx > 1 ? max_row_wgs / gx : 1;
+  const int64_t gx = (chunks + kThreads - 1) / kThreads;
+  const int64_t tx = ((chunks + gx - 1) / gx + 3) / 4 * 4, ty = kThreads / tx;
+  const int64_t all = (rows + ty - 1) / ty;  // one row to a thread
+  int64_t gy = all;
+  if (max_parts > 0) {
+    const int64_t eight = (rows + 7) / 8, some = (512 + gx - 1) / gx;
+    if (gy > eight && gy > some) gy = eight > some ? eight : some;
+    if (gy > max_parts) gy = max_parts;
+    if (all <= 4) gy = 1;  // (few rows: no second launch)
+  }
+  const int64_t cap = max_wgs / gx > 1 ? max_wgs / gx : 1;
   if (gy > cap) gy = cap;
   if (gy > 65535) gy = 65535;
-  if (max_parts > 0 && gy > max_parts / (int64_t)ty) gy = max_parts / (int64_t)ty > 1 ? max_parts / (int64_t)ty : 1;
   if (gy < 1) gy = 1;
-  return {dim3((unsigned)gx, (unsigned)gy), dim3(tx, ty), (int)(gy * ty)};
+  return {dim3((unsigned)gx, (unsigned)gy), dim3((unsigned)tx, (unsigned)ty)};
 }
 
-// this thread's partial column sums, one row of `part` per row of threads
-__device__ __forceinline__ void put_partial(float* part, int64_t cols, int64_t n, const float (&cs)[8]) {
-  if (!part || n >= cols) return;
-  const int64_t p = (int64_t)blockIdx.y * blockDim.y + threadIdx.y;
-  ep_store8<false>(part + p * cols + n, cols - n < 8 ? (int)(cols - n) : 8, cs);
+// The workgroup's column sums: this thread's eight, added over the rows of threads through LDS,
+// as one row of `part` per row of workgroups.  Every thread calls it (n >= cols: no columns).
+__device__ __forceinline__ void put_partial(float* part, int64_t cols, int64_t n, float (&cs)[8]) {
+  __shared__ float s[8][kThreads];
+  if (!part) return;
+  if (blockDim.y > 1) {
+    const int t = threadIdx.y * blockDim.x + threadIdx.x;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[i][t] = cs[i];
+    __syncthreads();
+    if (threadIdx.y > 0) return;
+    for (unsigned y = 1; y < blockDim.y; ++y)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) cs[i] += s[i][y * blockDim.x + t];
+  }
+  if (n < cols) ep_store8<false>(part + (int64_t)blockIdx.y * cols + n, cols - n < 8 ? (int)(cols - n) : 8, cs);
 }
 
 // Epilogue of a product in fp32 (the path of operands that the fused kernels do not take).
 __global__ __launch_bounds__(kThreads) void ep_rows_kernel(GemmEpArgs a, int64_t ldw) {
-  const int64_t k = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (k >= ((int64_t)a.N + 31) / 32 * 4) return;  // four lanes leave together
-  const int n = (int)(k * 8);
-  const int nv = a.N - n < 8 ? (a.N > n ? a.N - n : 0) : 8;
+  const int64_t n64 = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * 8;
+  const int n = n64 < a.N ? (int)n64 : a.N;  // (a thread past the columns has none)
+  const int nv = a.N - n < 8 ? a.N - n : 8;
   float cs[8] = {}, b[8];
   ep_bias8(a, n, nv, b);
   ep_dispatch(a.ep, [&](auto gc, auto ac) EP_INLINE {
@@ -59,7 +72,7 @@ __global__ __launch_bounds__(kThreads) void ep_rows_kernel(GemmEpArgs a, int64_t
       ep_finish8<false, decltype(gc)::value, decltype(ac)::value, true>(a, w, r, b, m, n, nv, cs);
     }
   });
-  put_partial(a.ep.colsum, a.N, n, cs);
+  put_partial(a.ep.colsum, a.N, n64, cs);
 }
 
 // Sums of the partial rows: 64 columns to a workgroup, four to a thread, the rows dealt to 64
@@ -120,10 +133,9 @@ __global__ __launch_bounds__(kThreads) void act_grad_mx_kernel(int64_t rows, int
                                                                int64_t ldq, const uint8_t* sc, int64_t ldsc,
                                                                const uint16_t* dh, int64_t lddh, uint16_t* dz,
                                                                int64_t lddz, uint16_t* h, int64_t ldh, float* part) {
-  const int64_t k = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  const int64_t n = k * 8;
-  if (n >= cols) return;
-  const int nv = cols - n < 8 ? (int)(cols - n) : 8;
+  const int64_t n = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * 8;
+  const int nv = cols - n < 8 ? (cols > n ? (int)(cols - n) : 0) : 8;
+  if (nv == 0) rows = 0;  // (a thread past the columns)
   const int64_t step = (int64_t)gridDim.y * blockDim.y;
   float cs[8] = {};
   ep_with_act(act, [&](auto ac) EP_INLINE {
@@ -177,7 +189,7 @@ __global__ __launch_bounds__(kThreads) void act_grad_mx_kernel(int64_t rows, int
 
 hipError_t launch_ep_rows(const GemmEpArgs& a, int64_t ldw, int max_parts, int* parts, hipStream_t s) {
   const RowGrid g = row_grid(a.M, a.N, 2048, a.ep.colsum ? max_parts : 0);
-  *parts = g.parts;
+  *parts = (int)g.grid.y;
   hipLaunchKernelGGL(ep_rows_kernel, g.grid, g.block, 0, s, a, ldw);
   return hipGetLastError();
 }
@@ -200,9 +212,11 @@ hipError_t launch_act_mx(int64_t rows, int64_t cols, int act, const void* z, int
 
 hipError_t launch_act_grad_mx(int64_t rows, int64_t cols, int act, const uint8_t* q, int64_t ldq, const uint8_t* sc,
                               int64_t ldsc, const void* dh, int64_t lddh, void* dz, int64_t lddz, void* h,
-                              int64_t ldh, float* colsum, int max_parts, int* parts, hipStream_t s) {
-  const RowGrid g = row_grid(rows, cols, 2048, colsum ? max_parts : 0);
-  *parts = g.parts;
+                              int64_t ldh, float* dbias, float* part, int max_parts, int* parts, hipStream_t s) {
+  const RowGrid g = row_grid(rows, cols, 2048, dbias ? max_parts : 0);
+  // a single row of workgroups has the sums themselves
+  *parts = g.grid.y > 1 ? (int)g.grid.y : 0;
+  float* colsum = !dbias ? nullptr : *parts ? part : dbias;
   hipLaunchKernelGGL(act_grad_mx_kernel, g.grid, g.block, 0, s, rows, cols, act, q, ldq, sc, ldsc,
                      (const uint16_t*)dh, lddh, (uint16_t*)dz, lddz, (uint16_t*)h, ldh, colsum);
   return hipGetLastError();

@@ -24,6 +24,13 @@ __device__ __forceinline__ float wave_sum(float v) {
   for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
   return v;
 }
+// over the 8, 16 or 32 lanes of a part of a wave
+__device__ __forceinline__ float lanes_sum(float v, int lanes) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1)
+    if (o < lanes) v += __shfl_xor(v, o);
+  return v;
+}
 
 // Eight elements of a row as they come from memory; the loads of the next rows are in flight
 // in this form while a row is worked on.
@@ -57,14 +64,15 @@ __device__ __forceinline__ void raw_load(Raw8<T>& r, const T* p, int nv) {
   }
 }
 
-// ---- the row kernels.  A team of blockDim.x threads (whole waves) holds a row in registers:
+// ---- the row kernels.  A team of blockDim.x threads (whole waves, or for narrow rows 8, 16 or
+// 32 lanes of one) holds a row in registers:
 // thread t its columns 8 (t + c blockDim.x) .. + 7 for c < CPT.  blockDim.y teams make up a
 // workgroup, and a workgroup walks the rows with R rows per team at a time: one exchange over
 // the waves of a team serves R rows, the weights stay in registers, and the next R rows'
 // loads are issued before the present rows' sums are waited for.  Wide rows (CPT = 4) have no
 // registers for either: the weights are read where they are used and the rows one by one.
 struct Team {
-  int t, T, waves, wave;  // thread and wave within the team
+  int t, T, waves, wave;  // thread and wave within the team (waves: 0 for part of a wave)
   int first_wave;         // the team's first wave within the workgroup
   __device__ Team()
       : t(threadIdx.x), T(blockDim.x), waves(blockDim.x >> 6), wave(threadIdx.x >> 6),
@@ -76,9 +84,14 @@ struct Team {
 // apart.  Every team of the workgroup calls it together.
 template <int V>
 __device__ __forceinline__ void team_sum(const Team& m, float (&v)[V], float* s, int& half) {
+  if (m.waves == 0) {  // (uniform over the workgroup, and so is the next)
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = lanes_sum(v[i], m.T);
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < V; ++i) v[i] = wave_sum(v[i]);
-  if (m.waves == 1) return;  // (uniform over the workgroup)
+  if (m.waves == 1) return;
   float* h = s + half * 16 * V;
   half ^= 1;
   if ((m.t & 63) == 0)
@@ -304,7 +317,9 @@ __global__ __launch_bounds__(MAXT) void layernorm_grad_kernel(NormArgs a) {
     // the teams' sums, one set of eight columns at a time: team y > 0 leaves its own in LDS
     // and team 0 adds them in order
     __shared__ float t8[8 * 1024];
-    float* out = a.part + (int64_t)blockIdx.x * 2 * a.cols;
+    // (a single workgroup has the sums themselves)
+    float* const out[2] = {gridDim.x > 1 ? a.part + (int64_t)blockIdx.x * 2 * a.cols : a.dgamma,
+                           gridDim.x > 1 ? a.part + ((int64_t)blockIdx.x * 2 + 1) * a.cols : a.dbeta};
     auto put = [&](float (&v)[8], int c, int set) {
       if (blockDim.y > 1) {
         __syncthreads();
@@ -317,7 +332,7 @@ __global__ __launch_bounds__(MAXT) void layernorm_grad_kernel(NormArgs a) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] += t8[i * 1024 + k * m.T + m.t];
       }
-      if (threadIdx.y == 0 && nv[c] > 0) ep_store8<false>(out + (int64_t)set * a.cols + col[c], nv[c], v);
+      if (threadIdx.y == 0 && nv[c] > 0 && out[set]) ep_store8<false>(out[set] + col[c], nv[c], v);
     };
 #pragma unroll
     for (int c = 0; c < CPT; ++c) {
@@ -416,13 +431,20 @@ __global__ __launch_bounds__(256) void layernorm_dw_kernel(NormArgs a) {
       db[i] += d.get(i);
     }
   }
-  float* out = a.part + (int64_t)blockIdx.y * 2 * a.cols + col;
-  ep_store8<false>(out, nv, dg);
-  ep_store8<false>(out + a.cols, nv, db);
+  const bool one = gridDim.y == 1;  // (the sums themselves)
+  float* og = one ? a.dgamma : a.part + (int64_t)blockIdx.y * 2 * a.cols;
+  float* ob = one ? a.dbeta : a.part + ((int64_t)blockIdx.y * 2 + 1) * a.cols;
+  if (og) ep_store8<false>(og + col, nv, dg);
+  if (ob) ep_store8<false>(ob + col, nv, db);
 }
 
-// Threads of a team for rows of `cols` columns at `cpt` chunks of 8 to a thread: whole waves.
-unsigned team_threads(int64_t cols, int cpt) { return (unsigned)((cols + 512 * cpt - 1) / (512 * cpt)) * 64; }
+// Threads of a team for rows of `cols` columns at `cpt` chunks of 8 to a thread: whole waves, or
+// as few lanes of one as do (8 at least).
+unsigned team_threads(int64_t cols, int cpt) {
+  const int64_t t = (cols + 8 * cpt - 1) / (8 * cpt);
+  if (t > 32) return (unsigned)((t + 63) / 64) * 64;
+  return t > 16 ? 32 : t > 8 ? 16 : 8;
+}
 
 template <class X, class Y, int CPT, int R, int MAXT>
 hipError_t fwd(const NormArgs& a, hipStream_t s) {
@@ -441,15 +463,18 @@ hipError_t grad(const NormArgs& a, int max_parts, int* parts, hipStream_t s) {
   constexpr unsigned wg = 512;
   const unsigned T = team_threads(a.cols, CPT);
   unsigned teams = T < wg ? wg / T : 1;
-  while (teams > 1 && (int64_t)teams * R * 256 > a.rows) --teams;  // few rows: spread them over the CUs
+  const bool few = SUMS && a.rows <= (int64_t)teams * R * 2;  // two rounds of one workgroup, no second launch
+  // else spread the rows over the CUs (a workgroup stays whole waves)
+  while (!few && teams > 1 && teams * T > 64 && (int64_t)teams * R * 256 > a.rows) teams = (teams + 1) / 2;
   const int64_t need = (a.rows + (int64_t)teams * R - 1) / ((int64_t)teams * R);
   // With the weights' sums one workgroup to a CU: a partial row more per CU costs more (its
   // write and its read) than a second workgroup's overlap gains, 128.4 against 136.6 us at
   // 16384 x 5120.  Narrow rows (one chunk a thread, no spills at 128 registers) take two.
   int64_t most = 256 * (SUMS && CPT > 1 ? 1 : 1024 / (T * teams) ? 1024 / (T * teams) : 1);
   if (SUMS && most > max_parts) most = max_parts;
+  if (few) most = 1;
   const unsigned n = (unsigned)(need < most ? need : most);
-  *parts = (int)n;
+  *parts = SUMS && n > 1 ? (int)n : 0;
   hipLaunchKernelGGL((layernorm_grad_kernel<X, Y, CPT, R, MAXT, SUMS>), dim3(n), dim3(T, teams), 0, s, a);
   return hipGetLastError();
 }
@@ -508,7 +533,7 @@ hipError_t grad_xy(const NormArgs& a, int max_parts, int* parts, hipStream_t s) 
   if (gy > max_parts) gy = max_parts;
   if (gy > a.rows) gy = a.rows;
   if (gy < 1) gy = 1;
-  *parts = (int)gy;
+  *parts = gy > 1 ? (int)gy : 0;
   hipLaunchKernelGGL((layernorm_dw_kernel<X, Y>), dim3((unsigned)gx, (unsigned)gy), dim3(256), 0, s, a);
   return hipGetLastError();
 }

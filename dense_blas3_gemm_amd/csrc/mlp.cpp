@@ -20,7 +20,7 @@ namespace {
 // The workspace: partial column sums, or a split product's partial tiles, first; behind them a
 // product in fp32, or the column sums of a product with an epilogue.
 constexpr size_t kPartBytes = (size_t)64 << 20;
-constexpr int kMaxParts = 512;
+constexpr int kMaxParts = 1024;
 
 // Makes the handle's device current for its lifetime.
 struct OnDevice {
@@ -281,8 +281,8 @@ gemm_status_t gemm_act_grad_mx(gemm_handle_t h, int64_t rows, int64_t cols, int 
   if (mp < 1) return GEMM_STATUS_NOT_SUPPORTED;
   int parts = 0;
   hipError_t e = launch_act_grad_mx(rows, cols, act, (const uint8_t*)codes, ld_codes, scales, ld_scales, dout, ld_dout,
-                                    dz, ld_dz, out, ld_out, dbias ? (float*)v.ws : nullptr, mp, &parts, v.stream);
-  if (e == hipSuccess && dbias) e = launch_colsum((const float*)v.ws, parts, cols, cols, dbias, nullptr, 0, v.stream);
+                                    dz, ld_dz, out, ld_out, dbias, (float*)v.ws, mp, &parts, v.stream);
+  if (e == hipSuccess && parts) e = launch_colsum((const float*)v.ws, parts, cols, cols, dbias, nullptr, 0, v.stream);
   return status(e);
 }
 
@@ -358,9 +358,11 @@ gemm_status_t gemm_layernorm_grad(gemm_handle_t h, int64_t rows, int64_t cols, c
   a.dr = residual;
   a.lddr = ld_residual;
   a.part = sums ? part : nullptr;
+  a.dgamma = dgamma;
+  a.dbeta = dbeta;
   int parts = 0;
   hipError_t e = launch_layernorm_grad(a, mp, &parts, v.stream);
-  if (e == hipSuccess && sums) e = add_up(parts);
+  if (e == hipSuccess && parts) e = add_up(parts);
   return status(e);
 }
 

@@ -72,10 +72,11 @@ hipError_t launch_colsum(const float* src, int parts, int64_t ld, int64_t cols, 
 // H <- act(Z) (bf16) and Z's E4M3 codes and scales, Z bf16.
 hipError_t launch_act_mx(int64_t rows, int64_t cols, int act, const void* z, int64_t ldz, void* h, int64_t ldh,
                          uint8_t* q, int64_t ldq, uint8_t* sc, int64_t ldsc, hipStream_t s);
-// dZ <- dH * act'(Z), H <- act(Z) from Z's codes (dh with dz, h, colsum each optional).
+// dZ <- dH * act'(Z), H <- act(Z) from Z's codes (dh with dz, h, dbias each optional).  *parts
+// receives the partial rows of dbias written to `part` (at most max_parts); 0: dbias is done.
 hipError_t launch_act_grad_mx(int64_t rows, int64_t cols, int act, const uint8_t* q, int64_t ldq, const uint8_t* sc,
                               int64_t ldsc, const void* dh, int64_t lddh, void* dz, int64_t lddz, void* h,
-                              int64_t ldh, float* colsum, int max_parts, int* parts, hipStream_t s);
+                              int64_t ldh, float* dbias, float* part, int max_parts, int* parts, hipStream_t s);
 
 struct NormArgs {
   int64_t rows;
@@ -97,9 +98,12 @@ struct NormArgs {
   const void* dr;  // grad: added to dx (x's type), or null
   int64_t lddr;
   float* part;  // grad: partial sums of dgamma and dbeta, [part][2][cols], or null
+  float* dgamma;  // grad: the sums themselves, either may be null
+  float* dbeta;
 };
 hipError_t launch_layernorm(const NormArgs& a, hipStream_t s);
-// *parts receives the number of partial rows written to a.part (at most max_parts).
+// *parts receives the number of partial rows written to a.part (at most max_parts); 0: a.dgamma
+// and a.dbeta are done.
 hipError_t launch_layernorm_grad(const NormArgs& a, int max_parts, int* parts, hipStream_t s);
 
 }  // namespace dbgemm

@@ -155,6 +155,10 @@ int policy_select(const Problem& pr, int cu_count, int64_t ws_floats, int* split
       // tiles of about K (1 - r/R), so the rounds add up to (R + 1) / 2 full-K rounds
       if (pr.kband) t *= (rounds + 1.0) / (2.0 * rounds);
       if (sp > 1) t += (1.5 + 0.75 * sp) * kUnitsPerUs;
+      // the partial tiles' way through memory and back, at 4 TB/s: with an epilogue, where the
+      // choice is between tiles that write C once, it decides (512 x 5120 x 5120: 256 x 128
+      // tiles split in two 52 us, 128 x 128 unsplit 39)
+      if (sp > 1 && pr.ep) t += tiles * sp * p.BM * p.BN * 8.0 / 4.0e6 * kUnitsPerUs;
       if (!have || t < best_t * 0.999) {
         best = i;
         best_t = t;

@@ -36,9 +36,9 @@ SOURCES = [("api.cpp", "api", []), ("policy.cpp", "policy", []), ("kernel_simt.h
     for ta in (0, 1) for tb in (0, 1) for part in (0, 1)] + [
     ("kernel_pingpong.hip", f"kernel_pingpong_{ta}{tb}", [f"-DDBGEMM_DMA_TA={ta}", f"-DDBGEMM_DMA_TB={tb}"])
     for ta in (0, 1) for tb in (0, 1)] + [
-    # the same three kernels for products with an epilogue
+    # the same two kernels for products with an epilogue
     (f"{k}.hip", f"{k}_ep_{ta}{tb}", [f"-DDBGEMM_DMA_TA={ta}", f"-DDBGEMM_DMA_TB={tb}", "-DDBGEMM_EPILOGUE"])
-    for k in ("kernel_pingpong", "kernel_mfma_dma", "kernel_mfma") for ta in (0, 1) for tb in (0, 1)]
+    for k in ("kernel_pingpong", "kernel_mfma_dma") for ta in (0, 1) for tb in (0, 1)]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 FLAGS = ["-O3", "-fPIC", "-std=c++17", f"--offload-arch={ARCH}", "-Xclang", "-target-feature",

@@ -123,7 +123,7 @@ __global__ __launch_bounds__(kThreads) void act_mx_kernel(int64_t rows, int64_t 
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = ep_act<decltype(ac)::value>(v[i]);
     });
-    ep_store8<false>(h + m * ldh + n, nv, v);
+    ep_store8<true>(h + m * ldh + n, nv, v);
   }
 }
 

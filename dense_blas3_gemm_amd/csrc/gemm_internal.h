@@ -113,6 +113,7 @@ struct Policy {
   float efficiency;  // relative per-CU throughput used by the wave-time model
   int k_contig_only;  // serves only A [M][K] with B [N][K] (transA = 0, transB = 1)
   int a_kc_only;      // serves only A [M][K] (transA = 0)
+  int ep_only;        // serves only products with an epilogue
 };
 
 // The table entries whose kernels are also built with an epilogue behind the product
@@ -120,7 +121,7 @@ struct Policy {
 constexpr bool has_epilogue(int pipe, int in_mode, int BM, int BN, int BK, int MT, int k_contig_only, float eff) {
   return eff > 0.f && MT == 16 && !k_contig_only &&
          ((pipe == 2 && BM == 256 && ((in_mode == 0 && BK == 32) || (in_mode == 5 && BK == 128))) ||
-          (pipe == 1 && in_mode == 0 && BN <= 128) || (pipe == 0 && in_mode == 1 && BM <= 128));
+          (pipe == 1 && (in_mode == 0 || in_mode == 5) && BN <= 128));
 }
 
 // Launchers (one per kernel family).  They return hipSuccess or the launch error.

@@ -24,18 +24,9 @@
 // The MFMA is issued with the B fragment as its first operand, so each lane ends
 // up holding four consecutive columns of one row of C (a row-major friendly store).
 #include "mfma_common.h"
-#ifdef DBGEMM_EPILOGUE  // the kernels of products with an epilogue
-#include "epilogue_tile.h"
-#endif
 
 namespace dbgemm {
 namespace {
-
-#ifdef DBGEMM_EPILOGUE
-using KernelArgs = GemmEpArgs;
-#else
-using KernelArgs = GemmArgs;
-#endif
 
 // Register-staged pipeline: chunk geometry of the global -> register -> LDS copy.
 template <class C>
@@ -47,7 +38,7 @@ struct Staged {
 };
 
 template <class C>
-__global__ __launch_bounds__(C::THREADS) void gemm_mfma_kernel(KernelArgs a) {
+__global__ __launch_bounds__(C::THREADS) void gemm_mfma_kernel(GemmArgs a) {
   (void)sizeof(Staged<C>);
   __shared__ __attribute__((aligned(1024))) char smem[C::STAGES * C::STAGE_BYTES];
   using Frag = typename FragOf<C::FP8>::T;
@@ -223,16 +214,11 @@ __global__ __launch_bounds__(C::THREADS) void gemm_mfma_kernel(KernelArgs a) {
     read_step(nxt, 0, fa[0], fb[0]);
   }
 
-#ifdef DBGEMM_EPILOGUE
-  ep_tile<C, C::STAGES * C::STAGE_BYTES, false>(a, acc, m0 + xa0, n0 + xb0, tm * C::WM + wm, wave, lane,
-                                                (uint32_t)(uintptr_t)sm);
-#else
   store_tile<C>(a, acc, m0 + xa0, n0 + xb0, lane);
-#endif
 }
 
 template <class C>
-hipError_t launch_cfg(const KernelArgs& a, hipStream_t s) {
+hipError_t launch_cfg(const GemmArgs& a, hipStream_t s) {
   hipLaunchKernelGGL(gemm_mfma_kernel<C>, dim3(grid_tiles(a)), dim3(C::THREADS), 0, s, a);
   return hipGetLastError();
 }
@@ -243,7 +229,7 @@ hipError_t launch_cfg(const KernelArgs& a, hipStream_t s) {
 
 // This object's transpose case (the file is compiled once per case).
 template <int BM, int BN, int BK, int WM, int WN, int MT, int ST, int IN>
-hipError_t launch_trans(const KernelArgs& a, hipStream_t s) {
+hipError_t launch_trans(const GemmArgs& a, hipStream_t s) {
   constexpr bool TA = DBGEMM_DMA_TA != 0, TB = DBGEMM_DMA_TB != 0;
   if constexpr (IN == IN_MX && (TA || !TB)) {  // block-scaled operands: A [M][K] and B [N][K] only
     return hipErrorInvalidConfiguration;
@@ -253,27 +239,6 @@ hipError_t launch_trans(const KernelArgs& a, hipStream_t s) {
 }
 
 }  // namespace
-
-#ifdef DBGEMM_EPILOGUE
-
-#define DBGEMM_ST_CAT2(a, b) launch_mfma_staged_ep_##a##b
-#define DBGEMM_ST_CAT(a, b) DBGEMM_ST_CAT2(a, b)
-
-hipError_t DBGEMM_ST_CAT(DBGEMM_DMA_TA, DBGEMM_DMA_TB)(const Policy& p, const GemmEpArgs& a, int* parts,
-                                                       hipStream_t s) {
-  *parts = a.tiles_m * p.WM;  // one partial row per row of waves
-#define DBGEMM_SIMT(name, eff)
-#define DBGEMM_MFMA(name_, pipe_, in_, bm_, bn_, bk_, wm_, wn_, mt_, st_, grp_, rn_, xcd_, sw_, eff_)      \
-  if constexpr (pipe_ == 0 && has_epilogue(pipe_, in_, bm_, bn_, bk_, mt_, ((sw_) >> 3) & 1, eff_))        \
-    if (p.BM == bm_ && p.BN == bn_ && p.BK == bk_ && p.WM == wm_ && p.WN == wn_ && p.in_mode == in_)       \
-      return launch_trans<bm_, bn_, bk_, wm_, wn_, mt_, st_, in_>(a, s);
-#include "policies.inc"
-#undef DBGEMM_SIMT
-#undef DBGEMM_MFMA
-  return hipErrorInvalidConfiguration;
-}
-
-#else
 
 #define DBGEMM_ST_CAT2(a, b) launch_mfma_staged_##a##b
 #define DBGEMM_ST_CAT(a, b) DBGEMM_ST_CAT2(a, b)
@@ -290,7 +255,5 @@ hipError_t DBGEMM_ST_CAT(DBGEMM_DMA_TA, DBGEMM_DMA_TB)(const Policy& p, const Ge
 #undef DBGEMM_MFMA
   return hipErrorInvalidConfiguration;
 }
-
-#endif
 
 }  // namespace dbgemm

@@ -81,6 +81,7 @@ template <class C>
 struct Dma {
   static_assert(C::IN != IN_E4M3, "widening needs the register-staged pipeline");
   static_assert(C::GES == C::ES, "LDS holds the global format");
+  static constexpr bool E8 = pp_e8<C>;  // E4M3 bytes in LDS, widened after each fragment read
   static constexpr int NW = C::THREADS / 64;
   static_assert(C::A_BYTES % (1024 * NW) == 0 && C::B_BYTES % (1024 * NW) == 0,
                 "each wave loads whole 1 KiB blocks of both tiles");
@@ -115,7 +116,7 @@ __global__ __launch_bounds__(C::THREADS) void gemm_dma_kernel(KernelArgs a) {
     else if constexpr (s == 2) return (lds_char*)lds_s2;
     else return (lds_char*)lds_s3;
   };
-  using Frag = typename FragOf<C::FP8>::T;
+  using Frag = std::conditional_t<D::E8, i32x2, typename FragOf<C::FP8>::T>;
   using Acc = typename AccOf<C::MT>::T;
 
   if (a.batch_y > 1 || a.batch_z > 1) {  // this workgroup's product of the batch
@@ -155,7 +156,8 @@ __global__ __launch_bounds__(C::THREADS) void gemm_dma_kernel(KernelArgs a) {
   for (int i = 0; i < D::A_IPW; ++i) {
     const int p = (wave * D::A_IPW + i) * 64 + lane;
     const int r = p / C::A_CPR;
-    const int c = (p % C::A_CPR) ^ (sw_on ? swz<C::A_KC, C::FP8, C::A_CPR, C::MT>(r) : 0);
+    const int c = (p % C::A_CPR) ^ (D::E8 ? pp_swz<C, C::A_KC, C::A_CPR>(r) :
+                                    sw_on ? swz<C::A_KC, C::FP8, C::A_CPR, C::MT>(r) : 0);
     if constexpr (C::A_KC) {  // rows = m, chunks along k
       a_goff[i] = (uint32_t)((m0 + r) * a.lda + c * C::VEC) * C::ES;
       a_ok[i] = (m0 + r) < a.M;
@@ -170,7 +172,8 @@ __global__ __launch_bounds__(C::THREADS) void gemm_dma_kernel(KernelArgs a) {
   for (int i = 0; i < D::B_IPW; ++i) {
     const int p = (wave * D::B_IPW + i) * 64 + lane;
     const int r = p / C::B_CPR;
-    const int c = (p % C::B_CPR) ^ (sw_on ? swz<C::B_KC, C::FP8, C::B_CPR, C::MT>(r) : 0);
+    const int c = (p % C::B_CPR) ^ (D::E8 ? pp_swz<C, C::B_KC, C::B_CPR>(r) :
+                                    sw_on ? swz<C::B_KC, C::FP8, C::B_CPR, C::MT>(r) : 0);
     if constexpr (C::B_KC) {  // rows = n, chunks along k
       b_goff[i] = (uint32_t)((n0 + r) * a.ldb + c * C::VEC) * C::ES;
       b_ok[i] = (n0 + r) < a.N;
@@ -260,6 +263,24 @@ __global__ __launch_bounds__(C::THREADS) void gemm_dma_kernel(KernelArgs a) {
   const int xa0 = wm * C::WTM, xb0 = wn * C::WTN;
 
   Frag fa[2][C::FM], fb[2][C::FN];
+  // one fragment of an operand: 8 E4M3 bytes as they are, or what the MFMA takes
+  auto frag = [&](auto kcc, auto rbc, const lds_char* base, int x0, int kbase) -> Frag {
+    constexpr bool KC = decltype(kcc)::value;
+    constexpr int RB = decltype(rbc)::value;
+    if constexpr (D::E8) {
+      const uint32_t o = pp_frag_off<C, KC, RB>(x0, kbase, lane, 0);
+      if constexpr (KC)
+        return *LDS_PTR(i32x2, base, o);
+      else
+        return __builtin_amdgcn_ds_read_tr8_b64_v2i32(LDS_PTR(i32x2, base, o));
+    } else {
+      return load_frag<C, KC, RB>(base, x0, kbase, lane, sw_on);
+    }
+  };
+  constexpr std::bool_constant<C::A_KC> akc{};
+  constexpr std::bool_constant<C::B_KC> bkc{};
+  constexpr std::integral_constant<int, C::A_RB> arb{};
+  constexpr std::integral_constant<int, C::B_RB> brb{};
   // Fragment r of K step kk, in the order the MFMAs first use them (the MFMAs run
   // A-fragment-major): A0, B0 .. B(FN-1), then A1 .. A(FM-1).
   auto read_one = [&](const lds_char* sb, int kk, Frag* xa, Frag* xb, auto rc) {
@@ -267,17 +288,16 @@ __global__ __launch_bounds__(C::THREADS) void gemm_dma_kernel(KernelArgs a) {
     constexpr bool is_b = r >= 1 && r <= C::FN;
     constexpr int idx = r == 0 ? 0 : (is_b ? r - 1 : r - C::FN);
     if constexpr (!is_b)
-      xa[idx] = load_frag<C, C::A_KC, C::A_RB>(sb, xa0 + idx * C::MT, kk * C::KT, lane, sw_on);
+      xa[idx] = frag(akc, arb, sb, xa0 + idx * C::MT, kk * C::KT);
     else
-      xb[idx] = load_frag<C, C::B_KC, C::B_RB>(sb + C::A_BYTES, xb0 + idx * C::MT, kk * C::KT, lane, sw_on);
+      xb[idx] = frag(bkc, brb, sb + C::A_BYTES, xb0 + idx * C::MT, kk * C::KT);
   };
   auto read_step = [&](const lds_char* sb, int kk, Frag* xa, Frag* xb) {
 #pragma unroll
     for (int i = 0; i < C::FM; ++i)
-      xa[i] = load_frag<C, C::A_KC, C::A_RB>(sb, xa0 + i * C::MT, kk * C::KT, lane, sw_on);
+      xa[i] = frag(akc, arb, sb, xa0 + i * C::MT, kk * C::KT);
 #pragma unroll
-    for (int j = 0; j < C::FN; ++j)
-      xb[j] = load_frag<C, C::B_KC, C::B_RB>(sb + C::A_BYTES, xb0 + j * C::MT, kk * C::KT, lane, sw_on);
+    for (int j = 0; j < C::FN; ++j) xb[j] = frag(bkc, brb, sb + C::A_BYTES, xb0 + j * C::MT, kk * C::KT);
   };
 
   // Scaled native E4M3: the scale bytes this lane's MFMAs take, one register per two
@@ -347,6 +367,14 @@ __global__ __launch_bounds__(C::THREADS) void gemm_dma_kernel(KernelArgs a) {
         Frag* rb_next = fb[(kk + 1) & 1];
         const lds_char* rsrc_slot = last ? nxt : cur;
         const int rkk = last ? 0 : kk + 1;
+        // E4M3: this step's fragments widened (the conversions issue beside the other waves' MFMAs)
+        bf16x8 wa[D::E8 ? C::FM : 1], wb[D::E8 ? C::FN : 1];
+        if constexpr (D::E8) {
+#pragma unroll
+          for (int i = 0; i < C::FM; ++i) wa[i] = pp_widen8(fa[kk & 1][i]);
+#pragma unroll
+          for (int j = 0; j < C::FN; ++j) wb[j] = pp_widen8(fb[kk & 1][j]);
+        }
         // Explicit order: MFMA i, then its share of the fragment reads for the next
         // step and of the loads for tile u+STAGES-1; nothing is moved across a group.
         static_for<NMF>([&](auto ic) {
@@ -359,6 +387,8 @@ __global__ __launch_bounds__(C::THREADS) void gemm_dma_kernel(KernelArgs a) {
             mma_mx<2 * (i % C::FN % 2) + kk, 2 * (i / C::FN % 2) + kk>(
                 acc[i / C::FN][i % C::FN], fb[kk & 1][i % C::FN], fa[kk & 1][i / C::FN],
                 scB[s & 1][i % C::FN / 2], scA[s & 1][i / C::FN / 2]);
+          else if constexpr (D::E8)
+            mma(acc[i / C::FN][i % C::FN], wb[i % C::FN], wa[i / C::FN]);
           else
             mma(acc[i / C::FN][i % C::FN], fb[kk & 1][i % C::FN], fa[kk & 1][i / C::FN]);
           if constexpr (i >= RD0) {
@@ -530,7 +560,7 @@ hipError_t DBGEMM_DMA_CAT(DBGEMM_DMA_TA, DBGEMM_DMA_TB)(const Policy& p, const G
 #define DBGEMM_SIMT(name, eff)
 #define DBGEMM_MFMA(name_, pipe_, in_, bm_, bn_, bk_, wm_, wn_, mt_, st_, grp_, rn_, xcd_, sw_, eff_)      \
   if constexpr (pipe_ == 1 && has_epilogue(pipe_, in_, bm_, bn_, bk_, mt_, ((sw_) >> 3) & 1, eff_))        \
-    if (p.BM == bm_ && p.BN == bn_ && p.BK == bk_ && p.WM == wm_ && p.WN == wn_ && p.stages == st_)        \
+    if (p.in_mode == in_ && p.BM == bm_ && p.BN == bn_ && p.BK == bk_ && p.WM == wm_ && p.WN == wn_ && p.stages == st_) \
       return launch_cfg<Cfg<bm_, bn_, bk_, wm_, wn_, mt_, st_, in_, DBGEMM_DMA_TA != 0, DBGEMM_DMA_TB != 0>>(a, s);
 #include "policies.inc"
 #undef DBGEMM_SIMT
@@ -549,7 +579,7 @@ bool DBGEMM_DMA_CAT(DBGEMM_DMA_TA, DBGEMM_DMA_TB, DBGEMM_DMA_PART)(const Policy&
                                                                    hipError_t* err) {
 #define DBGEMM_SIMT(name, eff)
 #define DBGEMM_MFMA(name_, pipe_, in_, bm_, bn_, bk_, wm_, wn_, mt_, st_, grp_, rn_, xcd_, sw_, eff_)       \
-  if constexpr (pipe_ == 1 && __LINE__ % 2 == DBGEMM_DMA_PART &&                                          \
+  if constexpr (pipe_ == 1 && __LINE__ % 2 == DBGEMM_DMA_PART && !(((sw_) >> 5) & 1) &&                   \
                 ((in_ != 4 && !(((sw_) >> 3) & 1)) || (DBGEMM_DMA_TA == 0 && DBGEMM_DMA_TB == 1)))        \
     if (p.BM == bm_ && p.BN == bn_ && p.BK == bk_ && p.WM == wm_ && p.WN == wn_ && p.MT == mt_ &&         \
         p.stages == st_ && p.in_mode == in_ && p.read_mode == ((((sw_) >> 2) & 1) ? 0 : 1)) {             \

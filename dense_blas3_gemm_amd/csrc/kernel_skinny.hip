@@ -246,12 +246,23 @@ hipError_t launch_rows(const GemmEpArgs& a, hipStream_t s) {
 
 }  // namespace
 
-// Up to 64 rows against B [N][K] (64 x 5120 x 5120: 15.9 us, the tiled kernels 17.2), and in E4M3,
-// whose tiled kernels do not split K; up to 16 against B [K][N] (64 rows: 20.2 us, tiled 17.2).
-int skinny_rows(int in_fp8, int transA, int transB) { return transA ? 0 : in_fp8 || transB ? 64 : 16; }
+// Where this kernel is the faster one (us here / us of the tiled kernels with split-K, bf16):
+// against B [N][K] up to 32 rows (16 x 5120 x 5120 10.5 / 16.9, 32 rows 12.0 / 16.9, 64 rows
+// 15.7 / 17.2), unless a few workgroups would walk a long K (16 x 1344 x 19696: 32 / 18); against
+// B [K][N], whose columns an XCD finds on some of its L2's channels only, up to 16 rows and K
+// not past N (4096 x 4096 11.4 / 12.4, 20480 x 5120 53.6 / 59.7, but 2048 x 8192 19.1 / 12.8),
+// small ones up to 32 rows (512 x 5120 9.0 / 11.5).  E4M3: up to 64 rows (the tiled kernels for
+// it reach 64 rows at 64 x 5120 x 5120 in 17 us, this one 13.0 and 17.4 for the two layouts).
+bool skinny_serves(int in_fp8, int transA, int transB, int64_t M, int64_t N, int64_t K) {
+  if (transA) return false;
+  const bool small = N * K <= (4 << 20);
+  if (in_fp8) return M <= 64 && (small || K <= 8192 || N >= K / 4);
+  if (transB) return M <= 32 && (K <= 8192 || N >= K / 4);
+  return small ? M <= 32 : M <= 16 && K <= N;
+}
 
 hipError_t launch_skinny(const GemmEpArgs& a, hipStream_t s) {
-  if (a.M < 1 || a.M > skinny_rows(a.in_fp8, a.transA, a.transB) || a.N % 8 != 0) return hipErrorInvalidConfiguration;
+  if (a.M < 1 || a.M > 64 || a.transA || a.N % 8 != 0) return hipErrorInvalidConfiguration;
   if (a.in_fp8) return a.transB ? launch_rows<true, true>(a, s) : launch_rows<true, false>(a, s);
   return a.transB ? launch_rows<false, true>(a, s) : launch_rows<false, false>(a, s);
 }

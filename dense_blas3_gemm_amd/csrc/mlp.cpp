@@ -114,7 +114,7 @@ bool run_fused(const HandleView& v, GemmEpArgs a, int transA, int transB, int dt
   a.in_fp8 = pr.in_fp8;
   a.transA = transA;
   a.transB = transB;
-  if (a.M <= skinny_rows(a.in_fp8, transA, transB)) {
+  if (skinny_serves(a.in_fp8, transA, transB, a.M, a.N, a.K)) {
     a.ep.colsum = dbias;
     *st = status(launch_skinny(a, v.stream));
     return true;
@@ -177,10 +177,8 @@ gemm_status_t run_product(gemm_handle_t h, int transA, int transB, int64_t M, in
 
 namespace dbgemm {
 hipError_t launch_mfma_ep(const Policy& p, const GemmEpArgs& a, int* parts, hipStream_t s) {
-#define DBGEMM_EP_CASE(ab)                                                                       \
-  return p.pipe == 2   ? launch_mfma_pp_ep_##ab(p, a, parts, s)                                  \
-         : p.pipe == 1 ? launch_mfma_dma_ep_##ab(p, a, parts, s)                                 \
-                       : launch_mfma_staged_ep_##ab(p, a, parts, s)
+#define DBGEMM_EP_CASE(ab) \
+  return p.pipe == 2 ? launch_mfma_pp_ep_##ab(p, a, parts, s) : launch_mfma_dma_ep_##ab(p, a, parts, s)
   switch (a.transA * 2 + a.transB) {
     case 0: DBGEMM_EP_CASE(00);
     case 1: DBGEMM_EP_CASE(01);

@@ -43,17 +43,16 @@ hipError_t launch_mfma_ep(const Policy& p, const GemmEpArgs& a, int* parts, hipS
 // one per kernel family and (transA, transB) case, each in its own object
 #define DBGEMM_EP_DECL(ab)                                                                               \
   hipError_t launch_mfma_pp_ep_##ab(const Policy& p, const GemmEpArgs& a, int* parts, hipStream_t s);     \
-  hipError_t launch_mfma_dma_ep_##ab(const Policy& p, const GemmEpArgs& a, int* parts, hipStream_t s);    \
-  hipError_t launch_mfma_staged_ep_##ab(const Policy& p, const GemmEpArgs& a, int* parts, hipStream_t s);
+  hipError_t launch_mfma_dma_ep_##ab(const Policy& p, const GemmEpArgs& a, int* parts, hipStream_t s);
 DBGEMM_EP_DECL(00)
 DBGEMM_EP_DECL(01)
 DBGEMM_EP_DECL(10)
 DBGEMM_EP_DECL(11)
 #undef DBGEMM_EP_DECL
 
-// Products of a few rows (at most skinny_rows), N a multiple of 8, operands as the MFMA kernels
-// take them; ep.colsum, when set, receives the column sums themselves.
-int skinny_rows(int in_fp8, int transA, int transB);
+// Products of a few rows, N a multiple of 8, operands as the MFMA kernels take them; ep.colsum,
+// when set, receives the column sums themselves.
+bool skinny_serves(int in_fp8, int transA, int transB, int64_t M, int64_t N, int64_t K);
 hipError_t launch_skinny(const GemmEpArgs& a, hipStream_t s);
 
 // ---- launchers (they return hipSuccess or the launch error)

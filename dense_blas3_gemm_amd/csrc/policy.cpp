@@ -14,10 +14,10 @@ namespace dbgemm {
 namespace {
 
 const Policy kTable[] = {
-#define DBGEMM_SIMT(name_, eff_) {name_, KIND_SIMT, 0, -1, 64, 64, 16, 1, 1, 0, 1, 1, 0, 1, 0, 0, 1, 256, eff_, 0, 0},
+#define DBGEMM_SIMT(name_, eff_) {name_, KIND_SIMT, 0, -1, 64, 64, 16, 1, 1, 0, 1, 1, 0, 1, 0, 0, 1, 256, eff_, 0, 0, 0},
 #define DBGEMM_MFMA(name_, pipe_, in_, bm_, bn_, bk_, wm_, wn_, mt_, st_, grp_, rn_, xcd_, sw_, eff_) \
   {name_, KIND_MFMA, pipe_, in_, bm_, bn_, bk_, wm_, wn_, mt_, st_, grp_, rn_, xcd_, (sw_) & 1,        \
-   ((sw_) >> 1) & 1, ((sw_) >> 2) & 1 ? 0 : 1, (wm_) * (wn_) * 64, eff_, ((sw_) >> 3) & 1, ((sw_) >> 4) & 1},
+   ((sw_) >> 1) & 1, ((sw_) >> 2) & 1 ? 0 : 1, (wm_) * (wn_) * 64, eff_, ((sw_) >> 3) & 1, ((sw_) >> 4) & 1, ((sw_) >> 5) & 1},
 #include "policies.inc"
 #include "policies_pp.inc"
 #undef DBGEMM_SIMT
@@ -58,6 +58,7 @@ int policy_find(const char* name) {
 bool policy_serves(const Policy& p, const Problem& pr) {
   if (p.kind == KIND_SIMT) return true;
   if (p.kind != KIND_MFMA || !pr.fast_ok) return false;
+  if (p.ep_only && !pr.ep) return false;
   if (pr.ep && !has_epilogue(p.pipe, p.in_mode, p.BM, p.BN, p.BK, p.MT, p.k_contig_only, p.efficiency)) return false;
   if (p.k_contig_only && (pr.transA != 0 || pr.transB != 1)) return false;
   if (p.a_kc_only && pr.transA != 0) return false;

@@ -190,6 +190,21 @@ def test_run_act_long_k_small_output(gpu):
         act_case(gpu, M, M, 136, 6144 + 8, (0, 0), "bf16", "f32", "silu", "f32", True, "bf16", alpha=0.01)
 
 
+# E4M3 operands under 256 x 256 tiles: whole and ragged tiles, a K of one tile and less, a K
+# that ends inside a tile, split and not
+@pytest.mark.parametrize("shape", [(70, 80, 96), (65, 144, 2064), (130, 272, 4112), (150, 528, 1040), (320, 512, 112),
+                                   (384, 1152, 2576), (72, 2048, 256), (272, 4096, 528)])
+@pytest.mark.parametrize("trans", [(0, 0), (0, 1), (1, 0), (1, 1)])
+def test_e4m3_small_tiles(gpu, shape, trans):
+    M, N, K = shape
+    if trans[0]:
+        M = M // 16 * 16  # rows of whole 16-byte pieces
+    i = 60 + trans[0] * 2 + trans[1]
+    act_case(gpu, i, M, N, K, trans, "e4m3", "bf16", "gelu", "f32", True, "mx", alpha=0.02)
+    act_case(gpu, i, M, N, K, trans, "e4m3", "f32", "silu", "bf16", False, "bf16", alpha=0.02)
+    dact_case(gpu, i, M, N, K, trans, "bf16", "silu", "mx", in_kind="e4m3", alpha=0.02)
+
+
 def test_run_act_in_place_residual(gpu):
     for shape in ((3, 40, 24), (70, 132, 64), (256, 512, 128), (65, 129, 71)):
         act_case(gpu, 5, *shape, (0, 1), "bf16", "bf16", "gelu", "f32", True, "none", in_place=True, pads=(0, 8, 0))

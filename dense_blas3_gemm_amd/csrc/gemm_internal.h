@@ -206,7 +206,16 @@ int64_t stream_k_ws_floats(const Policy& p, const StreamK& s);  // partial slots
 // never chosen here, only by name: on the grids it was built for (dX, dW) it measured
 // slower than the plain grid, because its workgroups run at scattered K offsets and lose
 // the L2 reuse of workgroups that step through K together.
-int policy_select(const Problem& pr, int cu_count, int64_t ws_floats, int* splits);
+// *cost (when asked for) receives the model's time in its own units.
+int policy_select(const Problem& pr, int cu_count, int64_t ws_floats, int* splits, double* cost = nullptr);
+// A product with an epilogue in two: [0, at) of M or N on policy p in whole rounds of the
+// CUs, the rest on policy_select's choice for it.  p < 0: one launch is as fast.
+struct Cut {
+  int p = -1;
+  bool by_rows = false;
+  int64_t at = 0;
+};
+Cut policy_cut(const Problem& pr, int cu_count, int64_t ws_floats, double whole);
 // fp32 partials a split-K call of policy p with `splits` needs, K tiles per split
 // (0: that split is not allowed), and whether the split fits a workspace.
 int64_t split_ws_floats(const Policy& p, const Problem& pr, int splits);

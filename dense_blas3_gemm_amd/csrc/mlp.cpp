@@ -105,6 +105,36 @@ gemm_status_t run_by_rows(const HandleView& v, GemmEpArgs a, int transA, int tra
   return GEMM_STATUS_SUCCESS;
 }
 
+// One launch on policy p with sp splits; dbias partials into ep.colsum, *parts rows of them.
+hipError_t run_tiles(const HandleView& v, GemmEpArgs a, const Policy& p, int sp, int* parts) {
+  a.tiles_m = (a.M + p.BM - 1) / p.BM;
+  a.tiles_n = (a.N + p.BN - 1) / p.BN;
+  a.group = p.group;
+  a.raster_n = p.raster_n;
+  a.xcd = p.xcd;
+  a.swizzle = p.swizzle;
+  a.splits = sp;
+  a.kt_per_split = (int)split_kt(p, a.K, sp);
+  a.ws = sp > 1 ? (float*)v.ws : nullptr;
+  return launch_mfma_ep(p, a, parts, v.stream);
+}
+
+// a's rows [m0, m0 + M) and columns [n0, n0 + N); n0 a multiple of 32.
+GemmEpArgs part_of(const GemmEpArgs& a, int64_t m0, int64_t n0, int64_t M, int64_t N) {
+  GemmEpArgs r = a;
+  const int64_t es = a.in_fp8 ? 1 : 2, ce = a.c_kind == C_F32 ? 4 : 2, ze = a.ep.z_kind == Z_MX ? 1 : 2;
+  r.M = (int)M;
+  r.N = (int)N;
+  r.A = (const char*)a.A + (a.transA ? m0 : m0 * a.lda) * es;
+  r.B = (const char*)a.B + (a.transB ? n0 * a.ldb : n0) * es;
+  r.C = (char*)a.C + (m0 * a.ldc + n0) * ce;
+  if (a.ep.bias) r.ep.bias = (const char*)a.ep.bias + n0 * (a.ep.bias_f32 ? 4 : 2);
+  if (a.ep.R) r.ep.R = (const char*)a.ep.R + (m0 * a.ep.ldr + n0) * ce;
+  if (a.ep.Z) r.ep.Z = (char*)a.ep.Z + (m0 * a.ep.ldz + n0) * ze;
+  if (a.ep.S) r.ep.S = a.ep.S + m0 * a.ep.lds + n0 / 32;
+  return r;
+}
+
 // The product with its epilogue in the kernel that computes it; false when no such kernel
 // takes the operands.
 bool run_fused(const HandleView& v, GemmEpArgs a, int transA, int transB, int dtype, float* dbias, gemm_status_t* st) {
@@ -121,27 +151,41 @@ bool run_fused(const HandleView& v, GemmEpArgs a, int transA, int transB, int dt
   }
   pr.ep = true;
   int sp = 1;
+  double cost = 0.0;
   const int64_t split_floats = v.ws ? (int64_t)(kPartBytes / sizeof(float)) : 0;
-  const Policy& p = policy_at(policy_select(pr, v.cu_count, split_floats, &sp));
-  if (p.kind != KIND_MFMA) return false;
-  a.tiles_m = (a.M + p.BM - 1) / p.BM;
-  a.tiles_n = (a.N + p.BN - 1) / p.BN;
-  a.group = p.group;
-  a.raster_n = p.raster_n;
-  a.xcd = p.xcd;
-  a.swizzle = p.swizzle;
-  a.splits = sp;
-  a.kt_per_split = (int)split_kt(p, a.K, sp);
-  a.ws = sp > 1 ? (float*)v.ws : nullptr;
-  if (dbias) {
-    // at most one partial row per 16 rows of C
-    const int64_t most = ((int64_t)a.tiles_m * p.BM / 16) * a.N * (int64_t)sizeof(float);
-    if (!v.ws || v.ws_bytes < kPartBytes + (size_t)most) return false;
-    a.ep.colsum = (float*)((char*)v.ws + kPartBytes);
+  int idx = policy_select(pr, v.cu_count, split_floats, &sp, &cost);
+  if (policy_at(idx).kind != KIND_MFMA) return false;
+  const Cut cut = policy_cut(pr, v.cu_count, split_floats, cost);
+  const int64_t M1 = cut.p >= 0 && cut.by_rows ? cut.at : a.M, N1 = cut.p >= 0 && !cut.by_rows ? cut.at : a.N;
+  GemmEpArgs a1 = part_of(a, 0, 0, M1, N1), a2{};
+  int idx2 = 0, sp2 = 1;
+  if (cut.p >= 0) {
+    a2 = part_of(a, a.M - M1 ? M1 : 0, a.N - N1 ? N1 : 0, cut.by_rows ? a.M - M1 : a.M, cut.by_rows ? a.N : a.N - N1);
+    idx = cut.p;
+    sp = 1;
+    pr.M = a2.M;
+    pr.N = a2.N;
+    idx2 = policy_select(pr, v.cu_count, split_floats, &sp2);
+    if (policy_at(idx2).kind != KIND_MFMA) return false;
   }
-  int parts = 0;
-  hipError_t e = launch_mfma_ep(p, a, &parts, v.stream);
-  if (e == hipSuccess && dbias) e = launch_colsum(a.ep.colsum, parts, a.N, a.N, dbias, nullptr, 0, v.stream);
+  float* part = nullptr;
+  if (dbias) {
+    // at most one partial row per 16 rows of C, whole tiles of at most 256 rows in each launch
+    const int64_t most = ((int64_t)a.M + 2 * 256) / 16 * a.N * (int64_t)sizeof(float);
+    if (!v.ws || v.ws_bytes < kPartBytes + (size_t)most) return false;
+    part = a1.ep.colsum = (float*)((char*)v.ws + kPartBytes);
+  }
+  int parts = 0, parts2 = 0;
+  hipError_t e = run_tiles(v, a1, policy_at(idx), sp, &parts);
+  if (e == hipSuccess && dbias && !cut.by_rows)
+    e = launch_colsum(part, parts, a1.N, a1.N, dbias, nullptr, 0, v.stream);
+  if (e == hipSuccess && cut.p >= 0) {
+    if (dbias) a2.ep.colsum = part + (int64_t)parts * a1.N;
+    e = run_tiles(v, a2, policy_at(idx2), sp2, &parts2);
+    if (e == hipSuccess && dbias)
+      e = cut.by_rows ? launch_colsum(part, parts + parts2, a.N, a.N, dbias, nullptr, 0, v.stream)
+                      : launch_colsum(a2.ep.colsum, parts2, a2.N, a2.N, dbias + N1, nullptr, 0, v.stream);
+  }
   *st = status(e);
   return true;
 }

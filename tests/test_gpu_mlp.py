@@ -205,6 +205,18 @@ def test_e4m3_small_tiles(gpu, shape, trans):
     dact_case(gpu, i, M, N, K, trans, "bf16", "silu", "mx", in_kind="e4m3", alpha=0.02)
 
 
+# more 256 x 256 tiles than CUs and not whole rounds of them: two launches, cut by columns or by
+# rows, the second on other tiles
+@pytest.mark.parametrize("shape", [(1300, 13088, 320), (13104, 1296, 320)])
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_products_in_two_launches(gpu, shape, kind):
+    M, N, K = shape
+    tB = int(kind == "e4m3")
+    act_case(gpu, 70, M, N, K, (0, tB), kind, "bf16", "silu", "f32", True, "mx", pads=(16, 8, 32), alpha=0.1)
+    act_case(gpu, 71, M, N, K, (int(M % 16 == 0), 1 - tB), kind, "f32", "none", "bf16", False, "bf16", alpha=0.1)
+    dact_case(gpu, 72, M, N, K, (0, 1 - tB), "bf16", "relu", "mx", in_kind=kind, alpha=0.1)
+
+
 def test_run_act_in_place_residual(gpu):
     for shape in ((3, 40, 24), (70, 132, 64), (256, 512, 128), (65, 129, 71)):
         act_case(gpu, 5, *shape, (0, 1), "bf16", "bf16", "gelu", "f32", True, "none", in_place=True, pads=(0, 8, 0))

@@ -39,6 +39,7 @@ __device__ __forceinline__ void ep_tile(const GemmEpArgs& a, const typename AccO
   constexpr int RB = C::WTN * 4, CPR = C::WTN / 4;  // bytes and 16-byte chunks of an LDS row
   constexpr int LPR = C::WTN / 8, RPS = 64 / LPR;   // lanes to a row, rows to a step
   constexpr int STEPS = PASS / RPS, BATCH = STEPS < 4 ? STEPS : 4;
+  constexpr int ALL = C::WTM / RPS;
   static_assert(PASS * RB * (C::THREADS / 64) <= LDS_BYTES, "a pass of every wave fits");
   static_assert(LPR % 4 == 0 && (CPR & (CPR - 1)) == 0 && PASS % RPS == 0 && STEPS % BATCH == 0,
                 "whole blocks of 32 columns, whole steps and batches");
@@ -48,22 +49,20 @@ __device__ __forceinline__ void ep_tile(const GemmEpArgs& a, const typename AccO
   const float alpha = a.alpha;
   float cs[8] = {}, b[8];
   ep_bias8(a, n, nvc, b);
-  __syncthreads();  // the LDS is free: the K loop's reads are done
   ep_dispatch(a.ep, [&](auto gc, auto ac) EP_INLINE {
     constexpr bool GRAD = decltype(gc)::value;
     constexpr int ACT = decltype(ac)::value;
+    EpRaw raw[BATCH];
+    auto fetch = [&](int step) EP_INLINE {
+      const int m = m0 + row + step * RPS;
+      return ep_fetch8<GRAD, false>(a, m, n, step < ALL && m < a.M ? nvc : 0);
+    };
+#pragma unroll
+    for (int s = 0; s < BATCH; ++s) raw[s] = fetch(s);
+    __syncthreads();  // the LDS is free: the K loop's reads are done
     static_for<C::WTM / PASS>([&](auto hc) EP_INLINE {
       constexpr int h = decltype(hc)::value;
       const int mp = m0 + h * PASS + row;
-      EpRaw raw[BATCH];
-      auto fetch = [&](int s0) EP_INLINE {
-#pragma unroll
-        for (int s = 0; s < BATCH; ++s) {
-          const int m = mp + (s0 + s) * RPS;
-          raw[s] = ep_fetch8<GRAD, false>(a, m, n, m < a.M ? nvc : 0);
-        }
-      };
-      fetch(0);
       static_for<PASS / 16 * C::FN>([&](auto pc) EP_INLINE {
         constexpr int p = decltype(pc)::value;
         constexpr int li = p / C::FN, i = h * (PASS / 16) + li, j = p % C::FN;
@@ -74,7 +73,6 @@ __device__ __forceinline__ void ep_tile(const GemmEpArgs& a, const typename AccO
       });
 #pragma unroll 1
       for (int s0 = 0; s0 < STEPS; s0 += BATCH) {
-        if (s0 > 0) fetch(s0);
 #pragma unroll
         for (int s = 0; s < BATCH; ++s) {
           const int r = (s0 + s) * RPS + row, m = mp + (s0 + s) * RPS;
@@ -83,6 +81,7 @@ __device__ __forceinline__ void ep_tile(const GemmEpArgs& a, const typename AccO
           const f32x4 hi = *(__attribute__((address_space(3))) f32x4*)(uintptr_t)(at + (((ch + 1) ^ x) * 16));
           float w[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
           ep_finish8<NT, GRAD, ACT, false>(a, w, raw[s], b, m, n, m < a.M ? nvc : 0, cs);
+          raw[s] = fetch(h * STEPS + s0 + s + BATCH);
         }
       }
     });

@@ -46,23 +46,18 @@ __device__ __forceinline__ float e4m3_to_f32(uint32_t c) {
 
 namespace dbgemm {
 
-// UE8M0 scale byte of a block whose largest magnitude is amax: the exponent floor(log2(amax))
-// - 8 (8 is the largest E4M3 exponent) stored plus 127, clamped to 0 .. 254; 0 for an
-// all-zero block.
+// UE8M0 scale byte of a block whose largest magnitude is amax (not NaN): the exponent
+// floor(log2(amax)) - 8 (8 is the largest E4M3 exponent) stored plus 127, at least 0; 0 for an
+// all-zero block.  amax's own exponent field less 8, where both are normal; a subnormal amax's
+// is below 0 either way.  At most 247 (infinity).
 __device__ __forceinline__ int mx_scale(float amax) {
-  if (!(amax > 0.0f)) return 0;
-  int ex;  // floor(log2(amax)); amax is normal or subnormal in fp32
-  const uint32_t ab = __builtin_bit_cast(uint32_t, amax);
-  if ((ab >> 23) != 0u)
-    ex = (int)(ab >> 23) - 127;
-  else
-    ex = -126 - (__builtin_clz(ab) - 8 - 1) - 1;  // subnormal: 2^-149 * mantissa
-  const int e = ex - 8 + 127;
-  return e < 0 ? 0 : (e > 254 ? 254 : e);
+  const int e = (int)(__builtin_bit_cast(uint32_t, amax) >> 23) - 8;
+  return e < 0 ? 0 : e;
 }
-// 2^(127-e): x / 2^(e-127) = x * mx_inv(e), exact (the results stay below 512 in magnitude).
+// 2^(127-e), e from mx_scale: x / 2^(e-127) = x * mx_inv(e), exact (the results stay below 512
+// in magnitude).
 __device__ __forceinline__ float mx_inv(int e) {
-  return e == 254 ? 0x1p-127f : __builtin_bit_cast(float, (uint32_t)(254 - e) << 23);
+  return __builtin_bit_cast(float, (uint32_t)(254 - e) << 23);
 }
 
 // Four values to four E4M3 codes (a in the low byte) with the gfx950 conversion

@@ -177,6 +177,19 @@ __device__ __forceinline__ void ep_with_act(int act, F&& f) {
   }
 }
 
+// The largest magnitude goes round the four lanes in the VALU (DPP quads), and the clamp is one
+// v_med3: that loses a NaN, so eights that hold one take the conversion that keeps it.
+__device__ __forceinline__ float ep_quad_max(float v) {
+  const int a = __builtin_bit_cast(int, v);
+  v = __builtin_fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(a, a, 0xB1, 0xF, 0xF, true)));
+  const int b = __builtin_bit_cast(int, v);
+  return __builtin_fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(b, b, 0x4E, 0xF, 0xF, true)));
+}
+__device__ __forceinline__ uint32_t ep_sat4(float a, float b, float c, float d) {
+  auto sat = [](float x) EP_INLINE { return __builtin_amdgcn_fmed3f(x, -448.f, 448.f); };
+  const int w = __builtin_amdgcn_cvt_pk_fp8_f32(sat(a), sat(b), 0, false);
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(sat(c), sat(d), w, true);
+}
 // Eight values of a row to E4M3 codes: the four neighbouring lanes that hold one block of
 // 32 columns (columns n & ~31 .. + 31) run this together, each with its eight (the invalid
 // ones zero).  Stores the first nv codes at q and, from the block's first lane when it has
@@ -186,12 +199,15 @@ __device__ __forceinline__ void ep_store_mx(const float (&v)[8], int nv, bool fi
   float amax = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) amax = __builtin_fmaxf(amax, __builtin_fabsf(v[i]));  // NaN does not set it
-  amax = __builtin_fmaxf(amax, __shfl_xor(amax, 1));
-  amax = __builtin_fmaxf(amax, __shfl_xor(amax, 2));
-  const int e = mx_scale(amax);
+  const int e = mx_scale(ep_quad_max(amax));
   const float inv = mx_inv(e);
-  const uint32_t lo = e4m3x4_from_f32(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
-  const uint32_t hi = e4m3x4_from_f32(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv);
+  uint32_t lo = ep_sat4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
+  uint32_t hi = ep_sat4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv);
+  if (__builtin_isunordered(v[0], v[1]) | __builtin_isunordered(v[2], v[3]) | __builtin_isunordered(v[4], v[5]) |
+      __builtin_isunordered(v[6], v[7])) {
+    lo = e4m3x4_from_f32(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
+    hi = e4m3x4_from_f32(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv);
+  }
   if (first && nv > 0) *s = (uint8_t)e;
   if (nv == 8) {
     *(ep_u32x2_u*)q = (ep_u32x2){lo, hi};

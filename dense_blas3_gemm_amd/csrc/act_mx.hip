@@ -64,12 +64,12 @@ __global__ __launch_bounds__(kThreads) void ep_rows_kernel(GemmEpArgs a, int64_t
   const int nv = a.N - n < 8 ? a.N - n : 8;
   float cs[8] = {}, b[8];
   ep_bias8(a, n, nv, b);
-  ep_dispatch(a.ep, [&](auto gc, auto ac) EP_INLINE {
+  ep_dispatch(a.ep, [&](auto mc, auto ac) EP_INLINE {
     for (int64_t m = (int64_t)blockIdx.y * blockDim.y + threadIdx.y; m < a.M; m += (int64_t)gridDim.y * blockDim.y) {
       float w[8];
-      const EpRaw r = ep_fetch8<decltype(gc)::value, true>(a, m, n, nv);
+      const EpRaw r = ep_fetch8<decltype(mc)::value, true>(a, m, n, nv);
       ep_load8(a.ws + m * ldw + n, nv, w);
-      ep_finish8<false, decltype(gc)::value, decltype(ac)::value, true>(a, w, r, b, m, n, nv, cs);
+      ep_finish8<false, decltype(mc)::value, decltype(ac)::value, true>(a, w, r, b, m, n, nv, cs);
     }
   });
   put_partial(a.ep.colsum, a.N, n64, cs);

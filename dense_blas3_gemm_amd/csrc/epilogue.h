@@ -250,6 +250,12 @@ __device__ __forceinline__ void ep_load_mx(const uint8_t* q, int nv, uint32_t sc
 // issues the load of what the row brings (the residual, or Z for a gradient), ep_finish8 does
 // the rest, so that a caller can have the loads of several rows in flight.  nv: the valid
 // columns, 0 .. 8 (0: no row or column here).
+//
+// A gradient's Z is a compile-time choice: where the loads of codes and of bf16 met again in one
+// register, the compiler waited for them at once and nothing was in flight (2048 x 20480 x 5120
+// from codes: 380 us, so 369).  The same for a residual's kinds, with unconditional loads, made
+// no difference.
+enum { EP_FORWARD = 0, EP_GRAD_BF16 = 1, EP_GRAD_MX = 2 };
 struct EpRaw {
   ep_u32x4 lo, hi;  // 8 bf16 in lo, 8 fp32, or 8 codes in lo[0..1] and their scale in lo[2]
 };
@@ -269,26 +275,24 @@ __device__ __forceinline__ ep_u32x4 ep_raw_part(const void* p, int nv, int first
   return v;
 }
 
-template <bool GRAD, bool PART>
+template <int MODE, bool PART>
 __device__ __forceinline__ EpRaw ep_fetch8(const GemmEpArgs& a, int64_t m, int n, int nv) {
   const EpArgs& e = a.ep;
   EpRaw r;
   r.lo = r.hi = (ep_u32x4){0, 0, 0, 0};
   if (nv == 0) return r;
   const bool whole = !PART || nv == 8;
-  if constexpr (GRAD) {
-    if (e.z_kind == Z_MX) {
-      const uint8_t* p = (const uint8_t*)e.Z + m * e.ldz + n;
-      if (whole) {
-        const ep_u32x2 v = *(const ep_u32x2_u*)p;
-        r.lo = (ep_u32x4){v[0], v[1], 0, 0};
-      } else if constexpr (PART) {
-        r.lo = ep_raw_part<1>(p, nv, 0);
-      }
-      r.lo[2] = e.S[m * e.lds + (n >> 5)];
-      return r;
+  if constexpr (MODE == EP_GRAD_MX) {
+    const uint8_t* p = (const uint8_t*)e.Z + m * e.ldz + n;
+    if (whole) {
+      const ep_u32x2 v = *(const ep_u32x2_u*)p;
+      r.lo = (ep_u32x4){v[0], v[1], 0, 0};
+    } else if constexpr (PART) {
+      r.lo = ep_raw_part<1>(p, nv, 0);
     }
-  } else {
+    r.lo[2] = e.S[m * e.lds + (n >> 5)];
+    return r;
+  } else if constexpr (MODE == EP_FORWARD) {
     if (!e.R) return r;
     if (a.c_kind == C_F32) {
       const float* p = (const float*)e.R + m * e.ldr + n;
@@ -302,7 +306,7 @@ __device__ __forceinline__ EpRaw ep_fetch8(const GemmEpArgs& a, int64_t m, int n
       return r;
     }
   }
-  const uint16_t* p = GRAD ? (const uint16_t*)e.Z + m * e.ldz + n : (const uint16_t*)e.R + m * e.ldr + n;
+  const uint16_t* p = MODE != EP_FORWARD ? (const uint16_t*)e.Z + m * e.ldz + n : (const uint16_t*)e.R + m * e.ldr + n;
   if (whole)
     r.lo = *(const ep_u32x4_2*)p;
   else if constexpr (PART)
@@ -327,14 +331,14 @@ __device__ __forceinline__ void ep_raw_f32(const EpRaw& r, float (&v)[8]) {
 
 // w = alpha * product, b = the bias of these columns (zeros without one).  The four lanes of a
 // block of 32 columns call it together.  A gradient's unrounded results are added to cs.
-template <bool NT, bool GRAD, int ACT, bool PART>
+template <bool NT, int MODE, int ACT, bool PART>
 __device__ __forceinline__ void ep_finish8(const GemmEpArgs& a, float (&w)[8], const EpRaw& r, const float (&b)[8],
                                            int64_t m, int n, int nv, float (&cs)[8]) {
   const EpArgs& e = a.ep;
   float v[8];
-  if constexpr (GRAD) {
+  if constexpr (MODE != EP_FORWARD) {
     if (nv == 0) return;
-    if (e.z_kind == Z_MX)
+    if constexpr (MODE == EP_GRAD_MX)
       ep_codes8(r.lo[0], r.lo[1], r.lo[2], v);
     else
       ep_raw_bf16(r, v);
@@ -374,13 +378,16 @@ __device__ __forceinline__ void ep_bias8(const GemmEpArgs& a, int n, int nv, flo
   if (!a.ep.grad && a.ep.bias) ep_load8(a.ep.bias, n, a.ep.bias_f32, nv, b);
 }
 
-// f(bool_constant<grad>, integral_constant<int, act>) for the call's epilogue
+// f(integral_constant<int, mode>, integral_constant<int, act>) for the call's epilogue
 template <class F>
 __device__ __forceinline__ void ep_dispatch(const EpArgs& e, F&& f) {
-  if (e.grad)
-    ep_with_act(e.act, [&](auto ac) EP_INLINE { f(std::true_type{}, ac); });
+  auto with = [&](auto mc) EP_INLINE { ep_with_act(e.act, [&](auto ac) EP_INLINE { f(mc, ac); }); };
+  if (!e.grad)
+    with(std::integral_constant<int, EP_FORWARD>{});
+  else if (e.z_kind == Z_MX)
+    with(std::integral_constant<int, EP_GRAD_MX>{});
   else
-    ep_with_act(e.act, [&](auto ac) EP_INLINE { f(std::false_type{}, ac); });
+    with(std::integral_constant<int, EP_GRAD_BF16>{});
 }
 
 }  // namespace

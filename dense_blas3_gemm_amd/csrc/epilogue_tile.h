@@ -49,13 +49,13 @@ __device__ __forceinline__ void ep_tile(const GemmEpArgs& a, const typename AccO
   const float alpha = a.alpha;
   float cs[8] = {}, b[8];
   ep_bias8(a, n, nvc, b);
-  ep_dispatch(a.ep, [&](auto gc, auto ac) EP_INLINE {
-    constexpr bool GRAD = decltype(gc)::value;
+  ep_dispatch(a.ep, [&](auto mc, auto ac) EP_INLINE {
+    constexpr int MODE = decltype(mc)::value;
     constexpr int ACT = decltype(ac)::value;
     EpRaw raw[BATCH];
     auto fetch = [&](int step) EP_INLINE {
       const int m = m0 + row + step * RPS;
-      return ep_fetch8<GRAD, false>(a, m, n, step < ALL && m < a.M ? nvc : 0);
+      return ep_fetch8<MODE, false>(a, m, n, step < ALL && m < a.M ? nvc : 0);
     };
 #pragma unroll
     for (int s = 0; s < BATCH; ++s) raw[s] = fetch(s);
@@ -80,7 +80,7 @@ __device__ __forceinline__ void ep_tile(const GemmEpArgs& a, const typename AccO
           const f32x4 lo = *(__attribute__((address_space(3))) f32x4*)(uintptr_t)(at + ((ch ^ x) * 16));
           const f32x4 hi = *(__attribute__((address_space(3))) f32x4*)(uintptr_t)(at + (((ch + 1) ^ x) * 16));
           float w[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-          ep_finish8<NT, GRAD, ACT, false>(a, w, raw[s], b, m, n, m < a.M ? nvc : 0, cs);
+          ep_finish8<NT, MODE, ACT, false>(a, w, raw[s], b, m, n, m < a.M ? nvc : 0, cs);
           raw[s] = fetch(h * STEPS + s0 + s + BATCH);
         }
       }

@@ -458,13 +458,13 @@ __global__ __launch_bounds__(C::THREADS) void split_reduce_ep_kernel(GemmEpArgs 
   ep_bias8(a, n, nvc, b);
   const f32x4* src = (const f32x4*)(a.ws + (size_t)tile * a.splits * (C::BM * C::BN)) + i * C::FN * C::THREADS + t;
   constexpr size_t stride = (size_t)C::FM * C::FN * C::THREADS;  // float4s per partial
-  ep_dispatch(a.ep, [&](auto gc, auto ac) EP_INLINE {
-    constexpr bool GRAD = decltype(gc)::value;
+  ep_dispatch(a.ep, [&](auto mc, auto ac) EP_INLINE {
+    constexpr int MODE = decltype(mc)::value;
     EpRaw raw[STEPS];
 #pragma unroll
     for (int s = 0; s < STEPS; ++s) {
       const int m = row_of(s * RPS + row);
-      raw[s] = ep_fetch8<GRAD, false>(a, m, n, m < a.M ? nvc : 0);
+      raw[s] = ep_fetch8<MODE, false>(a, m, n, m < a.M ? nvc : 0);
     }
     if (row_of(wm * 16) < a.M) {  // (this wave's rows past M hold no sums)
       f32x4 v[C::FN];
@@ -489,7 +489,7 @@ __global__ __launch_bounds__(C::THREADS) void split_reduce_ep_kernel(GemmEpArgs 
       const f32x4 lo = *(__attribute__((address_space(3))) f32x4*)(uintptr_t)(at + ((ch ^ (r & 15)) * 16));
       const f32x4 hi = *(__attribute__((address_space(3))) f32x4*)(uintptr_t)(at + (((ch + 1) ^ (r & 15)) * 16));
       float w[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-      ep_finish8<false, GRAD, decltype(ac)::value, false>(a, w, raw[s], b, m, n, m < a.M ? nvc : 0, cs);
+      ep_finish8<false, MODE, decltype(ac)::value, false>(a, w, raw[s], b, m, n, m < a.M ? nvc : 0, cs);
     }
   });
   if (a.ep.grad && a.ep.colsum) ep_put_colsum<C::THREADS, C::BN>(a, cs, (int64_t)tm * C::FM + i, n0, t, lds0);

@@ -75,7 +75,9 @@ __global__ __launch_bounds__(WAVES * 64) void gemm_skinny_kernel(GemmEpArgs a) {
   const int nv = t < OUT && om < a.M && on < a.N ? 8 : 0;
   float bias[8];
   ep_bias8(a, on, nv, bias);
-  const EpRaw raw = a.ep.grad ? ep_fetch8<true, false>(a, om, on, nv) : ep_fetch8<false, false>(a, om, on, nv);
+  const EpRaw raw = !a.ep.grad                ? ep_fetch8<EP_FORWARD, false>(a, om, on, nv)
+                    : a.ep.z_kind == Z_MX ? ep_fetch8<EP_GRAD_MX, false>(a, om, on, nv)
+                                          : ep_fetch8<EP_GRAD_BF16, false>(a, om, on, nv);
 
   const __amdgpu_buffer_rsrc_t ra = make_rsrc(a.A, (uint32_t)(a.M * a.lda * C::ES));
   const __amdgpu_buffer_rsrc_t rb =
@@ -202,8 +204,8 @@ __global__ __launch_bounds__(WAVES * 64) void gemm_skinny_kernel(GemmEpArgs a) {
     float w[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) w[i] = a.alpha * sums[om * P::LDR + (t % LPR) * 8 + i];
-    ep_dispatch(a.ep, [&](auto gc, auto ac) EP_INLINE {
-      ep_finish8<false, decltype(gc)::value, decltype(ac)::value, false>(a, w, raw, bias, om, on, nv, cs);
+    ep_dispatch(a.ep, [&](auto mc, auto ac) EP_INLINE {
+      ep_finish8<false, decltype(mc)::value, decltype(ac)::value, false>(a, w, raw, bias, om, on, nv, cs);
     });
   }
   if (a.ep.grad && a.ep.colsum) {  // every row is here: the column sums themselves

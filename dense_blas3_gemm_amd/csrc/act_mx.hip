@@ -40,10 +40,11 @@ RowGrid row_grid(int64_t rows, int64_t cols, int64_t max_wgs, int max_parts) {
 }
 
 // The workgroup's column sums: this thread's eight, added over the rows of threads through LDS,
-// as one row of `part` per row of workgroups.  Every thread calls it (n >= cols: no columns).
-__device__ __forceinline__ void put_partial(float* part, int64_t cols, int64_t n, float (&cs)[8]) {
+// as one row of `part`, of whole eights, per row of workgroups; or, from a single row of them,
+// the sums themselves into `out`.  Every thread calls it (n >= cols: no columns).
+__device__ __forceinline__ void put_partial(float* part, float* out, int64_t cols, int64_t n, float (&cs)[8]) {
   __shared__ float s[8][kThreads];
-  if (!part) return;
+  if (!part && !out) return;
   if (blockDim.y > 1) {
     const int t = threadIdx.y * blockDim.x + threadIdx.x;
 #pragma unroll
@@ -54,7 +55,11 @@ __device__ __forceinline__ void put_partial(float* part, int64_t cols, int64_t n
 #pragma unroll
       for (int i = 0; i < 8; ++i) cs[i] += s[i][y * blockDim.x + t];
   }
-  if (n < cols) ep_store8<false>(part + (int64_t)blockIdx.y * cols + n, cols - n < 8 ? (int)(cols - n) : 8, cs);
+  if (n >= cols) return;
+  if (out)
+    ep_store8<false>(out + n, cols - n < 8 ? (int)(cols - n) : 8, cs);
+  else
+    ep_store8<false>(part + (int64_t)blockIdx.y * whole8(cols) + n, 8, cs);
 }
 
 // Epilogue of a product in fp32 (the path of operands that the fused kernels do not take).
@@ -72,7 +77,7 @@ __global__ __launch_bounds__(kThreads) void ep_rows_kernel(GemmEpArgs a, int64_t
       ep_finish8<false, decltype(mc)::value, decltype(ac)::value, true>(a, w, r, b, m, n, nv, cs);
     }
   });
-  put_partial(a.ep.colsum, a.N, n64, cs);
+  put_partial(a.ep.colsum, nullptr, a.N, n64, cs);
 }
 
 // Sums of the partial rows: 64 columns to a workgroup, four to a thread, the rows dealt to 64
@@ -86,16 +91,11 @@ __global__ __launch_bounds__(16 * kSumGroups) void colsum_kernel(const float* sr
   if (!out) return;
   const int l = threadIdx.x & 15, g = threadIdx.x >> 4;
   const int64_t n = (int64_t)blockIdx.x * 64 + l * 4;
-  const float* p = src + blockIdx.y * cols + n;
+  const float* p = src + blockIdx.y * (ld / 2) + n;
   ep_f32x4 v = {0.f, 0.f, 0.f, 0.f};
-  if (n + 4 <= cols) {
+  if (n < cols) {
 #pragma unroll 4
     for (int r = g; r < parts; r += kSumGroups) v += *(const ep_f32x4_u*)(p + (int64_t)r * ld);
-  } else {
-    for (int r = g; r < parts; r += kSumGroups)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (n + i < cols) v[i] += p[(int64_t)r * ld + i];
   }
   *(ep_f32x4*)&s[g][l * 4] = v;
   __syncthreads();
@@ -127,15 +127,38 @@ __global__ __launch_bounds__(kThreads) void act_mx_kernel(int64_t rows, int64_t 
   }
 }
 
+// eight halves without the first k (0 < k < 8), zeros behind the rest
+__device__ __forceinline__ ep_u32x4 drop_halves(ep_u32x4 v, int k) {
+  uint64_t lo = (uint64_t)v[1] << 32 | v[0], hi = (uint64_t)v[3] << 32 | v[2];
+  if (k >= 4) {
+    lo = hi;
+    hi = 0;
+    k -= 4;
+  }
+  if (k > 0) {
+    lo = lo >> (16 * k) | hi << (64 - 16 * k);
+    hi >>= 16 * k;
+  }
+  return (ep_u32x4){(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+}
+
 // Backward from the checkpoint, kAhead rows of a thread at a time: their loads go out together.
+// ODD: cols is no multiple of 8; the others' kernel has no path of partial eights in its rows
+// (2047 x 5000 with GELU and all outputs 23 us, with that path 27).
 constexpr int kAhead = 4;
+template <bool ODD>
 __global__ __launch_bounds__(kThreads) void act_grad_mx_kernel(int64_t rows, int64_t cols, int act, const uint8_t* q,
                                                                int64_t ldq, const uint8_t* sc, int64_t ldsc,
                                                                const uint16_t* dh, int64_t lddh, uint16_t* dz,
-                                                               int64_t lddz, uint16_t* h, int64_t ldh, float* part) {
+                                                               int64_t lddz, uint16_t* h, int64_t ldh, float* part,
+                                                               float* dbias) {
   const int64_t n = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * 8;
-  const int nv = cols - n < 8 ? (cols > n ? (int)(cols - n) : 0) : 8;
+  const int nv = cols <= n ? 0 : ODD && cols - n < 8 ? (int)(cols - n) : 8;
   if (nv == 0) rows = 0;  // (a thread past the columns)
+  // the last columns of an odd row come with the seven or fewer before them, in loads as wide
+  // as the others' (a row of fewer than eight columns takes them one by one)
+  const int back = ODD && cols >= 8 ? 8 - nv : 0;
+  const bool whole = !ODD || cols >= 8;
   const int64_t step = (int64_t)gridDim.y * blockDim.y;
   float cs[8] = {};
   ep_with_act(act, [&](auto ac) EP_INLINE {
@@ -147,14 +170,14 @@ __global__ __launch_bounds__(kThreads) void act_grad_mx_kernel(int64_t rows, int
         const int64_t m = m0 + j * step;
         const bool live = m < rows;
         codes[j] = d[j] = (ep_u32x4){0, 0, 0, 0};
-        if (live && nv == 8) {
-          const ep_u32x2 w = *(const ep_u32x2_u*)(q + m * ldq + n);
+        if (live && whole) {
+          const ep_u32x2 w = *(const ep_u32x2_u*)(q + m * ldq + n - back);
           codes[j] = (ep_u32x4){w[0], w[1], sc[m * ldsc + (n >> 5)], 0};
-          if (dh) d[j] = *(const ep_u32x4_2*)(dh + m * lddh + n);
-        } else if (live) {
-          codes[j] = ep_raw_part<1>(q + m * ldq + n, nv, 0);
+          if (dh) d[j] = *(const ep_u32x4_2*)(dh + m * lddh + n - back);
+        } else if (ODD && live) {
+          codes[j] = ep_raw_part<1>(q + m * ldq + n, nv);
           codes[j][2] = sc[m * ldsc + (n >> 5)];
-          if (dh) d[j] = ep_raw_part<2>(dh + m * lddh + n, nv, 0);
+          if (dh) d[j] = ep_raw_part<2>(dh + m * lddh + n, nv);
         }
       }
 #pragma unroll
@@ -162,6 +185,12 @@ __global__ __launch_bounds__(kThreads) void act_grad_mx_kernel(int64_t rows, int
         const int64_t m = m0 + j * step;
         if (m >= rows) break;
         float z[8], g[8];
+        if (ODD && back) {
+          const uint64_t w = ((uint64_t)codes[j][1] << 32 | codes[j][0]) >> (8 * back);
+          codes[j][0] = (uint32_t)w;
+          codes[j][1] = (uint32_t)(w >> 32);
+          d[j] = drop_halves(d[j], back);
+        }
         ep_codes8(codes[j][0], codes[j][1], codes[j][2], z);
         if (dh) {
           EpRaw r;
@@ -170,19 +199,19 @@ __global__ __launch_bounds__(kThreads) void act_grad_mx_kernel(int64_t rows, int
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             g[i] *= ep_slope<ACT>(z[i]);
-            cs[i] += i < nv ? g[i] : 0.f;
+            cs[i] += !ODD || i < nv ? g[i] : 0.f;
           }
-          if (dz) ep_store8<true>(dz + m * lddz + n, nv, g);
+          if (dz) ep_store8<true, ODD>(dz + m * lddz + n, nv, g);
         }
         if (h) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) z[i] = ep_act<ACT>(z[i]);
-          ep_store8<true>(h + m * ldh + n, nv, z);
+          ep_store8<true, ODD>(h + m * ldh + n, nv, z);
         }
       }
     }
   });
-  put_partial(part, cols, n, cs);
+  put_partial(part, dbias, cols, n, cs);
 }
 
 }  // namespace
@@ -216,9 +245,11 @@ hipError_t launch_act_grad_mx(int64_t rows, int64_t cols, int act, const uint8_t
   const RowGrid g = row_grid(rows, cols, 2048, dbias ? max_parts : 0);
   // a single row of workgroups has the sums themselves
   *parts = g.grid.y > 1 ? (int)g.grid.y : 0;
-  float* colsum = !dbias ? nullptr : *parts ? part : dbias;
-  hipLaunchKernelGGL(act_grad_mx_kernel, g.grid, g.block, 0, s, rows, cols, act, q, ldq, sc, ldsc,
-                     (const uint16_t*)dh, lddh, (uint16_t*)dz, lddz, (uint16_t*)h, ldh, colsum);
+  const bool partial = dbias && *parts;
+  const auto kernel = cols % 8 ? act_grad_mx_kernel<true> : act_grad_mx_kernel<false>;
+  hipLaunchKernelGGL(kernel, g.grid, g.block, 0, s, rows, cols, act, q, ldq, sc, ldsc,
+                     (const uint16_t*)dh, lddh, (uint16_t*)dz, lddz, (uint16_t*)h, ldh, partial ? part : nullptr,
+                     partial ? nullptr : dbias);
   return hipGetLastError();
 }
 

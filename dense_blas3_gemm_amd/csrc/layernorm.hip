@@ -318,8 +318,9 @@ __global__ __launch_bounds__(MAXT) void layernorm_grad_kernel(NormArgs a) {
     // and team 0 adds them in order
     __shared__ float t8[8 * 1024];
     // (a single workgroup has the sums themselves)
-    float* const out[2] = {gridDim.x > 1 ? a.part + (int64_t)blockIdx.x * 2 * a.cols : a.dgamma,
-                           gridDim.x > 1 ? a.part + ((int64_t)blockIdx.x * 2 + 1) * a.cols : a.dbeta};
+    const bool one = gridDim.x == 1;
+    float* const out[2] = {one ? a.dgamma : a.part + (int64_t)blockIdx.x * 2 * whole8(a.cols),
+                           one ? a.dbeta : a.part + ((int64_t)blockIdx.x * 2 + 1) * whole8(a.cols)};
     auto put = [&](float (&v)[8], int c, int set) {
       if (blockDim.y > 1) {
         __syncthreads();
@@ -332,7 +333,7 @@ __global__ __launch_bounds__(MAXT) void layernorm_grad_kernel(NormArgs a) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] += t8[i * 1024 + k * m.T + m.t];
       }
-      if (threadIdx.y == 0 && nv[c] > 0 && out[set]) ep_store8<false>(out[set] + col[c], nv[c], v);
+      if (threadIdx.y == 0 && nv[c] > 0 && out[set]) ep_store8<false>(out[set] + col[c], one ? nv[c] : 8, v);
     };
 #pragma unroll
     for (int c = 0; c < CPT; ++c) {
@@ -432,10 +433,10 @@ __global__ __launch_bounds__(256) void layernorm_dw_kernel(NormArgs a) {
     }
   }
   const bool one = gridDim.y == 1;  // (the sums themselves)
-  float* og = one ? a.dgamma : a.part + (int64_t)blockIdx.y * 2 * a.cols;
-  float* ob = one ? a.dbeta : a.part + ((int64_t)blockIdx.y * 2 + 1) * a.cols;
-  if (og) ep_store8<false>(og + col, nv, dg);
-  if (ob) ep_store8<false>(ob + col, nv, db);
+  float* og = one ? a.dgamma : a.part + (int64_t)blockIdx.y * 2 * whole8(a.cols);
+  float* ob = one ? a.dbeta : a.part + ((int64_t)blockIdx.y * 2 + 1) * whole8(a.cols);
+  if (og) ep_store8<false>(og + col, one ? nv : 8, dg);
+  if (ob) ep_store8<false>(ob + col, one ? nv : 8, db);
 }
 
 // Threads of a team for rows of `cols` columns at `cpt` chunks of 8 to a thread: whole waves, or

@@ -76,7 +76,7 @@ gemm_status_t run_by_rows(const HandleView& v, GemmEpArgs a, int transA, int tra
   if (step > (1 << 21)) step = 1 << 21;  // the generic product's grid
   if (step >= 256) step -= step % 256;   // blocks of rows keep the operands' alignment
   if (step > M) step = M;
-  const int mp = dbias ? max_parts(v, a.N) : 1;
+  const int mp = dbias ? max_parts(v, whole8(a.N)) : 1;
   if (step < 1 || mp < 1) return GEMM_STATUS_NOT_SUPPORTED;
   float* part = (float*)v.ws;
   float* w = (float*)((char*)v.ws + kPartBytes);
@@ -99,7 +99,7 @@ gemm_status_t run_by_rows(const HandleView& v, GemmEpArgs a, int transA, int tra
     a.ep.colsum = dbias ? part : nullptr;
     int parts = 0;
     err = launch_ep_rows(a, ldw, mp, &parts, v.stream);
-    if (err == hipSuccess && dbias) err = launch_colsum(part, parts, a.N, a.N, dbias, nullptr, m0 > 0, v.stream);
+    if (err == hipSuccess && dbias) err = launch_colsum(part, parts, whole8(a.N), a.N, dbias, nullptr, m0 > 0, v.stream);
     if (err != hipSuccess) return GEMM_STATUS_LAUNCH_FAILED;
   }
   return GEMM_STATUS_SUCCESS;
@@ -319,12 +319,12 @@ gemm_status_t gemm_act_grad_mx(gemm_handle_t h, int64_t rows, int64_t cols, int 
   if (empty)
     return dbias && cols > 0 ? status(launch_colsum(nullptr, 0, cols, cols, dbias, nullptr, 0, v.stream))
                              : GEMM_STATUS_SUCCESS;
-  const int mp = dbias ? max_parts(v, cols) : 1;
+  const int mp = dbias ? max_parts(v, whole8(cols)) : 1;
   if (mp < 1) return GEMM_STATUS_NOT_SUPPORTED;
   int parts = 0;
   hipError_t e = launch_act_grad_mx(rows, cols, act, (const uint8_t*)codes, ld_codes, scales, ld_scales, dout, ld_dout,
                                     dz, ld_dz, out, ld_out, dbias, (float*)v.ws, mp, &parts, v.stream);
-  if (e == hipSuccess && parts) e = launch_colsum((const float*)v.ws, parts, cols, cols, dbias, nullptr, 0, v.stream);
+  if (e == hipSuccess && parts) e = launch_colsum((const float*)v.ws, parts, whole8(cols), cols, dbias, nullptr, 0, v.stream);
   return status(e);
 }
 
@@ -377,10 +377,10 @@ gemm_status_t gemm_layernorm_grad(gemm_handle_t h, int64_t rows, int64_t cols, c
   // the sums' two sets of columns in one launch: the first output carries dgamma
   float* const part = (float*)v.ws;
   auto add_up = [&](int parts) {
-    return launch_colsum(part, parts, 2 * cols, cols, dgamma, dbeta, 0, v.stream);
+    return launch_colsum(part, parts, 2 * whole8(cols), cols, dgamma, dbeta, 0, v.stream);
   };
   if (rows == 0) return sums ? status(add_up(0)) : GEMM_STATUS_SUCCESS;
-  const int mp = sums ? max_parts(v, 2 * cols) : 0;
+  const int mp = sums ? max_parts(v, 2 * whole8(cols)) : 0;
   if (sums && mp < 1) return GEMM_STATUS_NOT_SUPPORTED;
   NormArgs a{};
   a.rows = rows;

@@ -62,9 +62,14 @@ hipError_t launch_skinny(const GemmEpArgs& a, hipStream_t s);
 // most max_parts >= 1).
 hipError_t launch_ep_rows(const GemmEpArgs& a, int64_t ldw, int max_parts, int* parts, hipStream_t s);
 
+// Columns of a partial row: whole eights, so that the kernels on both sides move whole vectors
+// (the columns past the end hold nothing of use).
+constexpr int64_t whole8(int64_t cols) { return (cols + 7) / 8 * 8; }
+
 // out0[n] <- (accumulate ? out0[n] : 0) + sum over p < parts of src[p * ld + n], n < cols, and
-// the same for out1 (or null) from column cols on; added in an order fixed by parts: the
-// same bits every run.  parts == 0 writes zeros.
+// the same for out1 (or null) from column ld / 2 on; added in an order fixed by parts: the
+// same bits every run.  parts == 0 writes zeros.  A row of src (each half of one) holds
+// whole8(cols) columns.
 hipError_t launch_colsum(const float* src, int parts, int64_t ld, int64_t cols, float* out0, float* out1,
                          int accumulate, hipStream_t s);
 

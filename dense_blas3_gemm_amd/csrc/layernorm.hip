@@ -321,15 +321,23 @@ __global__ __launch_bounds__(MAXT) void layernorm_grad_kernel(NormArgs a) {
     const bool one = gridDim.x == 1;
     float* const out[2] = {one ? a.dgamma : a.part + (int64_t)blockIdx.x * 2 * whole8(a.cols),
                            one ? a.dbeta : a.part + ((int64_t)blockIdx.x * 2 + 1) * whole8(a.cols)};
+    // the teams of one wave by exchange, then a row of sums per wave (or team) through LDS: added
+    // up by the first team alone, 32 teams of 16 lanes took a microsecond (27214 x 128: 13.6, so 12.4)
+    const unsigned rows = m.T < 64 ? (blockDim.y * m.T + 63) / 64 : blockDim.y;
+    const unsigned mine_row = m.T < 64 ? (threadIdx.y * m.T + m.t) >> 6 : threadIdx.y;
+    const bool lead = m.T >= 64 || (threadIdx.y * m.T) % 64 == 0;
     auto put = [&](float (&v)[8], int c, int set) {
-      if (blockDim.y > 1) {
-        __syncthreads();
-        if (threadIdx.y > 0)
+      for (int o = m.T; o < 64; o <<= 1)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) t8[i * 1024 + threadIdx.y * m.T + m.t] = v[i];
+        for (int i = 0; i < 8; ++i) v[i] += __shfl_xor(v[i], o);
+      if (rows > 1) {
+        __syncthreads();
+        if (lead && mine_row > 0)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) t8[i * 1024 + mine_row * m.T + m.t] = v[i];
         __syncthreads();
         if (threadIdx.y == 0)
-          for (unsigned k = 1; k < blockDim.y; ++k)
+          for (unsigned k = 1; k < rows; ++k)
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] += t8[i * 1024 + k * m.T + m.t];
       }
@@ -465,8 +473,11 @@ hipError_t grad(const NormArgs& a, int max_parts, int* parts, hipStream_t s) {
   const unsigned T = team_threads(a.cols, CPT);
   unsigned teams = T < wg ? wg / T : 1;
   const bool few = SUMS && a.rows <= (int64_t)teams * R * 2;  // two rounds of one workgroup, no second launch
-  // else spread the rows over the CUs (a workgroup stays whole waves)
-  while (!few && teams > 1 && teams * T > 64 && (int64_t)teams * R * 256 > a.rows) teams = (teams + 1) / 2;
+  // else spread the rows over the CUs (a workgroup stays whole waves); with sums of two chunks, one
+  // workgroup to a CU, as long as that stays one round of them (1681 x 1488: 14.1 us, so 12.4)
+  while (!few && teams > 1 && teams * T > 64 && (int64_t)teams * R * 256 > a.rows &&
+         !(SUMS && CPT > 1 && (int64_t)((teams + 1) / 2) * R * 256 < a.rows))
+    teams = (teams + 1) / 2;
   const int64_t need = (a.rows + (int64_t)teams * R - 1) / ((int64_t)teams * R);
   // With the weights' sums one workgroup to a CU: a partial row more per CU costs more (its
   // write and its read) than a second workgroup's overlap gains, 128.4 against 136.6 us at

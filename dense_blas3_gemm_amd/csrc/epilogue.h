@@ -35,6 +35,11 @@ __device__ __forceinline__ uint16_t ep_f32bf(float v) {
   return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
 }
 
+// The last columns of a row that is no multiple of eight: one by one, or (fewer accesses, more
+// registers: the layer norm kernels of wide rows spilled) in pieces of four, two and one; none
+// where the host sees to it that there are no such columns.
+enum EpPart { EP_NONE = 0, EP_ONES = 1, EP_PIECES = 2 };
+
 // The first nv < 8 elements of ES bytes at p, zeros behind them: four, two and one of them in
 // one access each (an access per element cost the last lane of an odd row, and so its wave,
 // most of the time: 59881 x 671 from codes 155 us, now 61, against 51 at 672 columns).
@@ -81,18 +86,22 @@ __device__ __forceinline__ ep_u32x4 ep_raw_part(const void* p, int nv) {
 }
 
 // 8 elements at p, the first nv of them valid (the others read as zeros).
+template <int PART = EP_ONES>
 __device__ __forceinline__ void ep_load8(const uint16_t* p, int nv, float (&v)[8]) {
   if (nv == 8) {
     const ep_u16x8 w = *(const ep_u16x8_u*)p;
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = ep_bf16f(w[i]);
-  } else {
+  } else if constexpr (PART == EP_PIECES) {
     const ep_u32x4 w = ep_raw_part<2>(p, nv);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       v[2 * i] = __builtin_bit_cast(float, w[i] << 16);
       v[2 * i + 1] = __builtin_bit_cast(float, w[i] & 0xFFFF0000u);
     }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < nv ? ep_bf16f(p[i]) : 0.f;
   }
 }
 __device__ __forceinline__ void ep_load8(const float* p, int nv, float (&v)[8]) {
@@ -104,26 +113,8 @@ __device__ __forceinline__ void ep_load8(const float* p, int nv, float (&v)[8]) 
       v[4 + i] = b[i];
     }
   } else {
-    ep_f32x4 a = {0.f, 0.f, 0.f, 0.f}, t = a;
-    if (nv & 4) {
-      a = *(const ep_f32x4_u*)p;
-      p += 4;
-    }
-    if (nv & 2) {
-      t[0] = p[0];
-      t[1] = p[1];
-      p += 2;
-    }
-    if (nv & 1) {
-      const float one = *p;
-      t[0] = nv & 2 ? t[0] : one;
-      t[2] = nv & 2 ? one : 0.f;
-    }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[i] = nv & 4 ? a[i] : t[i];
-      v[4 + i] = nv & 4 ? t[i] : 0.f;
-    }
+    for (int i = 0; i < 8; ++i) v[i] = i < nv ? p[i] : 0.f;
   }
 }
 // 8 elements of a matrix of either type
@@ -135,8 +126,8 @@ __device__ __forceinline__ void ep_load8(const void* p, int64_t idx, int f32, in
 }
 
 // The whole-vector stores of large outputs are non-temporal (NT): the kernel does not read
-// them again.  PART = false: nv is 8 or 0 (columns in whole eights), here and below.
-template <bool NT, bool PART = true>
+// them again.
+template <bool NT, int PART = EP_ONES>
 __device__ __forceinline__ void ep_store8(uint16_t* p, int nv, const float (&v)[8]) {
   if (nv == 8) {
     ep_u16x8 w;
@@ -146,7 +137,11 @@ __device__ __forceinline__ void ep_store8(uint16_t* p, int nv, const float (&v)[
       __builtin_nontemporal_store(w, (ep_u16x8_u*)p);
     else
       *(ep_u16x8_u*)p = w;
-  } else if constexpr (PART) {  // four, two and one of them
+  } else if constexpr (PART == EP_ONES) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < nv) p[i] = ep_f32bf(v[i]);
+  } else if constexpr (PART == EP_PIECES) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[i] = ep_f32bf(v[2 * i]) | (uint32_t)ep_f32bf(v[2 * i + 1]) << 16;
@@ -164,7 +159,7 @@ __device__ __forceinline__ void ep_store8(uint16_t* p, int nv, const float (&v)[
     if (nv & 1) *p = (uint16_t)w[0];
   }
 }
-template <bool NT, bool PART = true>
+template <bool NT, int PART = EP_ONES>
 __device__ __forceinline__ void ep_store8(float* p, int nv, const float (&v)[8]) {
   if (nv == 8) {
     const ep_f32x4 a = {v[0], v[1], v[2], v[3]}, b = {v[4], v[5], v[6], v[7]};
@@ -175,7 +170,11 @@ __device__ __forceinline__ void ep_store8(float* p, int nv, const float (&v)[8])
       *(ep_f32x4_u*)p = a;
       *(ep_f32x4_u*)(p + 4) = b;
     }
-  } else if constexpr (PART) {
+  } else if constexpr (PART == EP_ONES) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < nv) p[i] = v[i];
+  } else if constexpr (PART == EP_PIECES) {
     float a = v[0], b = v[1], c = v[2];
     if (nv & 4) {
       *(ep_f32x4_u*)p = (ep_f32x4){v[0], v[1], v[2], v[3]};
@@ -193,7 +192,7 @@ __device__ __forceinline__ void ep_store8(float* p, int nv, const float (&v)[8])
     if (nv & 1) *p = a;
   }
 }
-template <bool NT, bool PART = true>
+template <bool NT, int PART = EP_ONES>
 __device__ __forceinline__ void ep_store8(void* p, int64_t idx, int f32, int nv, const float (&v)[8]) {
   if (f32)
     ep_store8<NT, PART>((float*)p + idx, nv, v);
@@ -431,7 +430,7 @@ __device__ __forceinline__ void ep_finish8(const GemmEpArgs& a, float (&w)[8], c
       ep_store_mx<PART>(v, nv, (n & 31) == 0, (uint8_t*)e.Z + m * e.ldz + n, e.S + m * e.lds + (n >> 5));
     }
     if (nv == 0) return;
-    if (e.z_kind == Z_BF16) ep_store8<NT, PART>((uint16_t*)e.Z + m * e.ldz + n, nv, w);
+    if (e.z_kind == Z_BF16) ep_store8<NT, PART ? EP_PIECES : EP_NONE>((uint16_t*)e.Z + m * e.ldz + n, nv, w);
 #pragma unroll
     for (int i = 0; i < 8; ++i) w[i] = ep_act<ACT>(w[i]);
     if (e.R) {
@@ -443,7 +442,7 @@ __device__ __forceinline__ void ep_finish8(const GemmEpArgs& a, float (&w)[8], c
       for (int i = 0; i < 8; ++i) w[i] += e.beta * v[i];
     }
   }
-  ep_store8<NT, PART>(a.C, m * a.ldc + n, a.c_kind == C_F32, nv, w);
+  ep_store8<NT, PART ? EP_PIECES : EP_NONE>(a.C, m * a.ldc + n, a.c_kind == C_F32, nv, w);
 }
 
 // the bias of columns [n, n + 8)

@@ -248,19 +248,30 @@ hipError_t launch_rows(const GemmEpArgs& a, hipStream_t s) {
 
 }  // namespace
 
-// Where this kernel is the faster one (us here / us of the tiled kernels with split-K, bf16):
-// against B [N][K] up to 32 rows (16 x 5120 x 5120 10.5 / 16.9, 32 rows 12.0 / 16.9, 64 rows
-// 15.7 / 17.2), unless a few workgroups would walk a long K (16 x 1344 x 19696: 32 / 18); against
-// B [K][N], whose columns an XCD finds on some of its L2's channels only, up to 16 rows and K
-// not past N (4096 x 4096 11.4 / 12.4, 20480 x 5120 53.6 / 59.7, but 2048 x 8192 19.1 / 12.8),
-// small ones up to 32 rows (512 x 5120 9.0 / 11.5).  E4M3: up to 64 rows (the tiled kernels for
-// it reach 64 rows at 64 x 5120 x 5120 in 17 us, this one 13.0 and 17.4 for the two layouts).
-bool skinny_serves(int in_fp8, int transA, int transB, int64_t M, int64_t N, int64_t K) {
-  if (transA) return false;
-  const bool small = N * K <= (4 << 20);
-  if (in_fp8) return M <= 64 && (small || K <= 8192 || N >= K / 4);
-  if (transB) return M <= 32 && (K <= 8192 || N >= K / 4);
-  return small ? M <= 32 : M <= 16 && K <= N;
+// Where this kernel is the faster one: up to some K, past which a workgroup's waves walk too
+// long and the tiled kernels' split of K wins.  Measured both ways on 24557 products of 1 to 64
+// rows, N and K from 256 to 20480; time of the tiled kernels over this one's, N under / from 1500:
+//
+//                      K < 1024      1024-2048     2048-4096     4096-8192     8192 on
+//   bf16 [N][K] M<=16  1.51 / 1.38   2.00 / 1.64   1.83 / 1.54   1.52 / 1.38   0.94 / 1.13
+//               M<=32  1.52 / 1.28   1.81 / 1.37   1.55 / 1.29   1.20 / 1.11   0.68 / 0.89
+//               M<=64  1.29 / 1.07   1.42 / 1.12   1.13 / 1.09   0.83 / 0.92   0.48 / 0.72
+//   bf16 [K][N] M<=16  1.44 / 1.24   1.83 / 1.34   1.45 / 1.12   1.03 / 0.99   0.63 / 0.84
+//               M<=32  1.38 / 1.05   1.60 / 1.18   1.18 / 1.04   0.77 / 0.88   0.50 / 0.74
+//               M<=64  1.24 / 0.95   1.32 / 0.96   0.98 / 0.86   0.64 / 0.75   0.39 / 0.63
+//   E4M3 [N][K] M<=16  1.42 / 1.38   1.80 / 1.71   1.74 / 1.74   1.50 / 1.69   1.09 / 1.47
+//               M<=32  1.39 / 1.21   1.62 / 1.43   1.51 / 1.44   1.24 / 1.35   0.87 / 1.14
+//               M<=64  1.20 / 0.99   1.28 / 1.11   1.09 / 1.05   0.82 / 0.98   0.54 / 0.84
+//   E4M3 [K][N] M<=16  1.57 / 1.39   1.87 / 1.52   1.62 / 1.38   1.12 / 1.21   0.73 / 0.99
+//               M<=32  1.47 / 1.15   1.66 / 1.29   1.38 / 1.16   0.99 / 1.05   0.64 / 0.88
+//               M<=64  1.27 / 1.02   1.32 / 1.07   1.03 / 0.93   0.72 / 0.84   0.49 / 0.71
+//
+// (In B [K][N] an XCD finds its columns on some of its L2's channels only.)  With these limits the
+// choice is 1.7 % slower than the better of the two in the mean.
+bool skinny_serves(int in_fp8, int transA, int transB, int64_t M, int64_t K) {
+  constexpr int64_t most[2][2][3] = {{{6144, 3072, 2048}, {12288, 8192, 4096}},   // bf16: B [K][N], [N][K]
+                                     {{8192, 6144, 2560}, {20480, 12288, 5120}}};  // E4M3
+  return !transA && M <= 64 && K <= most[in_fp8 != 0][transB != 0][M <= 16 ? 0 : M <= 32 ? 1 : 2];
 }
 
 hipError_t launch_skinny(const GemmEpArgs& a, hipStream_t s) {

@@ -144,7 +144,7 @@ bool run_fused(const HandleView& v, GemmEpArgs a, int transA, int transB, int dt
   a.in_fp8 = pr.in_fp8;
   a.transA = transA;
   a.transB = transB;
-  if (skinny_serves(a.in_fp8, transA, transB, a.M, a.N, a.K)) {
+  if (skinny_serves(a.in_fp8, transA, transB, a.M, a.K)) {
     a.ep.colsum = dbias;
     *st = status(launch_skinny(a, v.stream));
     return true;

@@ -52,7 +52,7 @@ DBGEMM_EP_DECL(11)
 
 // Products of a few rows, N a multiple of 8, operands as the MFMA kernels take them; ep.colsum,
 // when set, receives the column sums themselves.
-bool skinny_serves(int in_fp8, int transA, int transB, int64_t M, int64_t N, int64_t K);
+bool skinny_serves(int in_fp8, int transA, int transB, int64_t M, int64_t K);
 hipError_t launch_skinny(const GemmEpArgs& a, hipStream_t s);
 
 // ---- launchers (they return hipSuccess or the launch error)

@@ -119,6 +119,12 @@ hipError_t run_tiles(const HandleView& v, GemmEpArgs a, const Policy& p, int sp,
   return launch_mfma_ep(p, a, parts, v.stream);
 }
 
+// the partial rows of column sums that run_tiles leaves: a row of waves each, or after a split
+// a row of fragments
+int64_t partial_rows(const Policy& p, int64_t M, int sp) {
+  return (M + p.BM - 1) / p.BM * (sp > 1 ? p.BM / p.WM / 16 : p.WM);
+}
+
 // a's rows [m0, m0 + M) and columns [n0, n0 + N); n0 a multiple of 32.
 GemmEpArgs part_of(const GemmEpArgs& a, int64_t m0, int64_t n0, int64_t M, int64_t N) {
   GemmEpArgs r = a;
@@ -170,9 +176,9 @@ bool run_fused(const HandleView& v, GemmEpArgs a, int transA, int transB, int dt
   }
   float* part = nullptr;
   if (dbias) {
-    // at most one partial row per 16 rows of C, whole tiles of at most 256 rows in each launch
-    const int64_t most = ((int64_t)a.M + 2 * 256) / 16 * a.N * (int64_t)sizeof(float);
-    if (!v.ws || v.ws_bytes < kPartBytes + (size_t)most) return false;
+    const int64_t floats = partial_rows(policy_at(idx), a1.M, sp) * a1.N +
+                           (cut.p >= 0 ? partial_rows(policy_at(idx2), a2.M, sp2) * a2.N : 0);
+    if (!v.ws || v.ws_bytes < kPartBytes + (size_t)floats * sizeof(float)) return false;
     part = a1.ep.colsum = (float*)((char*)v.ws + kPartBytes);
   }
   int parts = 0, parts2 = 0;

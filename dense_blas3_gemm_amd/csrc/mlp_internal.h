@@ -29,7 +29,7 @@ struct EpArgs {
   int64_t ldz;
   uint8_t* S;  // Z_MX: ceil(N / 32) scale bytes per row
   int64_t lds;
-  float* colsum;  // grad: fp32 partial sums, [part][N], or null
+  float* colsum;  // grad: fp32 partial sums, [part][whole8(N)], or null
 };
 
 // A product with an epilogue: the kernels take this in place of GemmArgs.

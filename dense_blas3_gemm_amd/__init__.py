@@ -15,6 +15,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 # DBGEMM_LIB selects another build of the same library (the sanitized host-only build the
 # CPU tests run under AddressSanitizer)
 LIB_PATH = os.environ.get("DBGEMM_LIB") or os.path.join(PKG, "libdbgemm.so")
+BINDING_PATH = os.path.join(PKG, "_binding.so")
 
 OP_N, OP_T = 0, 1
 BF16_F32, BF16_BF16, E4M3_BF16, E4M3_F32, MXE4M3_BF16, MXE4M3_F32, E4M3_E4M3, MXE4M3_E4M3 = range(8)
@@ -48,8 +49,8 @@ class Epilogue(ctypes.Structure):
 
 
 _lib = None
-# set when the library is loaded: device index -> raw handle of torch's current stream there,
-# and the native part of the binding (with torch only)
+# device index -> raw handle of torch's current stream there (set when the library is loaded, with
+# torch only), and the native part of the binding (loaded by the first call that goes through it)
 _RAW_STREAM, _NATIVE = [], []
 
 
@@ -137,23 +138,33 @@ def load_library():
                "gemm_trsm", "gemm_run_act", "gemm_run_dact", "gemm_act_mx", "gemm_act_grad_mx", "gemm_layernorm",
                "gemm_layernorm_grad"]:
         getattr(lib, fn).restype = i32
-    if _RAW_STREAM:
-        _load_native()
     _lib = lib
     return lib
 
 
 def _load_native():
-    """Loads the native part of the binding on the library just loaded; raises if it is missing."""
-    path = os.path.join(PKG, "_binding.so")
-    if not os.path.exists(path):
-        raise RuntimeError(f"{path} is missing: build it with `python -m dense_blas3_gemm_amd.build`")
+    """Loads the native part of the binding (the MLP-block operators' torch side) beside the library
+    and returns it; RuntimeError where it cannot be had.  The other calls do without it."""
+    load_library()
+    if not _RAW_STREAM:
+        raise RuntimeError("the MLP-block operators take torch tensors: torch is not installed")
+    if not os.path.exists(BINDING_PATH):
+        raise RuntimeError(f"{BINDING_PATH} is missing: build it with `python -m dense_blas3_gemm_amd.build`")
     import importlib.util
-    spec = importlib.util.spec_from_file_location(__name__ + "._binding", path)
-    native = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(native)
+    spec = importlib.util.spec_from_file_location(__name__ + "._binding", BINDING_PATH)
+    try:
+        native = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(native)
+    except ImportError as e:
+        raise RuntimeError(f"{BINDING_PATH} does not load with this torch ({e}): build it again with "
+                           "`python -m dense_blas3_gemm_amd.build`") from e
     native.bind(LIB_PATH)
     _NATIVE[:] = [native]
+    return native
+
+
+def _native():
+    return _NATIVE[0] if _NATIVE else _load_native()
 
 
 def version() -> str:
@@ -432,7 +443,7 @@ class Gemm:
         A and B bf16 or float8_e4m3fn, C bf16 or float32, bias (N values) bf16 or float32,
         residual of C's type (C itself allowed); act one of ACTS.  Z is left in `z`: bf16, or
         with z_scales (uint8 [M][ceil(N/32)]) block-scaled E4M3 codes (float8_e4m3fn or uint8)."""
-        st = _NATIVE[0].run_act(self._follow(), self.device, A, B, C, transA, transB, alpha, act, bias, residual, beta,
+        st = _native().run_act(self._follow(), self.device, A, B, C, transA, transB, alpha, act, bias, residual, beta,
                                 z, z_scales)
         if st != 0:
             raise GemmError("gemm_run_act", st)
@@ -442,14 +453,14 @@ class Gemm:
                  act: str = "none", dbias=None):
         """C <- (alpha*op(A)*op(B)) * act'(z); dbias (float32, N values) its column sums
         (gemm_run_dact).  z as run_act or act_mx left it."""
-        st = _NATIVE[0].run_dact(self._follow(), self.device, A, B, C, z, z_scales, transA, transB, alpha, act, dbias)
+        st = _native().run_dact(self._follow(), self.device, A, B, C, z, z_scales, transA, transB, alpha, act, dbias)
         if st != 0:
             raise GemmError("gemm_run_dact", st)
         return C
 
     def act_mx(self, z, out, codes, scales, act: str = "none"):
         """out <- act(z) and z's block-scaled E4M3 checkpoint (gemm_act_mx); z and out bf16."""
-        st = _NATIVE[0].act_mx(self._follow(), self.device, z, out, codes, scales, act)
+        st = _native().act_mx(self._follow(), self.device, z, out, codes, scales, act)
         if st != 0:
             raise GemmError("gemm_act_mx", st)
         return out
@@ -457,7 +468,7 @@ class Gemm:
     def act_grad_mx(self, codes, scales, act: str = "none", dh=None, dz=None, dbias=None, h=None):
         """From the checkpoint: dz <- dh * act'(z), dbias (float32) its column sums, h <- act(z)
         (gemm_act_grad_mx); dh, dz and h bf16, each output optional."""
-        st = _NATIVE[0].act_grad_mx(self._follow(), self.device, codes, scales, act, dh, dz, dbias, h)
+        st = _native().act_grad_mx(self._follow(), self.device, codes, scales, act, dh, dz, dbias, h)
         if st != 0:
             raise GemmError("gemm_act_grad_mx", st)
         return dz
@@ -465,7 +476,7 @@ class Gemm:
     def layernorm(self, x, y, gamma=None, beta=None, eps: float = 1e-5, mean=None, rstd=None):
         """y <- layer norm of x's rows, times gamma plus beta (gemm_layernorm); mean and rstd
         (float32, one per row) receive the statistics."""
-        st = _NATIVE[0].layernorm(self._follow(), self.device, x, y, gamma, beta, eps, mean, rstd)
+        st = _native().layernorm(self._follow(), self.device, x, y, gamma, beta, eps, mean, rstd)
         if st != 0:
             raise GemmError("gemm_layernorm", st)
         return y
@@ -473,7 +484,7 @@ class Gemm:
     def layernorm_grad(self, dy, x, mean, rstd, dx, gamma=None, dgamma=None, dbeta=None, residual=None):
         """dx <- the gradient of layernorm at x (+ residual), dgamma and dbeta (float32) those
         of its weights (gemm_layernorm_grad)."""
-        st = _NATIVE[0].layernorm_grad(self._follow(), self.device, dy, x, mean, rstd, dx, gamma, dgamma, dbeta,
+        st = _native().layernorm_grad(self._follow(), self.device, dy, x, mean, rstd, dx, gamma, dgamma, dbeta,
                                        residual)
         if st != 0:
             raise GemmError("gemm_layernorm_grad", st)

@@ -88,12 +88,15 @@ BINDING = os.path.join(PKG, "_binding.so")
 
 def _build_binding(incremental: bool = False) -> None:
     """The native part of the Python binding (csrc/binding.cpp): host code against torch's and
-    Python's headers."""
+    Python's headers.  Nothing to build where torch is missing: its calls take torch tensors."""
     src = os.path.join(CSRC, "binding.cpp")
     if incremental and not _stale("binding.cpp", BINDING):
         return
     import sysconfig
-    import torch
+    try:
+        import torch
+    except ImportError:
+        return
     root = os.path.dirname(torch.__file__)
     cmd = ["g++", "-O2", "-fPIC", "-shared", "-std=c++17", "-Wall", "-Wno-cast-function-type",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", "-I", INCLUDE, "-isystem",
@@ -121,14 +124,14 @@ def _write_build_info() -> None:
 
 
 def build(verbose: bool = False, incremental: bool = False) -> str:
-    """Compiles every translation unit (only the stale ones with `incremental`) and links."""
+    """Compiles every translation unit (only the stale ones with `incremental`) and links; then
+    raises if the binding beside the library could not be built."""
     os.makedirs(BUILD, exist_ok=True)
     # the slowest translation units first, so that they start at once
     order = sorted(SOURCES, key=lambda e: not e[0].startswith("kernel_mfma"))
     with cf.ThreadPoolExecutor(max_workers=min(len(SOURCES), os.cpu_count() or 8)) as ex:
         binding = ex.submit(_build_binding, incremental)
         objs = list(ex.map(lambda e: _compile(e, incremental), order))
-        binding.result()
     tmp = OUT + ".tmp"
     cmd = [HIPCC, "-shared", "-fPIC", f"--offload-arch={ARCH}", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -136,6 +139,7 @@ def build(verbose: bool = False, incremental: bool = False) -> str:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, OUT)
     _write_build_info()
+    binding.result()  # (the library does not depend on it: linked first)
     if verbose:
         print(f"built {OUT}")
     return OUT

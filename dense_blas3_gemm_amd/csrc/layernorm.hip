@@ -1,6 +1,7 @@
 // Layer norm and its gradient, fp32 statistics.
 //
-//   forward   mu = mean(x), r = 1 / sqrt(mean((x - mu)^2) + eps), y = (x - mu) r gamma + beta
+//   forward   mu = mean(x), r = 1 / sqrt(mean((x - mu)^2) + eps), y = (x - mu) r gamma + beta;
+//             with m the fp32 number next to mu and d = mu - m: mean((x - mu)^2) = mean((x - m)^2) - d^2
 //   gradient  xh = (x - mu) r, g = dy gamma,
 //             dx = r (g - mean(g) - xh mean(g xh)) [+ dr],
 //             dgamma = sum over rows of dy xh, dbeta = sum over rows of dy
@@ -23,13 +24,15 @@ __device__ __forceinline__ void ln_store(void* p, int64_t i, int kind, float v) 
     ((uint16_t*)p)[i] = ep_f32bf(v);
 }
 
-__device__ __forceinline__ float wave_sum(float v) {
+template <class T>
+__device__ __forceinline__ T wave_sum(T v) {
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
   return v;
 }
 // over the 8, 16 or 32 lanes of a part of a wave
-__device__ __forceinline__ float lanes_sum(float v, int lanes) {
+template <class T>
+__device__ __forceinline__ T lanes_sum(T v, int lanes) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1)
     if (o < lanes) v += __shfl_xor(v, o);
@@ -68,6 +71,32 @@ __device__ __forceinline__ void raw_load(Raw8<T>& r, const T* p, int nv) {
   }
 }
 
+// The mean of a row from its sum: m and d = mu - m.  Sums of fp32 rows are taken in 64 bits: in 32 a
+// constant row is one or more units from its own mean, all columns alike, and normalises to +-0.02
+// at 1000.1 and to +-1 at 1e6 + 0.3 where it is 0; in 64 its mean is exact and d = 0.  Sums of up to
+// 2^15 bf16 values of one size are exact in fp32 (8 bits each), and others have a spread that its
+// rounding does not show in: d is 0 there (in 64 bits 16384 x 5120 took 69 us, with d 63, so 59).
+struct Mean {
+  float m, d;
+  __device__ Mean(double sum, int cols) {
+    const double mu = sum / cols;
+    m = (float)mu;
+    d = (float)(mu - m);
+    d = d == d ? d : 0.f;  // (an infinite mean)
+  }
+  __device__ Mean(float sum, int cols) : m(sum / (float)cols), d(0.f) {}
+};
+template <class X>
+using RowSum = std::conditional_t<sizeof(X) == 2, float, double>;
+__device__ __forceinline__ float row_rstd(float sq, float n, float d, float eps) {
+  return 1.0f / __builtin_sqrtf(sq / n - d * d + eps);
+}
+// (x - m) r as (x - mu) r
+template <class X>
+__device__ __forceinline__ float row_norm(float v, float rs, float off) {
+  return sizeof(X) == 2 ? v * rs : v * rs + off;
+}
+
 // ---- the row kernels.  A team of blockDim.x threads (whole waves, or for narrow rows 8, 16 or
 // 32 lanes of one) holds a row in registers:
 // thread t its columns 8 (t + c blockDim.x) .. + 7 for c < CPT.  blockDim.y teams make up a
@@ -83,11 +112,12 @@ struct Team {
         first_wave(threadIdx.y * (blockDim.x >> 6)) {}
 };
 
-// Sums over the team of V values per thread, the same in every thread.  s: 2 x 16 x V floats,
-// its two halves used in turn: the barrier of the use between two of one half keeps them
-// apart.  Every team of the workgroup calls it together.
-template <int V>
-__device__ __forceinline__ void team_sum(const Team& m, float (&v)[V], float* s, int& half) {
+// Sums over the team of V values per thread, the same in every thread.  s: two halves of 16 x V
+// values (of the widest V and T), used in turn: the barrier of the use between two of one half
+// keeps them apart.  Every team of the workgroup calls it together.
+template <int V, class T, int BYTES>
+__device__ __forceinline__ void team_sum(const Team& m, T (&v)[V], char (&s)[BYTES], int& half) {
+  static_assert(16 * V * sizeof(T) <= BYTES / 2, "a half holds it");
   if (m.waves == 0) {  // (uniform over the workgroup, and so is the next)
 #pragma unroll
     for (int i = 0; i < V; ++i) v[i] = lanes_sum(v[i], m.T);
@@ -96,24 +126,31 @@ __device__ __forceinline__ void team_sum(const Team& m, float (&v)[V], float* s,
 #pragma unroll
   for (int i = 0; i < V; ++i) v[i] = wave_sum(v[i]);
   if (m.waves == 1) return;
-  float* h = s + half * 16 * V;
+  T* h = (T*)(s + half * (BYTES / 2));
   half ^= 1;
   if ((m.t & 63) == 0)
 #pragma unroll
     for (int i = 0; i < V; ++i) h[(m.first_wave + m.wave) * V + i] = v[i];
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < V; ++i) v[i] = 0.f;
+  for (int i = 0; i < V; ++i) v[i] = 0;
   for (int w = 0; w < m.waves; ++w)
 #pragma unroll
     for (int i = 0; i < V; ++i) v[i] += h[(m.first_wave + w) * V + i];
 }
 
+// Waves to a SIMD that the registers have to leave room for: three workgroups of five waves to a CU
+// (5120 columns) take five on one SIMD.  (Left to the compiler, fp32 rows take 106-108 registers.)
+template <class X, int CPT, int R, int MAXT>
+constexpr int fwd_waves() {
+  return sizeof(X) == 4 && CPT == 2 && R == 1 && MAXT == 512 ? 5 : 1;
+}
+
 // Forward: reads x once, writes y once.  Bound by those bytes.
 template <class X, class Y, int CPT, int R, int MAXT>
-__global__ __launch_bounds__(MAXT) void layernorm_kernel(NormArgs a) {
+__global__ __launch_bounds__(MAXT, (fwd_waves<X, CPT, R, MAXT>())) void layernorm_kernel(NormArgs a) {
   constexpr bool kWide = CPT >= 4;
-  __shared__ float s[2 * 16 * R];
+  __shared__ __attribute__((aligned(16))) char s[2 * 16 * R * sizeof(RowSum<X>)];
   const Team m;
   int half = 0;
   const X* x = (const X*)a.x;
@@ -149,25 +186,29 @@ __global__ __launch_bounds__(MAXT) void layernorm_kernel(NormArgs a) {
   // (the workgroup's teams run the same number of rounds: they share the barriers)
   for (int64_t r0 = (int64_t)blockIdx.x * blockDim.y * R; r0 < a.rows; r0 += step) {
     const int64_t r = r0 + (mine - (int64_t)blockIdx.x * blockDim.y * R);
-    float v[R][CPT][8], mu[R], q[R];
+    float v[R][CPT][8], q[R];
+    RowSum<X> sum[R];
     if constexpr (kWide) load(r);
 #pragma unroll
     for (int j = 0; j < R; ++j) {
-      mu[j] = 0.f;
+      sum[j] = 0;
 #pragma unroll
       for (int c = 0; c < CPT; ++c)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           v[j][c][i] = in[j][c].get(i);
-          mu[j] += v[j][c][i];
+          sum[j] += v[j][c][i];
         }
     }
     if constexpr (!kWide)
       if (r0 + step < a.rows) load(r + step);
-    team_sum<R>(m, mu, s, half);
+    team_sum(m, sum, s, half);
+    float mu[R], d[R];
 #pragma unroll
     for (int j = 0; j < R; ++j) {
-      mu[j] /= n;  // (a constant row's mean is exact)
+      const Mean mean(sum[j], a.cols);
+      mu[j] = mean.m;
+      d[j] = mean.d;
       q[j] = 0.f;
 #pragma unroll
       for (int c = 0; c < CPT; ++c)
@@ -177,17 +218,18 @@ __global__ __launch_bounds__(MAXT) void layernorm_kernel(NormArgs a) {
           q[j] += i < nv[c] ? v[j][c][i] * v[j][c][i] : 0.f;
         }
     }
-    team_sum<R>(m, q, s, half);
+    team_sum(m, q, s, half);
 #pragma unroll
     for (int j = 0; j < R; ++j) {
       if (r + j >= a.rows) continue;
-      const float rs = 1.0f / __builtin_sqrtf(q[j] / n + a.eps);
+      const float rs = row_rstd(q[j], n, d[j], a.eps), off = -d[j] * rs;
 #pragma unroll
       for (int c = 0; c < CPT; ++c) {
         if (nv[c] == 0) continue;
         if constexpr (kWide) weights(c, g[0], b[0]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[j][c][i] = v[j][c][i] * rs * g[kWide ? 0 : c][i] + b[kWide ? 0 : c][i];
+        for (int i = 0; i < 8; ++i)
+          v[j][c][i] = row_norm<X>(v[j][c][i], rs, off) * g[kWide ? 0 : c][i] + b[kWide ? 0 : c][i];
         ep_store8<true>(y + (r + j) * a.ldy + col[c], nv[c], v[j][c]);
       }
       if (m.t == 0) {
@@ -206,7 +248,7 @@ __global__ __launch_bounds__(MAXT) void layernorm_grad_kernel(NormArgs a) {
   constexpr bool kWide = CPT >= 4;
   static_assert(!(kWide && SUMS), "no registers for the sums of a wide row");
   constexpr bool kAhead = !kWide && (CPT == 1 || MAXT <= 512);  // the next rows' loads ahead
-  __shared__ float s[2 * 16 * 2 * R];
+  __shared__ __attribute__((aligned(16))) char s[2 * 16 * 2 * R * sizeof(float)];
   const Team m;
   int half = 0;
   const X* x = (const X*)a.x;
@@ -289,7 +331,7 @@ __global__ __launch_bounds__(MAXT) void layernorm_grad_kernel(NormArgs a) {
     }
     if constexpr (kAhead)
       if (r0 + step < a.rows) load(r + step);
-    team_sum<2 * R>(m, c12, s, half);
+    team_sum(m, c12, s, half);
 #pragma unroll
     for (int j = 0; j < R; ++j) {
       if (r + j >= a.rows) continue;
@@ -357,7 +399,8 @@ __global__ __launch_bounds__(MAXT) void layernorm_grad_kernel(NormArgs a) {
 
 // ---- rows too wide for the registers of a workgroup
 // Sums of two values over a workgroup of 256 threads, the same in every thread.
-__device__ __forceinline__ void group_sum(float& u, float& v, float (*s)[2]) {
+template <class T>
+__device__ __forceinline__ void group_sum(T& u, T& v, T (*s)[2]) {
   u = wave_sum(u);
   v = wave_sum(v);
   __syncthreads();  // the previous use of s is over
@@ -372,20 +415,23 @@ __device__ __forceinline__ void group_sum(float& u, float& v, float (*s)[2]) {
 
 // One workgroup to a row, which is read three times (any width).
 __global__ __launch_bounds__(256) void layernorm_rows_kernel(NormArgs a) {
-  __shared__ float s[4][2];
+  __shared__ double s[4][2];
   for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
-    float sum = 0.f, none = 0.f, sq = 0.f;
+    double sum = 0.0, sq = 0.0, none = 0.0;
     for (int i = threadIdx.x; i < a.cols; i += 256) sum += ln_load(a.x, r * a.ldx + i, a.x_kind);
     group_sum(sum, none, s);
-    const float mu = sum / (float)a.cols;
+    const Mean mean(sum, a.cols);
+    const float mu = mean.m;
+    float q = 0.f;
     for (int i = threadIdx.x; i < a.cols; i += 256) {
       const float d = ln_load(a.x, r * a.ldx + i, a.x_kind) - mu;
-      sq += d * d;
+      q += d * d;
     }
+    sq = q;
     group_sum(sq, none, s);
-    const float rs = 1.0f / __builtin_sqrtf(sq / (float)a.cols + a.eps);
+    const float rs = row_rstd((float)sq, (float)a.cols, mean.d, a.eps), off = -mean.d * rs;
     for (int i = threadIdx.x; i < a.cols; i += 256) {
-      float v = (ln_load(a.x, r * a.ldx + i, a.x_kind) - mu) * rs;
+      float v = (ln_load(a.x, r * a.ldx + i, a.x_kind) - mu) * rs + off;
       if (a.gamma) v *= ln_load(a.gamma, i, a.w_kind);
       if (a.beta) v += ln_load(a.beta, i, a.w_kind);
       ln_store(a.y, r * a.ldy + i, a.y_kind, v);

@@ -416,21 +416,22 @@ __device__ __forceinline__ void group_sum(T& u, T& v, T (*s)[2]) {
 // One workgroup to a row, which is read three times (any width).
 __global__ __launch_bounds__(256) void layernorm_rows_kernel(NormArgs a) {
   __shared__ double s[4][2];
+  const uint32_t cols = (uint32_t)a.cols;  // (up to 2^31 - 1: an int index would pass its end by one step)
   for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
     double sum = 0.0, sq = 0.0, none = 0.0;
-    for (int i = threadIdx.x; i < a.cols; i += 256) sum += ln_load(a.x, r * a.ldx + i, a.x_kind);
+    for (uint32_t i = threadIdx.x; i < cols; i += 256) sum += ln_load(a.x, r * a.ldx + i, a.x_kind);
     group_sum(sum, none, s);
     const Mean mean(sum, a.cols);
     const float mu = mean.m;
     float q = 0.f;
-    for (int i = threadIdx.x; i < a.cols; i += 256) {
+    for (uint32_t i = threadIdx.x; i < cols; i += 256) {
       const float d = ln_load(a.x, r * a.ldx + i, a.x_kind) - mu;
       q += d * d;
     }
     sq = q;
     group_sum(sq, none, s);
     const float rs = row_rstd((float)sq, (float)a.cols, mean.d, a.eps), off = -mean.d * rs;
-    for (int i = threadIdx.x; i < a.cols; i += 256) {
+    for (uint32_t i = threadIdx.x; i < cols; i += 256) {
       float v = (ln_load(a.x, r * a.ldx + i, a.x_kind) - mu) * rs + off;
       if (a.gamma) v *= ln_load(a.gamma, i, a.w_kind);
       if (a.beta) v += ln_load(a.beta, i, a.w_kind);
@@ -446,10 +447,11 @@ __global__ __launch_bounds__(256) void layernorm_rows_kernel(NormArgs a) {
 // dx: one workgroup to a row, read twice.
 __global__ __launch_bounds__(256) void layernorm_dx_kernel(NormArgs a) {
   __shared__ float s[4][2];
+  const uint32_t cols = (uint32_t)a.cols;
   for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
     const float mu = a.mean[r], rs = a.rstd[r];
     float c1 = 0.f, c2 = 0.f;
-    for (int i = threadIdx.x; i < a.cols; i += 256) {
+    for (uint32_t i = threadIdx.x; i < cols; i += 256) {
       float g = ln_load(a.dy, r * a.lddy + i, a.y_kind);
       if (a.gamma) g *= ln_load(a.gamma, i, a.w_kind);
       c1 += g;
@@ -458,7 +460,7 @@ __global__ __launch_bounds__(256) void layernorm_dx_kernel(NormArgs a) {
     group_sum(c1, c2, s);
     c1 /= (float)a.cols;
     c2 /= (float)a.cols;
-    for (int i = threadIdx.x; i < a.cols; i += 256) {
+    for (uint32_t i = threadIdx.x; i < cols; i += 256) {
       float g = ln_load(a.dy, r * a.lddy + i, a.y_kind);
       if (a.gamma) g *= ln_load(a.gamma, i, a.w_kind);
       const float xh = (ln_load(a.x, r * a.ldx + i, a.x_kind) - mu) * rs;

@@ -122,6 +122,14 @@ float number(PyObject* o) {
   }
   return (float)v;
 }
+int flag(PyObject* o, const char* name) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) {
+    PyErr_Clear();
+    throw BadType(std::string(name) + " has to be a flag");
+  }
+  return v;
+}
 // (a handle's address and a device index, integers from the package itself)
 gemm_handle_t handle(PyObject* o) {
   if (!PyLong_Check(o)) throw BadType("a handle's address is wanted");
@@ -142,8 +150,8 @@ Product product(PyObject* oa, PyObject* ob, PyObject* oc, PyObject* ta, PyObject
   const at::Tensor &A = needed(oa, "A"), &B = needed(ob, "B"), &C = needed(oc, "C");
   if (A.dim() != 2 || B.dim() != 2 || C.dim() != 2) throw Bad("A, B and C have to be matrices");
   Product p;
-  p.tA = PyObject_IsTrue(ta) != 0;
-  p.tB = PyObject_IsTrue(tb) != 0;
+  p.tA = flag(ta, "transA");
+  p.tB = flag(tb, "transB");
   p.M = C.size(0);
   p.N = C.size(1);
   p.K = A.size(p.tA ? 0 : 1);

@@ -216,6 +216,8 @@ PyObject* run_act(PyObject*, PyObject* const* a, Py_ssize_t n) {
       e.ld_z = k.z.ld;
       e.z_scales = (uint8_t*)k.s.p;
       e.ld_z_scales = k.s.ld;
+    } else if (a[13] != Py_None) {
+      throw Bad("z_scales without z");
     }
     const gemm_handle_t h = handle(a[0]);
     const float alpha = number(a[7]);

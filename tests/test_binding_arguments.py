@@ -20,6 +20,13 @@ def test_arguments_in_order():
     assert run_act() == run_act(z=z) == run_act(z=q, z_scales=s) == run_act(transA=True, transB=1) == NOT_INITIALIZED
 
 
+def test_scales_without_codes_are_refused():
+    """(the checkpoint would not be written)"""
+    import torch
+    with pytest.raises(ValueError, match="z"):
+        run_act(z_scales=torch.zeros(32, 1, dtype=torch.uint8))
+
+
 @pytest.mark.parametrize("name", ["transA", "transB"])
 def test_a_flag_without_a_truth_value(name):
     import torch

@@ -50,8 +50,20 @@ class Epilogue(ctypes.Structure):
 
 _lib = None
 # device index -> raw handle of torch's current stream there (set when the library is loaded, with
-# torch only), and the native part of the binding (loaded by the first call that goes through it)
-_RAW_STREAM, _NATIVE = [], []
+# torch only)
+_RAW_STREAM = []
+
+
+class _Unloaded:
+    """Stands for the native part of the binding until the first call that goes through it."""
+
+    def __getattr__(self, name):
+        if name.startswith("__"):
+            raise AttributeError(name)
+        return getattr(_load_native(), name)
+
+
+_native = _Unloaded()
 
 
 class GemmError(RuntimeError):
@@ -145,6 +157,7 @@ def load_library():
 def _load_native():
     """Loads the native part of the binding (the MLP-block operators' torch side) beside the library
     and returns it; RuntimeError where it cannot be had.  The other calls do without it."""
+    global _native
     load_library()
     if not _RAW_STREAM:
         raise RuntimeError("the MLP-block operators take torch tensors: torch is not installed")
@@ -159,12 +172,8 @@ def _load_native():
         raise RuntimeError(f"{BINDING_PATH} does not load with this torch ({e}): build it again with "
                            "`python -m dense_blas3_gemm_amd.build`") from e
     native.bind(LIB_PATH)
-    _NATIVE[:] = [native]
+    _native = native
     return native
-
-
-def _native():
-    return _NATIVE[0] if _NATIVE else _load_native()
 
 
 def version() -> str:
@@ -443,8 +452,8 @@ class Gemm:
         A and B bf16 or float8_e4m3fn, C bf16 or float32, bias (N values) bf16 or float32,
         residual of C's type (C itself allowed); act one of ACTS.  Z is left in `z`: bf16, or
         with z_scales (uint8 [M][ceil(N/32)]) block-scaled E4M3 codes (float8_e4m3fn or uint8)."""
-        st = _native().run_act(self._follow(), self.device, A, B, C, transA, transB, alpha, act, bias, residual, beta,
-                                z, z_scales)
+        st = _native.run_act(self._follow(), self.device, A, B, C, transA, transB, alpha, act, bias, residual, beta,
+                             z, z_scales)
         if st != 0:
             raise GemmError("gemm_run_act", st)
         return C
@@ -453,14 +462,14 @@ class Gemm:
                  act: str = "none", dbias=None):
         """C <- (alpha*op(A)*op(B)) * act'(z); dbias (float32, N values) its column sums
         (gemm_run_dact).  z as run_act or act_mx left it."""
-        st = _native().run_dact(self._follow(), self.device, A, B, C, z, z_scales, transA, transB, alpha, act, dbias)
+        st = _native.run_dact(self._follow(), self.device, A, B, C, z, z_scales, transA, transB, alpha, act, dbias)
         if st != 0:
             raise GemmError("gemm_run_dact", st)
         return C
 
     def act_mx(self, z, out, codes, scales, act: str = "none"):
         """out <- act(z) and z's block-scaled E4M3 checkpoint (gemm_act_mx); z and out bf16."""
-        st = _native().act_mx(self._follow(), self.device, z, out, codes, scales, act)
+        st = _native.act_mx(self._follow(), self.device, z, out, codes, scales, act)
         if st != 0:
             raise GemmError("gemm_act_mx", st)
         return out
@@ -468,7 +477,7 @@ class Gemm:
     def act_grad_mx(self, codes, scales, act: str = "none", dh=None, dz=None, dbias=None, h=None):
         """From the checkpoint: dz <- dh * act'(z), dbias (float32) its column sums, h <- act(z)
         (gemm_act_grad_mx); dh, dz and h bf16, each output optional."""
-        st = _native().act_grad_mx(self._follow(), self.device, codes, scales, act, dh, dz, dbias, h)
+        st = _native.act_grad_mx(self._follow(), self.device, codes, scales, act, dh, dz, dbias, h)
         if st != 0:
             raise GemmError("gemm_act_grad_mx", st)
         return dz
@@ -476,7 +485,7 @@ class Gemm:
     def layernorm(self, x, y, gamma=None, beta=None, eps: float = 1e-5, mean=None, rstd=None):
         """y <- layer norm of x's rows, times gamma plus beta (gemm_layernorm); mean and rstd
         (float32, one per row) receive the statistics."""
-        st = _native().layernorm(self._follow(), self.device, x, y, gamma, beta, eps, mean, rstd)
+        st = _native.layernorm(self._follow(), self.device, x, y, gamma, beta, eps, mean, rstd)
         if st != 0:
             raise GemmError("gemm_layernorm", st)
         return y
@@ -484,7 +493,7 @@ class Gemm:
     def layernorm_grad(self, dy, x, mean, rstd, dx, gamma=None, dgamma=None, dbeta=None, residual=None):
         """dx <- the gradient of layernorm at x (+ residual), dgamma and dbeta (float32) those
         of its weights (gemm_layernorm_grad)."""
-        st = _native().layernorm_grad(self._follow(), self.device, dy, x, mean, rstd, dx, gamma, dgamma, dbeta,
+        st = _native.layernorm_grad(self._follow(), self.device, dy, x, mean, rstd, dx, gamma, dgamma, dbeta,
                                        residual)
         if st != 0:
             raise GemmError("gemm_layernorm_grad", st)

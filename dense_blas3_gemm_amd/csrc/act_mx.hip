@@ -8,7 +8,7 @@
 // fixed order (no atomics: the same bits every run).
 //
 // Bound by memory (8192 x 20480 with SiLU and codes: 159 us for 844 MB, 5.3 TB/s); a gradient
-// with GELU (erf) by its arithmetic too (2047 x 5000 with all outputs and the sums' launch 22 us
+// with GELU (erf) by its arithmetic too (2047 x 5000 with all outputs and the sums' launch 22.8 us
 // for 72 MB).
 #include "epilogue.h"
 
@@ -19,8 +19,9 @@ constexpr int kThreads = 256;
 
 // Threads along the columns (whole blocks of 32 columns: 4 neighbouring threads), rows of
 // threads of a workgroup, and the grid: at most max_wgs workgroups.  With partial rows (at most
-// max_parts, one per row of workgroups) a workgroup takes 16 rows or more, as long as that
-// leaves 128 workgroups: a partial row is written and read again.
+// max_parts, one per row of workgroups) there are no more rows of workgroups than eighths of the
+// matrix's rows or, where those are fewer, than make 512 workgroups: a partial row is written and
+// read again.
 struct RowGrid {
   dim3 grid, block;
 };

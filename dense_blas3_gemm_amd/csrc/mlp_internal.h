@@ -101,7 +101,7 @@ struct NormArgs {
   int64_t lddy;
   const void* dr;  // grad: added to dx (x's type), or null
   int64_t lddr;
-  float* part;  // grad: partial sums of dgamma and dbeta, [part][2][cols], or null
+  float* part;  // grad: partial sums of dgamma and dbeta, [part][2][whole8(cols)], or null
   float* dgamma;  // grad: the sums themselves, either may be null
   float* dbeta;
 };

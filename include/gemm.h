@@ -262,7 +262,9 @@ gemm_status_t gemm_lds_probe(gemm_handle_t h, int kind, const uint32_t* offsets,
 gemm_status_t gemm_hw_probe(gemm_handle_t h, int kind, int param, int iters, int workgroups,
                             const void* src, int64_t src_bytes, unsigned long long* cycles);
 
-/* The policy table: count and names (index 0 .. count-1).  Out-of-range -> NULL. */
+/* The policy table: count and names (index 0 .. count-1).  Out-of-range -> NULL.  Names that
+ * begin with "ep_" are tiles of products with an epilogue only (gemm_run_act, gemm_run_dact, which
+ * choose them by themselves): gemm_run under one returns NOT_SUPPORTED. */
 int gemm_policy_count(void);
 const char* gemm_policy_name(int index);
 
@@ -442,7 +444,8 @@ gemm_status_t gemm_act_grad_mx(gemm_handle_t h, int64_t rows, int64_t cols, int 
 /* Layer norm of each row:  mu = mean(x), r = 1 / sqrt(mean((x - mu)^2) + eps),
  * y <- (x - mu) * r * gamma + beta.  x and y bf16 or fp32 each; gamma and beta (cols values
  * of weight_type) may be NULL (1 and 0).  mean and rstd receive mu and r (one fp32 per row)
- * for the gradient, or are NULL.  eps finite and >= 0.  y may be x (same type and stride). */
+ * for the gradient, or are NULL.  eps finite and >= 0.  y may be x (same type and stride).
+ * A constant row gives beta where eps > 0.  rows == 0 or cols == 0: nothing is written. */
 gemm_status_t gemm_layernorm(gemm_handle_t h, int64_t rows, int64_t cols, const void* x, int64_t ld_x, int x_type,
                              const void* gamma, const void* beta, int weight_type, float eps, void* y, int64_t ld_y,
                              int y_type, float* mean, float* rstd);
@@ -452,7 +455,7 @@ gemm_status_t gemm_layernorm(gemm_handle_t h, int64_t rows, int64_t cols, const 
  *   dgamma <- sum over the rows of dy * n,  dbeta <- sum over the rows of dy  (fp32).
  * dy has y's type, dx and residual x's.  residual (the gradient that reaches x past the norm)
  * may be NULL and may be dx itself (same stride); gamma, dgamma and dbeta may be NULL.
- * rows == 0: dgamma and dbeta are set to zeros. */
+ * rows == 0: dgamma and dbeta are set to zeros; cols == 0: nothing is written. */
 gemm_status_t gemm_layernorm_grad(gemm_handle_t h, int64_t rows, int64_t cols, const void* dy, int64_t ld_dy,
                                   int y_type, const void* x, int64_t ld_x, int x_type, const float* mean,
                                   const float* rstd, const void* gamma, int weight_type, const void* residual,

@@ -79,3 +79,16 @@ def test_infinite_rows(gpu, shape):
     assert np.isnan(y[[1, 3, 4]]).all() and np.isnan(rstd[[1, 3, 4]]).all()
     rest = [i for i in range(M) if i not in (1, 3, 4)]
     assert np.isfinite(y[rest]).all() and np.isfinite(mean[rest]).all() and np.isfinite(rstd[rest]).all()
+
+
+@pytest.mark.parametrize("shape", [(3, 0), (0, 7)])
+def test_nothing_to_normalise(gpu, shape):
+    import torch
+    x = torch.empty(shape, device="cuda")
+    mean, rstd = torch.full((shape[0],), 5.0, device="cuda"), torch.full((shape[0],), 6.0, device="cuda")
+    gpu.layernorm(x, torch.empty_like(x), mean=mean, rstd=rstd)
+    if shape[0]:
+        gpu.layernorm_grad(x, x, mean, rstd, torch.empty_like(x), dgamma=torch.empty(0, device="cuda"),
+                           dbeta=torch.empty(0, device="cuda"))
+    torch.cuda.synchronize()
+    assert (mean == 5).all() and (rstd == 6).all()

@@ -302,3 +302,22 @@ def test_run_dact_sums_of_the_largest(gpu, shape):
     assert torch.equal(db, sums.float())
     del z, C
     torch.cuda.empty_cache()
+
+
+def test_epilogue_tiles_serve_no_plain_product(gpu):
+    import torch
+    import dense_blas3_gemm_amd as d
+    names = [n for n in d.policies() if n.startswith("ep_")]
+    assert names
+    A, B = (torch.ones(256, 256, device="cuda").to(torch.float8_e4m3fn) for _ in range(2))
+    C = torch.full((256, 256), -77.0, dtype=torch.bfloat16, device="cuda")
+    for n in names:
+        gpu.set_policy(n)
+        try:
+            with pytest.raises(d.GemmError) as e:
+                gpu(A, B, C)
+        finally:
+            gpu.set_policy(None)
+        assert e.value.status == 2, n
+    torch.cuda.synchronize()
+    assert (C == -77).all()

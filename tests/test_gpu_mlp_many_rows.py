@@ -321,3 +321,25 @@ def test_epilogue_tiles_serve_no_plain_product(gpu):
         assert e.value.status == 2, n
     torch.cuda.synchronize()
     assert (C == -77).all()
+
+
+# a few rows, ring tiles unsplit and split, 256 x 256 tiles, two launches, blocks of rows
+@pytest.mark.parametrize("shape", [(13, 512, 1000), (300, 520, 256), (40, 136, 8192), (2048, 1536, 520), (1300, 13088, 320),
+                                   (130, 99, 264)])
+def test_codes_are_those_of_the_fp32_argument(gpu, shape):
+    """The codes and scales that a product leaves are its fp32 Z's, bit for bit (some two dozen rows)."""
+    import numpy as np
+    import oracle
+    import torch
+    M, N, K = shape
+    gen = torch.Generator(device="cuda").manual_seed(K)
+    A, B = (torch.randn(n, K, generator=gen, device="cuda").bfloat16() for n in (M, N))
+    b = torch.randn(N, generator=gen, device="cuda")
+    Z, C = torch.empty(M, N, device="cuda"), torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+    q, s = mx_buffers(M, N)
+    gpu.run_act(A, B, Z, transB=1, alpha=0.1, act="none", bias=b)
+    gpu.run_act(A, B, C, transB=1, alpha=0.1, act="gelu_tanh", bias=b, z=q, z_scales=s)
+    torch.cuda.synchronize()
+    some = slice(0, M, max(1, M // 24))
+    codes, scales = oracle.quantize_mx(Z[some].cpu().numpy().astype(np.float64))
+    assert np.array_equal(s[some].cpu().numpy(), scales) and np.array_equal(q[some].cpu().numpy(), codes)

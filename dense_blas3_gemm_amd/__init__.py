@@ -494,7 +494,7 @@ class Gemm:
         """dx <- the gradient of layernorm at x (+ residual), dgamma and dbeta (float32) those
         of its weights (gemm_layernorm_grad)."""
         st = _native.layernorm_grad(self._follow(), self.device, dy, x, mean, rstd, dx, gamma, dgamma, dbeta,
-                                       residual)
+                                    residual)
         if st != 0:
             raise GemmError("gemm_layernorm_grad", st)
         return dx

@@ -28,7 +28,8 @@ EXPORTS = ["gemm_create", "gemm_destroy", "gemm_set_stream", "gemm_run", "gemm_r
            "gemm_lds_probe", "gemm_hw_probe", "gemm_policy_count", "gemm_policy_name", "gemm_version",
            "gemm_status_string", "gemm_syrk", "gemm_syr2k", "gemm_symm", "gemm_trmm", "gemm_trsm",
            "gemm_run_act", "gemm_run_dact", "gemm_act_mx", "gemm_act_grad_mx", "gemm_layernorm",
-           "gemm_layernorm_grad"]
+           "gemm_layernorm_grad", "gemm_run_gated", "gemm_run_dgated", "gemm_quantize_i8", "gemm_run_i8",
+           "gemm_run_gated_i8"]
 
 LOWER, UPPER = 0, 1
 LEFT, RIGHT = 0, 1
@@ -46,6 +47,13 @@ class Epilogue(ctypes.Structure):
                 ("residual", ctypes.c_void_p), ("ld_residual", ctypes.c_int64), ("beta", ctypes.c_float),
                 ("z_kind", ctypes.c_int), ("z", ctypes.c_void_p), ("ld_z", ctypes.c_int64),
                 ("z_scales", ctypes.c_void_p), ("ld_z_scales", ctypes.c_int64)]
+
+
+class Gate(ctypes.Structure):
+    """gemm_gate_t"""
+    _fields_ = [("act", ctypes.c_int), ("bias_type", ctypes.c_int), ("bias_g", ctypes.c_void_p),
+                ("bias_u", ctypes.c_void_p), ("g", ctypes.c_void_p), ("ld_g", ctypes.c_int64),
+                ("u", ctypes.c_void_p), ("ld_u", ctypes.c_int64)]
 
 
 _lib = None
@@ -144,18 +152,28 @@ def load_library():
     lib.gemm_layernorm.argtypes = [vp, i64, i64, vp, i64, i32, vp, vp, i32, f32, vp, i64, i32, vp, vp]
     lib.gemm_layernorm_grad.argtypes = [vp, i64, i64, vp, i64, i32, vp, i64, i32, vp, vp, vp, i32, vp, i64, vp, i64,
                                         vp, vp]
+    lib.gemm_run_gated.argtypes = [vp, i32, i64, i64, i64, f32, vp, i64, vp, i64, vp, i64, ctypes.POINTER(Gate), vp,
+                                   i64, i32]
+    lib.gemm_run_dgated.argtypes = [vp, i32, i64, i64, i64, f32, vp, i64, vp, i64, i32, vp, i64, vp, i64, vp, i64, vp,
+                                    i64, vp, i64, vp, vp, i32]
+    lib.gemm_quantize_i8.argtypes = [vp, i64, i64, vp, i64, i32, vp, i64, vp]
+    lib.gemm_run_i8.argtypes = [vp, i32, i64, i64, i64, vp, i64, vp, vp, i64, vp, ctypes.POINTER(Epilogue), vp, i64,
+                                i32]
+    lib.gemm_run_gated_i8.argtypes = [vp, i32, i64, i64, i64, vp, i64, vp, vp, i64, vp, vp, i64, vp,
+                                      ctypes.POINTER(Gate), vp, i64, i32]
     for fn in ["gemm_create", "gemm_destroy", "gemm_set_stream", "gemm_run", "gemm_run_noalloc", "gemm_check_args",
                "gemm_query_policy", "gemm_set_policy", "gemm_lds_probe", "gemm_hw_probe", "gemm_policy_count",
                "gemm_run_mx", "gemm_quantize_mx", "gemm_syrk", "gemm_syr2k", "gemm_symm", "gemm_trmm",
                "gemm_trsm", "gemm_run_act", "gemm_run_dact", "gemm_act_mx", "gemm_act_grad_mx", "gemm_layernorm",
-               "gemm_layernorm_grad"]:
+               "gemm_layernorm_grad", "gemm_run_gated", "gemm_run_dgated", "gemm_quantize_i8", "gemm_run_i8",
+               "gemm_run_gated_i8"]:
         getattr(lib, fn).restype = i32
     _lib = lib
     return lib
 
 
 def _load_native():
-    """Loads the native part of the binding (the MLP-block operators' torch side) beside the library
+    """Loads the native part of the binding (the MLP-block and gated operators' torch side) beside the library
     and returns it; RuntimeError where it cannot be had.  The other calls do without it."""
     global _native
     load_library()
@@ -498,6 +516,57 @@ class Gemm:
         if st != 0:
             raise GemmError("gemm_layernorm_grad", st)
         return dx
+
+    def run_gated(self, A, Bg, Bu, C, transB: int = 0, alpha: float = 1.0, act: str = "silu", bias_g=None,
+                  bias_u=None, g=None, u=None):
+        """C <- act(G) * U with G = alpha*A*op(Bg) + bias_g and U = alpha*A*op(Bu) + bias_u
+        (gemm_run_gated).
+
+        A, Bg and Bu bf16 or float8_e4m3fn, C bf16 or float32, biases (N values) bf16 or float32;
+        act one of ACTS.  G and U are left in `g` and `u` (bf16, each optional) for run_dgated."""
+        st = _native.run_gated(self._follow(), self.device, A, Bg, Bu, C, transB, alpha, act, bias_g, bias_u, g, u)
+        if st != 0:
+            raise GemmError("gemm_run_gated", st)
+        return C
+
+    def run_dgated(self, A, B, g, u, dg, du, transB: int = 0, alpha: float = 1.0, act: str = "silu", h=None,
+                   dbias_g=None, dbias_u=None):
+        """With D = alpha*A*op(B): dg <- D * u * act'(g), du <- D * act(g), h <- act(g) * u, dbias_g
+        and dbias_u (float32, N values) the column sums of dg and du (gemm_run_dgated).
+
+        g, u as run_gated left them; dg and du bf16 or float32, h bf16.  dg may be g and du u."""
+        st = _native.run_dgated(self._follow(), self.device, A, B, g, u, dg, du, transB, alpha, act, h, dbias_g,
+                                dbias_u)
+        if st != 0:
+            raise GemmError("gemm_run_dgated", st)
+        return dg, du
+
+    def quantize_i8(self, src, dst, scales):
+        """dst (int8) <- the rows of src (bf16 or float32) as multiples of scales (float32, one per
+        row), the largest magnitude at 127 (gemm_quantize_i8)."""
+        st = _native.quantize_i8(self._follow(), self.device, src, dst, scales)
+        if st != 0:
+            raise GemmError("gemm_quantize_i8", st)
+        return dst
+
+    def run_i8(self, A, SA, B, SB, C, transB: int = 0, act: str = "none", bias=None, residual=None,
+               beta: float = 1.0):
+        """C <- act(P + bias) + beta*residual with P[m][n] = SA[m]*SB[n]*sum_k A[m][k]*op(B)[k][n]
+        (gemm_run_i8); A and B int8, SA and SB float32, the rest as in run_act."""
+        st = _native.run_i8(self._follow(), self.device, A, SA, B, SB, C, transB, act, bias, residual, beta)
+        if st != 0:
+            raise GemmError("gemm_run_i8", st)
+        return C
+
+    def run_gated_i8(self, A, SA, Bg, SBg, Bu, SBu, C, transB: int = 0, act: str = "silu", bias_g=None, bias_u=None,
+                     g=None, u=None):
+        """run_gated on int8 operands with a factor for each row of A and each column of op(Bg)
+        and op(Bu) (gemm_run_gated_i8)."""
+        st = _native.run_gated_i8(self._follow(), self.device, A, SA, Bg, SBg, Bu, SBu, C, transB, act, bias_g, bias_u,
+                                  g, u)
+        if st != 0:
+            raise GemmError("gemm_run_gated_i8", st)
+        return C
 
     def query_policy(self, M, N, K, transA=0, transB=0, dtype=BF16_BF16, A_ptr=0, lda=None,
                      B_ptr=0, ldb=None, C_ptr=0, ldc=None) -> str:

@@ -1,4 +1,4 @@
-// Native part of the Python binding for the MLP-block operators: reads what a call needs from
+// Native part of the Python binding for the MLP-block and gated operators: reads what a call needs from
 // its torch tensors, checks what the C-ABI cannot see of them, and calls the C-ABI.  These
 // calls stand beside kernels of a few microseconds, and reading half a dozen tensors in Python
 // takes about ten: layernorm of one row measured 7.8 us of host time that way (1.5 of them in
@@ -26,6 +26,11 @@ decltype(&gemm_act_mx) p_act_mx;
 decltype(&gemm_act_grad_mx) p_act_grad_mx;
 decltype(&gemm_layernorm) p_layernorm;
 decltype(&gemm_layernorm_grad) p_layernorm_grad;
+decltype(&gemm_run_gated) p_run_gated;
+decltype(&gemm_run_dgated) p_run_dgated;
+decltype(&gemm_quantize_i8) p_quantize_i8;
+decltype(&gemm_run_i8) p_run_i8;
+decltype(&gemm_run_gated_i8) p_run_gated_i8;
 
 struct Bad : std::runtime_error {
   using std::runtime_error::runtime_error;
@@ -140,15 +145,35 @@ int device_of(PyObject* o) {
   return (int)PyLong_AsLong(o);
 }
 
-// C = op(A) op(B)
+// the epilogue of a gated product
+gemm_gate_t gate(int64_t M, int64_t N, PyObject* act, PyObject* obg, PyObject* obu, PyObject* og, PyObject* ou,
+                 int dev) {
+  gemm_gate_t e{};
+  e.act = act_of(act);
+  int tg = GEMM_TYPE_F32, tu = GEMM_TYPE_F32;
+  e.bias_g = vec(tensor(obg, "bias_g"), N, dev, "bias_g", &tg);
+  e.bias_u = vec(tensor(obu, "bias_u"), N, dev, "bias_u", &tu);
+  if (e.bias_g && e.bias_u && tg != tu) throw Bad("bias_g and bias_u have to be of one type");
+  e.bias_type = e.bias_g ? tg : tu;
+  const Mat g = mat_or(tensor(og, "g"), M, N, dev, "g", at::kBFloat16);
+  const Mat u = mat_or(tensor(ou, "u"), M, N, dev, "u", at::kBFloat16);
+  e.g = g.p;
+  e.ld_g = g.ld;
+  e.u = u.p;
+  e.ld_u = u.ld;
+  return e;
+}
+
+// C = op(A) op(B); dtype a gemm_dtype_t, or for 8-bit integers (i8) C's gemm_type_t
 struct Product {
   int64_t M, N, K;
   Mat A, B, C;
   int tA, tB, dtype;
 };
-Product product(PyObject* oa, PyObject* ob, PyObject* oc, PyObject* ta, PyObject* tb, int device) {
-  const at::Tensor &A = needed(oa, "A"), &B = needed(ob, "B"), &C = needed(oc, "C");
-  if (A.dim() != 2 || B.dim() != 2 || C.dim() != 2) throw Bad("A, B and C have to be matrices");
+Product product(PyObject* oa, PyObject* ob, PyObject* oc, PyObject* ta, PyObject* tb, int device,
+                const char* c_name = "C", bool i8 = false) {
+  const at::Tensor &A = needed(oa, "A"), &B = needed(ob, "B"), &C = needed(oc, c_name);
+  if (A.dim() != 2 || B.dim() != 2 || C.dim() != 2) throw Bad(std::string("A, B and ") + c_name + " have to be matrices");
   Product p;
   p.tA = flag(ta, "transA");
   p.tB = flag(tb, "transB");
@@ -159,14 +184,16 @@ Product product(PyObject* oa, PyObject* ob, PyObject* oc, PyObject* ta, PyObject
     throw Bad("op(A) times op(B) is not C's: A " + text(A.sizes()) + ", B " + text(B.sizes()) + ", C " +
               text(C.sizes()));
   const bool bf16 = A.scalar_type() == at::kBFloat16;
-  if (A.scalar_type() != B.scalar_type() || (!bf16 && A.scalar_type() != at::kFloat8_e4m3fn))
-    throw Bad(std::string("A and B have to be bfloat16 or float8_e4m3fn: got ") + at::toString(A.scalar_type()) + ", " +
-              at::toString(B.scalar_type()));
-  const bool f32 = type_of(C, "C") == GEMM_TYPE_F32;
-  p.dtype = bf16 ? (f32 ? GEMM_BF16_F32 : GEMM_BF16_BF16) : (f32 ? GEMM_E4M3_F32 : GEMM_E4M3_BF16);
+  if (A.scalar_type() != B.scalar_type() ||
+      (i8 ? A.scalar_type() != at::kChar : !bf16 && A.scalar_type() != at::kFloat8_e4m3fn))
+    throw Bad(std::string(i8 ? "A and B have to be int8: got " : "A and B have to be bfloat16 or float8_e4m3fn: got ") +
+              at::toString(A.scalar_type()) + ", " + at::toString(B.scalar_type()));
+  const int type = type_of(C, c_name);
+  const bool f32 = type == GEMM_TYPE_F32;
+  p.dtype = i8 ? type : bf16 ? (f32 ? GEMM_BF16_F32 : GEMM_BF16_BF16) : (f32 ? GEMM_E4M3_F32 : GEMM_E4M3_BF16);
   p.A = mat(A, A.size(0), A.size(1), device, "A");
   p.B = mat(B, B.size(0), B.size(1), device, "B");
-  p.C = mat(C, p.M, p.N, device, "C");
+  p.C = mat(C, p.M, p.N, device, c_name);
   return p;
 }
 
@@ -337,6 +364,103 @@ PyObject* layernorm_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// (handle, device, A, Bg, Bu, C, transB, alpha, act, bias_g, bias_u, g, u)
+PyObject* run_gated(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return call(n, 13, [&] {
+    const int dev = device_of(a[1]);
+    const Product p = product(a[2], a[3], a[5], Py_False, a[6], dev);
+    const at::Tensor &bg = THPVariable_Unpack(a[3]), &bu = needed(a[4], "Bu");
+    const Mat b2 = mat_or(&bu, bg.size(0), bg.size(1), dev, "Bu", bg.scalar_type());
+    const gemm_gate_t e = gate(p.M, p.N, a[8], a[9], a[10], a[11], a[12], dev);
+    const gemm_handle_t h = handle(a[0]);
+    const float alpha = number(a[7]);
+    return unlocked([&] {
+      return p_run_gated(h, p.tB, p.M, p.N, p.K, alpha, p.A.p, p.A.ld, p.B.p, p.B.ld, b2.p, b2.ld, &e, p.C.p, p.C.ld,
+                         p.dtype);
+    });
+  });
+}
+
+// (handle, device, A, B, g, u, dg, du, transB, alpha, act, h, dbias_g, dbias_u)
+PyObject* run_dgated(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return call(n, 14, [&] {
+    const int dev = device_of(a[1]);
+    const Product p = product(a[2], a[3], a[6], Py_False, a[8], dev, "dg");
+    const Mat g = mat_or(&needed(a[4], "g"), p.M, p.N, dev, "g", at::kBFloat16);
+    const Mat u = mat_or(&needed(a[5], "u"), p.M, p.N, dev, "u", at::kBFloat16);
+    const Mat du = mat_or(&needed(a[7], "du"), p.M, p.N, dev, "du", THPVariable_Unpack(a[6]).scalar_type());
+    const Mat out = mat_or(tensor(a[11], "h"), p.M, p.N, dev, "h", at::kBFloat16);
+    const int act = act_of(a[10]);
+    float* dbg = (float*)vec(tensor(a[12], "dbias_g"), p.N, dev, "dbias_g");
+    float* dbu = (float*)vec(tensor(a[13], "dbias_u"), p.N, dev, "dbias_u");
+    const gemm_handle_t h = handle(a[0]);
+    const float alpha = number(a[9]);
+    return unlocked([&] {
+      return p_run_dgated(h, p.tB, p.M, p.N, p.K, alpha, p.A.p, p.A.ld, p.B.p, p.B.ld, act, g.p, g.ld, u.p, u.ld, p.C.p,
+                          p.C.ld, du.p, du.ld, out.p, out.ld, dbg, dbu, p.dtype);
+    });
+  });
+}
+
+// (handle, device, src, dst, scales)
+PyObject* quantize_i8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return call(n, 5, [&] {
+    const int dev = device_of(a[1]);
+    const at::Tensor& x = needed(a[2], "src");
+    if (x.dim() != 2) throw Bad("src has to be a matrix");
+    const int64_t M = x.size(0), N = x.size(1);
+    const int type = type_of(x, "src");
+    const Mat xm = mat(x, M, N, dev, "src");
+    const Mat q = mat_or(&needed(a[3], "dst"), M, N, dev, "dst", at::kChar);
+    float* s = (float*)vec(&needed(a[4], "scales"), M, dev, "scales");
+    const gemm_handle_t h = handle(a[0]);
+    return unlocked([&] { return p_quantize_i8(h, M, N, xm.p, xm.ld, type, (int8_t*)q.p, q.ld, s); });
+  });
+}
+
+// (handle, device, A, SA, B, SB, C, transB, act, bias, residual, beta)
+PyObject* run_i8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return call(n, 12, [&] {
+    const int dev = device_of(a[1]);
+    const Product p = product(a[2], a[4], a[6], Py_False, a[7], dev, "C", true);
+    const float* sa = (const float*)vec(&needed(a[3], "SA"), p.M, dev, "SA");
+    const float* sb = (const float*)vec(&needed(a[5], "SB"), p.N, dev, "SB");
+    gemm_epilogue_t e{};
+    e.act = act_of(a[8]);
+    e.bias = vec(tensor(a[9], "bias"), p.N, dev, "bias", &e.bias_type);
+    if (const at::Tensor* r = tensor(a[10], "residual")) {
+      const Mat m = mat_or(r, p.M, p.N, dev, "residual", THPVariable_Unpack(a[6]).scalar_type());
+      e.residual = m.p;
+      e.ld_residual = m.ld;
+      e.beta = number(a[11]);
+    }
+    const gemm_handle_t h = handle(a[0]);
+    return unlocked([&] {
+      return p_run_i8(h, p.tB, p.M, p.N, p.K, (const int8_t*)p.A.p, p.A.ld, sa, (const int8_t*)p.B.p, p.B.ld, sb, &e,
+                      p.C.p, p.C.ld, p.dtype);
+    });
+  });
+}
+
+// (handle, device, A, SA, Bg, SBg, Bu, SBu, C, transB, act, bias_g, bias_u, g, u)
+PyObject* run_gated_i8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return call(n, 15, [&] {
+    const int dev = device_of(a[1]);
+    const Product p = product(a[2], a[4], a[8], Py_False, a[9], dev, "C", true);
+    const at::Tensor &bg = THPVariable_Unpack(a[4]), &bu = needed(a[6], "Bu");
+    const Mat b2 = mat_or(&bu, bg.size(0), bg.size(1), dev, "Bu", bg.scalar_type());
+    const float* sa = (const float*)vec(&needed(a[3], "SA"), p.M, dev, "SA");
+    const float* sg = (const float*)vec(&needed(a[5], "SBg"), p.N, dev, "SBg");
+    const float* su = (const float*)vec(&needed(a[7], "SBu"), p.N, dev, "SBu");
+    const gemm_gate_t e = gate(p.M, p.N, a[10], a[11], a[12], a[13], a[14], dev);
+    const gemm_handle_t h = handle(a[0]);
+    return unlocked([&] {
+      return p_run_gated_i8(h, p.tB, p.M, p.N, p.K, (const int8_t*)p.A.p, p.A.ld, sa, (const int8_t*)p.B.p, p.B.ld, sg,
+                            (const int8_t*)b2.p, b2.ld, su, &e, p.C.p, p.C.ld, p.dtype);
+    });
+  });
+}
+
 // bind(path): the entry points of the loaded library
 PyObject* bind(PyObject*, PyObject* arg) {
   const char* path = PyUnicode_AsUTF8(arg);
@@ -348,7 +472,9 @@ PyObject* bind(PyObject*, PyObject* arg) {
   };
   if (!take(p_run_act, "gemm_run_act") || !take(p_run_dact, "gemm_run_dact") || !take(p_act_mx, "gemm_act_mx") ||
       !take(p_act_grad_mx, "gemm_act_grad_mx") || !take(p_layernorm, "gemm_layernorm") ||
-      !take(p_layernorm_grad, "gemm_layernorm_grad")) {
+      !take(p_layernorm_grad, "gemm_layernorm_grad") || !take(p_run_gated, "gemm_run_gated") ||
+      !take(p_run_dgated, "gemm_run_dgated") || !take(p_quantize_i8, "gemm_quantize_i8") ||
+      !take(p_run_i8, "gemm_run_i8") || !take(p_run_gated_i8, "gemm_run_gated_i8")) {
     PyErr_Format(PyExc_RuntimeError, "%s is not loaded, or lacks an entry point", path);
     return nullptr;
   }
@@ -356,8 +482,19 @@ PyObject* bind(PyObject*, PyObject* arg) {
 }
 
 #define FAST(f) {#f, (PyCFunction)(void*)f, METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {{"bind", bind, METH_O, nullptr}, FAST(run_act),   FAST(run_dact),       FAST(act_mx),
-                         FAST(act_grad_mx),               FAST(layernorm), FAST(layernorm_grad), {nullptr, nullptr, 0, nullptr}};
+PyMethodDef methods[] = {{"bind", bind, METH_O, nullptr},
+                         FAST(run_act),
+                         FAST(run_dact),
+                         FAST(act_mx),
+                         FAST(act_grad_mx),
+                         FAST(layernorm),
+                         FAST(layernorm_grad),
+                         FAST(run_gated),
+                         FAST(run_dgated),
+                         FAST(quantize_i8),
+                         FAST(run_i8),
+                         FAST(run_gated_i8),
+                         {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", "Native part of the binding.", -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
 

@@ -1,0 +1,57 @@
+// Internal interfaces of the gated feed-forward operators: both projections of a gated block
+// with the activation and the product of the two behind them, the product that runs back
+// through that, and products of 8-bit integers with a scale for each row of A and column of B.
+#pragma once
+
+#include "mlp_internal.h"
+
+namespace dbgemm {
+
+// What a product's results go through, element (m, n); w is alpha * (A op(B)), or for 8-bit
+// integers (the exact sum * sa[m]) * sb[n], w2 the same of the second B:
+//   GT_LINEAR: C <- act(w + bias) + beta * R
+//   GT_GATED:  g = w + bias, u = w2 + bias2; G <- g, U <- u (where kept); C <- act(g) * u
+//   GT_GRAD:   C <- w * U * act'(G); D2 <- w * act(G); H <- act(G) * U; the column sums of the
+//              first two in fp32, before their rounding
+enum { GT_LINEAR = 0, GT_GATED = 1, GT_GRAD = 2 };
+// operands: bf16, E4M3 bytes, 8-bit integers
+enum { GT_BF16 = 0, GT_E4M3 = 1, GT_I8 = 2 };
+
+struct GatedEp {
+  int act;
+  int bias_f32;
+  const void* bias;  // N values or null
+  const void* bias2;
+  const float* sa;  // 8-bit integers: one factor for each row of A and each column of B (and of B2)
+  const float* sb;
+  const float* sb2;
+  const void* R;  // C's element type, or null
+  int64_t ldr;
+  float beta;
+  void* G;  // bf16; written and null unless kept (GT_GATED), or read (GT_GRAD)
+  int64_t ldg;
+  void* U;
+  int64_t ldu;
+  void* D2;  // C's element type
+  int64_t ldd2;
+  void* H;  // bf16, or null
+  int64_t ldh;
+  float* colsum;  // fp32 partial sums, [part][2][whole8(N)], or null
+};
+
+// (B2 and ldb2 of GemmArgs hold the second B.)
+struct GatedArgs : GemmArgs {
+  int op;
+  int in_kind;
+  GatedEp ep;
+};
+
+// Any sizes, strides and alignment (op(A) = A).  With ep.colsum set, *parts receives the number
+// of partial rows written (at most max_parts >= 1).
+hipError_t launch_gated_simt(const GatedArgs& a, int max_parts, int* parts, hipStream_t s);
+
+// Rows of bf16 or fp32 -> 8-bit integers and a factor each.
+hipError_t launch_quantize_i8(int64_t rows, int64_t cols, const void* src, int64_t ld_src, int src_kind, int8_t* dst,
+                              int64_t ld_dst, float* scales, hipStream_t s);
+
+}  // namespace dbgemm

@@ -4,8 +4,7 @@
 #include <cmath>
 #include <cstdint>
 
-#include "blas3_internal.h"
-#include "mlp_internal.h"
+#include "mlp_host.h"
 
 using namespace dbgemm;
 
@@ -16,38 +15,6 @@ static_assert(GEMM_Z_NONE == Z_NONE && GEMM_Z_BF16 == Z_BF16 && GEMM_Z_MX == Z_M
 static_assert(GEMM_TYPE_BF16 == T_BF16 && GEMM_TYPE_F32 == T_F32, "the kernels' element types");
 
 namespace {
-
-// The workspace: partial column sums, or a split product's partial tiles, first; behind them a
-// product in fp32, or the column sums of a product with an epilogue.
-constexpr size_t kPartBytes = (size_t)64 << 20;
-constexpr int kMaxParts = 1024;
-
-// Makes the handle's device current for its lifetime.
-struct OnDevice {
-  int cur = -1;
-  int dev;
-  bool ok;
-  explicit OnDevice(int device) : dev(device) {
-    ok = hipGetDevice(&cur) == hipSuccess && (cur == device || hipSetDevice(device) == hipSuccess);
-  }
-  ~OnDevice() {
-    if (ok && cur != dev) (void)hipSetDevice(cur);
-  }
-};
-
-gemm_status_t status(hipError_t e) { return e == hipSuccess ? GEMM_STATUS_SUCCESS : GEMM_STATUS_LAUNCH_FAILED; }
-
-bool valid_act(int a) { return a >= GEMM_ACT_NONE && a <= GEMM_ACT_SILU; }
-bool valid_type(int t) { return t == GEMM_TYPE_BF16 || t == GEMM_TYPE_F32; }
-bool valid_size(int64_t v) { return v >= 0 && v <= 0x7FFFFFFF; }
-bool valid_ld(int64_t ld, int64_t cols) { return ld >= (cols > 1 ? cols : 1); }
-
-// partial rows of `width` floats that fit the workspace's first part, at most kMaxParts
-int max_parts(const HandleView& v, int64_t width) {
-  if (!v.ws || width <= 0) return 0;
-  const int64_t n = (int64_t)(kPartBytes / sizeof(float)) / width;
-  return (int)(n < kMaxParts ? n : kMaxParts);
-}
 
 // Operand checks shared by the two products; bf16 or E4M3 operands, bf16 or fp32 C.
 gemm_status_t check_product(int transA, int transB, int64_t M, int64_t N, int64_t K, float alpha, const void* A,

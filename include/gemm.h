@@ -461,6 +461,72 @@ gemm_status_t gemm_layernorm_grad(gemm_handle_t h, int64_t rows, int64_t cols, c
                                   const float* rstd, const void* gamma, int weight_type, const void* residual,
                                   int64_t ld_residual, void* dx, int64_t ld_dx, float* dgamma, float* dbeta);
 
+/* ---------------------------------------------------------------------------------
+ * The gated feed-forward block, H = act(X Wg) * (X Wu), Y = H Wd: both projections with
+ * the activation and the product of the two behind them, the product that runs back
+ * through it, and the block in 8-bit integers for serving.  What is said of the MLP
+ * block's operators above holds here too: row-major with row strides, the handle's stream
+ * and workspace, fp32 up to the last rounding, any size and alignment, errors.  A is stored
+ * [M][lda >= K]; B (Bg, Bu) [K][ldb >= N] (transB = 0) or [N][ldb >= K] (transB = 1).
+ * The other products of a training step are gemm_run's: with Wg and Wu, and dG and dU, side
+ * by side in one buffer each (the pointers and strides here reach into it),
+ * dX = [dG dU] [Wg Wu]^T and d[Wg Wu] = X^T [dG dU].
+ * --------------------------------------------------------------------------------- */
+
+/* The epilogue of gemm_run_gated; zeroed memory is the empty one. */
+typedef struct {
+  int act;            /* gemm_act_t, of the gate */
+  int bias_type;      /* gemm_type_t of both biases */
+  const void* bias_g; /* N values each, or NULL */
+  const void* bias_u;
+  void* g;            /* G and U in bf16, M x N each, for the backward pass; each or NULL */
+  int64_t ld_g;
+  void* u;
+  int64_t ld_u;
+} gemm_gate_t;
+
+/* G <- alpha * A * op(Bg) + bias_g;  U <- alpha * A * op(Bu) + bias_u;  C <- act(G) * U, from
+ * the fp32 values of G and U.  dtype GEMM_BF16_F32, GEMM_BF16_BF16, GEMM_E4M3_BF16 or
+ * GEMM_E4M3_F32.  K == 0 or alpha == 0: both products are 0 and the epilogue runs all the
+ * same.  gemm_set_policy does not apply to the calls of this section. */
+gemm_status_t gemm_run_gated(gemm_handle_t h, int transB, int64_t M, int64_t N, int64_t K, float alpha, const void* A,
+                             int64_t lda, const void* Bg, int64_t ldbg, const void* Bu, int64_t ldbu,
+                             const gemm_gate_t* ep, void* C, int64_t ldc, int dtype);
+
+/* D <- alpha * A * op(B);  dg <- D * U * act'(G);  du <- D * act(G);  out <- act(G) * U;
+ * dbias_g[n], dbias_u[n] <- sums over the rows of dg and du (fp32, from their unrounded
+ * values).  With A = dY and op(B) = Wd^T these are the gradients of G, U and the biases, and
+ * out is H again, for the gradient of Wd.  G, U (bf16, M x N) as gemm_run_gated left them; dg
+ * and du bf16 or fp32 (C's type of the dtypes of gemm_run_gated); out bf16 or NULL, each sum
+ * or NULL.  dg may be G and du may be U (bf16, same stride).  M == 0: the sums are set to zeros. */
+gemm_status_t gemm_run_dgated(gemm_handle_t h, int transB, int64_t M, int64_t N, int64_t K, float alpha, const void* A,
+                              int64_t lda, const void* B, int64_t ldb, int act, const void* g, int64_t ld_g,
+                              const void* u, int64_t ld_u, void* dg, int64_t ld_dg, void* du, int64_t ld_du, void* out,
+                              int64_t ld_out, float* dbias_g, float* dbias_u, int dtype);
+
+/* Rows (tokens, or a weight's output channels as [N][K]) to 8-bit integers with a factor
+ * each:  scales[r] <- max|x| / 127;  dst <- the whole number nearest to 127 x / max|x|, ties to
+ * even (of the exact quotient; -127 .. 127).  src bf16 or fp32 (src_type, a gemm_type_t).  A
+ * row of zeros: factor 0, codes 0; a row with Inf or NaN: factor NaN, codes 0.  cols == 0:
+ * the factors are zeros. */
+gemm_status_t gemm_quantize_i8(gemm_handle_t h, int64_t rows, int64_t cols, const void* src, int64_t ld_src,
+                               int src_type, int8_t* dst, int64_t ld_dst, float* scales);
+
+/* P[m][n] <- scale_a[m] * scale_b[n] * sum_k A[m][k] * op(B)[k][n] (the sum of 8-bit integers
+ * exact);  C <- act(P + bias) + beta * R.  scale_a: M values, scale_b: N values.  ep as in
+ * gemm_run_act with z_kind GEMM_Z_NONE; C bf16 or fp32 (c_type).  K up to 131071, else
+ * NOT_SUPPORTED (longer sums of codes down to -128 may leave 32 bits). */
+gemm_status_t gemm_run_i8(gemm_handle_t h, int transB, int64_t M, int64_t N, int64_t K, const int8_t* A, int64_t lda,
+                          const float* scale_a, const int8_t* B, int64_t ldb, const float* scale_b,
+                          const gemm_epilogue_t* ep, void* C, int64_t ldc, int c_type);
+
+/* The gated form: G and U are such products of A with Bg and Bu, plus their biases;
+ * C <- act(G) * U.  ep as in gemm_run_gated. */
+gemm_status_t gemm_run_gated_i8(gemm_handle_t h, int transB, int64_t M, int64_t N, int64_t K, const int8_t* A,
+                                int64_t lda, const float* scale_a, const int8_t* Bg, int64_t ldbg,
+                                const float* scale_bg, const int8_t* Bu, int64_t ldbu, const float* scale_bu,
+                                const gemm_gate_t* ep, void* C, int64_t ldc, int c_type);
+
 #ifdef __cplusplus
 }
 #endif

@@ -30,7 +30,8 @@ SOURCES = [("api.cpp", "api", []), ("policy.cpp", "policy", []), ("kernel_simt.h
            ("mlp.cpp", "mlp", []), ("act_mx.hip", "act_mx", []), ("layernorm.hip", "layernorm", []),
            ("kernel_skinny.hip", "kernel_skinny", []),
            ("gated.cpp", "gated", []), ("quantize_i8.hip", "quantize_i8", []),
-           ("kernel_gated_simt.hip", "kernel_gated_simt", [])] + [
+           ("kernel_gated_simt.hip", "kernel_gated_simt", []),
+           ("kernel_skinny.hip", "kernel_skinny_gt", ["-DDBGEMM_GATED"])] + [
     ("kernel_mfma.hip", f"kernel_mfma_{ta}{tb}", [f"-DDBGEMM_DMA_TA={ta}", f"-DDBGEMM_DMA_TB={tb}"])
     for ta in (0, 1) for tb in (0, 1)] + [
     ("kernel_mfma_dma.hip", f"kernel_mfma_dma_{ta}{tb}_p{part}",
@@ -40,7 +41,10 @@ SOURCES = [("api.cpp", "api", []), ("policy.cpp", "policy", []), ("kernel_simt.h
     for ta in (0, 1) for tb in (0, 1)] + [
     # the same two kernels for products with an epilogue
     (f"{k}.hip", f"{k}_ep_{ta}{tb}", [f"-DDBGEMM_DMA_TA={ta}", f"-DDBGEMM_DMA_TB={tb}", "-DDBGEMM_EPILOGUE"])
-    for k in ("kernel_pingpong", "kernel_mfma_dma") for ta in (0, 1) for tb in (0, 1)]
+    for k in ("kernel_pingpong", "kernel_mfma_dma") for ta in (0, 1) for tb in (0, 1)] + [
+    # and for the gated operators, once per operand kind
+    (f"{k}.hip", f"{k}_gt_{kind}{tb}", [f"-DDBGEMM_GATED={kind}", "-DDBGEMM_DMA_TA=0", f"-DDBGEMM_DMA_TB={tb}"])
+    for k in ("kernel_pingpong", "kernel_mfma_dma") for kind in (0, 1, 2) for tb in (0, 1)]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 FLAGS = ["-O3", "-fPIC", "-std=c++17", f"--offload-arch={ARCH}", "-Xclang", "-target-feature",

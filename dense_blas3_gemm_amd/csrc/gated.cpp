@@ -4,6 +4,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "gated_internal.h"
 #include "mlp_host.h"
@@ -28,6 +29,138 @@ gemm_status_t run_simt(const HandleView& v, GatedArgs a, float* dbias, float* db
   return status(e);
 }
 
+// bytes per element of the operands, of C
+int64_t in_bytes(const GatedArgs& a) { return a.in_kind == GT_BF16 ? 2 : 1; }
+int64_t c_bytes(const GatedArgs& a) { return a.c_kind == C_F32 ? 4 : 2; }
+
+// a's rows [m0, m0 + M) and columns [n0, n0 + N)
+GatedArgs part_of(const GatedArgs& a, int64_t m0, int64_t n0, int64_t M, int64_t N) {
+  GatedArgs r = a;
+  const int64_t es = in_bytes(a), ce = c_bytes(a), be = a.ep.bias_f32 ? 4 : 2;
+  auto at = [](auto*& p, int64_t bytes) {
+    if (p) p = (std::remove_reference_t<decltype(p)>)((const char*)p + bytes);
+  };
+  r.M = (int)M;
+  r.N = (int)N;
+  at(r.A, m0 * a.lda * es);
+  at(r.B, (a.transB ? n0 * a.ldb : n0) * es);
+  at(r.B2, (a.transB ? n0 * a.ldb2 : n0) * es);
+  at(r.C, (m0 * a.ldc + n0) * ce);
+  at(r.ep.bias, n0 * be);
+  at(r.ep.bias2, n0 * be);
+  at(r.ep.sa, m0 * 4);
+  at(r.ep.sb, n0 * 4);
+  at(r.ep.sb2, n0 * 4);
+  at(r.ep.R, (m0 * a.ep.ldr + n0) * ce);
+  at(r.ep.G, (m0 * a.ep.ldg + n0) * 2);
+  at(r.ep.U, (m0 * a.ep.ldu + n0) * 2);
+  at(r.ep.D2, (m0 * a.ep.ldd2 + n0) * ce);
+  at(r.ep.H, (m0 * a.ep.ldh + n0) * 2);
+  return r;
+}
+
+// One launch on policy p with sp splits; partial column sums into ep.colsum, *parts rows of them.
+hipError_t run_tiles(const HandleView& v, GatedArgs a, const Policy& p, int sp, int* parts) {
+  const int64_t cols = a.op == GT_GATED ? p.BN / 2 : p.BN;
+  a.tiles_m = (a.M + p.BM - 1) / p.BM;
+  a.tiles_n = (int)((a.N + cols - 1) / cols);
+  a.group = p.group;
+  a.raster_n = p.raster_n;
+  a.xcd = p.xcd;
+  a.swizzle = p.swizzle;
+  a.splits = sp;
+  a.kt_per_split = (int)split_kt(p, a.in_kind == GT_I8 ? (a.K + 1) / 2 : a.K, sp);
+  a.ws = sp > 1 ? (float*)v.ws : nullptr;
+  return launch_mfma_gated(p, a, parts, v.stream);
+}
+
+// The partial rows of column sums that run_tiles leaves: a row of waves each, or after a split a
+// row of fragments.
+int64_t partial_rows(const Policy& p, int64_t M, int sp) {
+  return (M + p.BM - 1) / p.BM * (sp > 1 ? p.BM / p.WM / 16 : p.WM);
+}
+
+// What the tile policies see of a: a product of both B side by side; 8-bit integers as bf16 of
+// half the K (the same bytes, and the integer MFMA takes as long for them).
+Problem problem_of(const GatedArgs& a) {
+  Problem pr{};
+  pr.transB = a.transB;
+  pr.M = a.M;
+  pr.N = a.op == GT_GATED ? 2 * (int64_t)a.N : a.N;
+  pr.K = a.in_kind == GT_I8 ? (a.K + 1) / 2 : a.K;
+  pr.in_fp8 = a.in_kind == GT_E4M3;
+  pr.c_kind = a.c_kind;
+  pr.fast_ok = true;
+  pr.ep = true;
+  return pr;
+}
+
+// Whether the MFMA kernels take the operands: 16-byte aligned, strides and contiguous extents in
+// whole 16 bytes (`cols`: of B's columns), and spans that 32-bit offsets cover.
+bool operands_ok(const GatedArgs& a, int64_t cols) {
+  const int64_t es = in_bytes(a), vec = 16 / es;
+  auto fits = [&](const void* p, int64_t ld, int64_t rows) {
+    return ((uintptr_t)p & 15) == 0 && ld * es % 16 == 0 && (double)(rows + 256) * (double)ld * (double)es < 2147483647.0;
+  };
+  const int64_t b_rows = a.transB ? a.N : a.K;
+  return a.K % vec == 0 && (a.transB || cols % vec == 0) && fits(a.A, a.lda, a.M) && fits(a.B, a.ldb, b_rows) &&
+         (a.op != GT_GATED || fits(a.B2, a.ldb2, b_rows));
+}
+
+// a's columns, whole eights of them, on the MFMA kernels; false (nothing launched) where they, or
+// the workspace, cannot.  accumulate: the sums are added to dbias and dbias2.
+bool run_fused(const HandleView& v, GatedArgs a, float* dbias, float* dbias2, int accumulate, hipError_t* e) {
+  const bool sums = dbias || dbias2;
+  if (!accumulate && gated_skinny_serves(a.op, a.in_kind, a.transB, a.M, a.K)) {
+    a.ep.sum1 = dbias;
+    a.ep.sum2 = dbias2;
+    *e = launch_gated_skinny(a, v.stream);
+    return true;
+  }
+  const int nb = a.op == GT_GATED ? 2 : 1;
+  Problem pr = problem_of(a);
+  int sp = 1, idx2 = 0, sp2 = 1;
+  double cost = 0.0;
+  const int64_t split_floats = v.ws ? (int64_t)(kPartBytes / sizeof(float)) : 0;
+  int idx = policy_select(pr, v.cu_count, split_floats, &sp, &cost);
+  if (policy_at(idx).kind != KIND_MFMA) return false;
+  const Cut cut = policy_cut(pr, v.cu_count, split_floats, cost);
+  GatedArgs a1 = a, a2 = a;
+  const int64_t at = cut.p < 0 || cut.by_rows ? cut.at : cut.at / nb;
+  if (cut.p >= 0) {
+    a1 = cut.by_rows ? part_of(a, 0, 0, at, a.N) : part_of(a, 0, 0, a.M, at);
+    a2 = cut.by_rows ? part_of(a, at, 0, a.M - at, a.N) : part_of(a, 0, at, a.M, a.N - at);
+    idx = cut.p;
+    sp = 1;
+    pr.M = a2.M;
+    pr.N = (int64_t)a2.N * nb;
+    idx2 = policy_select(pr, v.cu_count, split_floats, &sp2);
+    if (policy_at(idx2).kind != KIND_MFMA) return false;
+  }
+  if (sums) {
+    const int64_t f1 = partial_rows(policy_at(idx), a1.M, sp) * 2 * a1.N;
+    const int64_t f2 = cut.p >= 0 ? partial_rows(policy_at(idx2), a2.M, sp2) * 2 * a2.N : 0;
+    if (!v.ws || v.ws_bytes < kPartBytes + (size_t)(f1 + f2) * sizeof(float)) return false;
+    a1.ep.colsum = (float*)((char*)v.ws + kPartBytes);
+    a2.ep.colsum = a1.ep.colsum + f1;
+  }
+  auto add_up = [&](const GatedArgs& p, int parts, int64_t n0) {
+    return launch_colsum(p.ep.colsum, parts, 2 * (int64_t)p.N, p.N, dbias ? dbias + n0 : nullptr,
+                         dbias2 ? dbias2 + n0 : nullptr, accumulate, v.stream);
+  };
+  int parts = 0, parts2 = 0;
+  *e = run_tiles(v, a1, policy_at(idx), sp, &parts);
+  if (cut.p >= 0 && *e == hipSuccess) *e = run_tiles(v, a2, policy_at(idx2), sp2, &parts2);
+  if (!sums || *e != hipSuccess) return true;
+  if (cut.p >= 0 && cut.by_rows) {  // (the rows of partial sums of both follow each other)
+    *e = add_up(a1, parts + parts2, 0);
+  } else {
+    *e = add_up(a1, parts, 0);
+    if (cut.p >= 0 && *e == hipSuccess) *e = add_up(a2, parts2, at);
+  }
+  return true;
+}
+
 gemm_status_t run(gemm_handle_t h, GatedArgs a, float* dbias = nullptr, float* dbias2 = nullptr) {
   HandleView v;
   if (!handle_view(h, &v)) return GEMM_STATUS_NOT_INITIALIZED;
@@ -38,7 +171,25 @@ gemm_status_t run(gemm_handle_t h, GatedArgs a, float* dbias = nullptr, float* d
     return status(launch_colsum(nullptr, 0, 2 * whole8(a.N), a.N, dbias, dbias2, 0, v.stream));
   }
   if (a.alpha == 0.f) a.K = 0;
-  return run_simt(v, a, dbias, dbias2);
+  // the columns of the MFMA kernels: whole eights, of [K][N] operands whole 16 bytes; the generic
+  // kernel has the rest
+  const int64_t step = a.transB ? 8 : 16 / in_bytes(a), N1 = a.K > 0 ? a.N / step * step : 0;
+  if (N1 == 0) return run_simt(v, a, dbias, dbias2);
+  // rows that 32-bit offsets into A cover, 256 at a time
+  const int64_t most = (int64_t)(2147483647.0 / ((double)a.lda * (double)in_bytes(a))) / 256 * 256 - 512;
+  const int64_t rows = most >= a.M ? a.M : most;
+  if (rows < 1 || !operands_ok(part_of(a, 0, 0, rows, a.N), N1)) return run_simt(v, a, dbias, dbias2);
+  for (int64_t m0 = 0; m0 < a.M; m0 += rows) {
+    const int64_t M = a.M - m0 < rows ? a.M - m0 : rows;
+    hipError_t e;
+    if (!run_fused(v, part_of(a, m0, 0, M, N1), dbias, dbias2, m0 > 0, &e)) {
+      if (m0 > 0) return GEMM_STATUS_INTERNAL;
+      return run_simt(v, a, dbias, dbias2);
+    }
+    if (e != hipSuccess) return status(e);
+  }
+  if (N1 == a.N) return GEMM_STATUS_SUCCESS;
+  return run_simt(v, part_of(a, 0, N1, a.M, a.N - N1), dbias ? dbias + N1 : nullptr, dbias2 ? dbias2 + N1 : nullptr);
 }
 
 // Operands (the second B is checked by the same rules) and C of one call.
@@ -112,6 +263,22 @@ void set_gate(GatedArgs& a, const gemm_gate_t* ep, const void* B2, int64_t ldb2)
 }
 
 }  // namespace
+
+namespace dbgemm {
+hipError_t launch_mfma_gated(const Policy& p, const GatedArgs& a, int* parts, hipStream_t s) {
+#define DBGEMM_GT_CASE(in, b) \
+  return p.pipe == 2 ? launch_mfma_pp_gt_##in##b(p, a, parts, s) : launch_mfma_dma_gt_##in##b(p, a, parts, s)
+  switch (a.in_kind * 2 + (a.transB != 0)) {
+    case 0: DBGEMM_GT_CASE(0, 0);
+    case 1: DBGEMM_GT_CASE(0, 1);
+    case 2: DBGEMM_GT_CASE(1, 0);
+    case 3: DBGEMM_GT_CASE(1, 1);
+    case 4: DBGEMM_GT_CASE(2, 0);
+    default: DBGEMM_GT_CASE(2, 1);
+  }
+#undef DBGEMM_GT_CASE
+}
+}  // namespace dbgemm
 
 extern "C" {
 

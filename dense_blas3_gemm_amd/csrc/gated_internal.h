@@ -37,6 +37,8 @@ struct GatedEp {
   void* H;  // bf16, or null
   int64_t ldh;
   float* colsum;  // fp32 partial sums, [part][2][whole8(N)], or null
+  float* sum1;    // the kernels of a few rows: the sums themselves, each or null
+  float* sum2;
 };
 
 // (B2 and ldb2 of GemmArgs hold the second B.)
@@ -45,6 +47,33 @@ struct GatedArgs : GemmArgs {
   int in_kind;
   GatedEp ep;
 };
+
+// The MFMA kernels of an operand kind: the input mode of the policies that serve it, of its own
+// configurations, and their K tile for a policy's.  8-bit integers run on the bf16 tiles: as many
+// bytes of K, twice the elements.
+constexpr int gt_policy_in(int kind) { return kind == GT_E4M3 ? 5 : 0; }
+constexpr int gt_in(int kind) { return kind == GT_E4M3 ? 5 : kind == GT_I8 ? 7 : 0; }
+constexpr int gt_bk(int kind, int bk) { return kind == GT_I8 ? 2 * bk : bk; }
+
+// a, whose grid fields are set, on policy p (has_epilogue); N in whole eights, operands as the MFMA
+// kernels take them.  With ep.colsum set, *parts receives the partial rows it writes.
+hipError_t launch_mfma_gated(const Policy& p, const GatedArgs& a, int* parts, hipStream_t s);
+// one per kernel family, operand kind and transB, each in its own object
+#define DBGEMM_GT_DECL(in, b)                                                                           \
+  hipError_t launch_mfma_pp_gt_##in##b(const Policy& p, const GatedArgs& a, int* parts, hipStream_t s); \
+  hipError_t launch_mfma_dma_gt_##in##b(const Policy& p, const GatedArgs& a, int* parts, hipStream_t s);
+DBGEMM_GT_DECL(0, 0)
+DBGEMM_GT_DECL(0, 1)
+DBGEMM_GT_DECL(1, 0)
+DBGEMM_GT_DECL(1, 1)
+DBGEMM_GT_DECL(2, 0)
+DBGEMM_GT_DECL(2, 1)
+#undef DBGEMM_GT_DECL
+
+// Products of a few rows, the rest as for launch_mfma_gated; ep.sum1 and ep.sum2 receive the
+// column sums.
+bool gated_skinny_serves(int op, int in_kind, int transB, int64_t M, int64_t K);
+hipError_t launch_gated_skinny(const GatedArgs& a, hipStream_t s);
 
 // Any sizes, strides and alignment (op(A) = A).  With ep.colsum set, *parts receives the number
 // of partial rows written (at most max_parts >= 1).

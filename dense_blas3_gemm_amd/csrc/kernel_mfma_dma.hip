@@ -24,12 +24,17 @@
 #ifdef DBGEMM_EPILOGUE  // the kernels of products with an epilogue
 #include "epilogue_tile.h"
 #endif
+#ifdef DBGEMM_GATED  // the kernels of the gated operators
+#include "gated_tile.h"
+#endif
 
 namespace dbgemm {
 namespace {
 
 #ifdef DBGEMM_EPILOGUE
 using KernelArgs = GemmEpArgs;
+#elif defined(DBGEMM_GATED)
+using KernelArgs = GatedArgs;
 #else
 using KernelArgs = GemmArgs;
 #endif
@@ -100,7 +105,8 @@ struct Dma {
   static constexpr int loads_before(int kk) { return IPW * kk / LOAD_STEPS; }
 };
 
-template <class C>
+// OP: what a gated operator's kernel does with its sums.
+template <class C, int OP = 0>
 __global__ __launch_bounds__(C::THREADS) void gemm_dma_kernel(KernelArgs a) {
   using D = Dma<C>;
   // One LDS object per ring slot: the compiler tracks the loads into each slot on
@@ -128,20 +134,24 @@ __global__ __launch_bounds__(C::THREADS) void gemm_dma_kernel(KernelArgs a) {
   }
   int tm, tn, split;
   tile_of(blockIdx.x, a, tm, tn, split);
-  const int m0 = tm * C::BM, n0 = tn * C::BN;
+  const int m0 = tm * C::BM, n0 = tn * C::SUB_BN;
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
   const int wm = wave / C::WN, wn = wave % C::WN;
   const int sw_on = a.swizzle;
+  // two B: the first half of the waves loads the one's sub-tile, the others the other's
+  const bool upper = C::DUAL && __builtin_amdgcn_readfirstlane(wave) >= D::NW / 2;
+  const void* const b_ptr = upper ? a.B2 : a.B;
+  const int64_t ldb = upper ? a.ldb2 : a.ldb;
 
   const uint32_t a_rows = C::A_KC ? a.M : a.K;
   const uint32_t b_rows = C::B_KC ? a.N : a.K;
   const __amdgpu_buffer_rsrc_t ra = make_rsrc(a.A, (uint32_t)(a_rows * a.lda * C::ES));
-  const __amdgpu_buffer_rsrc_t rb = make_rsrc(a.B, (uint32_t)(b_rows * a.ldb * C::ES));
+  const __amdgpu_buffer_rsrc_t rb = make_rsrc(b_ptr, (uint32_t)(b_rows * ldb * C::ES));
   // Two products in one sum (the rank-2K update), in the bf16 A [M][K], B [N][K]
   // instantiations only: their register budget has room for the second pair of buffer
   // descriptors, which pushed the transposed-A 256 x 256 tile (and the scaled-E4M3 one) into
   // scratch.  Same strides as (A, B).
-  constexpr bool kDual = !C::TA && C::TB && C::IN == IN_BF16;
+  constexpr bool kDual = !C::TA && C::TB && C::IN == IN_BF16 && !C::DUAL;
   const __amdgpu_buffer_rsrc_t ra2 = kDual ? make_rsrc(a.dual ? a.A2 : a.A, (uint32_t)(a_rows * a.lda * C::ES)) : ra;
   const __amdgpu_buffer_rsrc_t rb2 = kDual ? make_rsrc(a.dual ? a.B2 : a.B, (uint32_t)(b_rows * a.ldb * C::ES)) : rb;
 
@@ -156,7 +166,7 @@ __global__ __launch_bounds__(C::THREADS) void gemm_dma_kernel(KernelArgs a) {
   for (int i = 0; i < D::A_IPW; ++i) {
     const int p = (wave * D::A_IPW + i) * 64 + lane;
     const int r = p / C::A_CPR;
-    const int c = (p % C::A_CPR) ^ (D::E8 ? pp_swz<C, C::A_KC, C::A_CPR>(r) :
+    const int c = (p % C::A_CPR) ^ (D::E8 || C::I8 ? pp_swz<C, C::A_KC, C::A_CPR>(r) :
                                     sw_on ? swz<C::A_KC, C::FP8, C::A_CPR, C::MT>(r) : 0);
     if constexpr (C::A_KC) {  // rows = m, chunks along k
       a_goff[i] = (uint32_t)((m0 + r) * a.lda + c * C::VEC) * C::ES;
@@ -170,22 +180,23 @@ __global__ __launch_bounds__(C::THREADS) void gemm_dma_kernel(KernelArgs a) {
   }
 #pragma unroll
   for (int i = 0; i < D::B_IPW; ++i) {
-    const int p = (wave * D::B_IPW + i) * 64 + lane;
-    const int r = p / C::B_CPR;
-    const int c = (p % C::B_CPR) ^ (D::E8 ? pp_swz<C, C::B_KC, C::B_CPR>(r) :
-                                    sw_on ? swz<C::B_KC, C::FP8, C::B_CPR, C::MT>(r) : 0);
+    // (a chunk of its sub-tile)
+    const int p = (wave % (D::NW / C::NSUB) * D::B_IPW + i) * 64 + lane;
+    const int r = p / C::SUB_CPR;
+    const int c = (p % C::SUB_CPR) ^ (D::E8 || C::I8 ? pp_swz<C, C::B_KC, C::SUB_CPR>(r) :
+                                      sw_on ? swz<C::B_KC, C::FP8, C::SUB_CPR, C::MT>(r) : 0);
     if constexpr (C::B_KC) {  // rows = n, chunks along k
-      b_goff[i] = (uint32_t)((n0 + r) * a.ldb + c * C::VEC) * C::ES;
+      b_goff[i] = (uint32_t)((n0 + r) * ldb + c * C::VEC) * C::ES;
       b_ok[i] = (n0 + r) < a.N;
       b_kc[i] = c * C::VEC;
     } else {  // rows = k, chunks along n
-      b_goff[i] = (uint32_t)(r * a.ldb + n0 + c * C::VEC) * C::ES;
+      b_goff[i] = (uint32_t)(r * ldb + n0 + c * C::VEC) * C::ES;
       b_ok[i] = (n0 + c * C::VEC) < a.N;
       b_kc[i] = r;
     }
   }
   const uint32_t a_kstep = C::A_KC ? C::BK * C::ES : (uint32_t)(C::BK * a.lda * C::ES);
-  const uint32_t b_kstep = C::B_KC ? C::BK * C::ES : (uint32_t)(C::BK * a.ldb * C::ES);
+  const uint32_t b_kstep = C::B_KC ? C::BK * C::ES : (uint32_t)(C::BK * ldb * C::ES);
 
   // ---- scaled native E4M3: this wave's scale words (rows wave*64 + lane of A's tile, or
   // of B's for the upper waves); K tile kt reads the word at byte kt*4 of the row.  Rows
@@ -260,7 +271,9 @@ __global__ __launch_bounds__(C::THREADS) void gemm_dma_kernel(KernelArgs a) {
 #pragma unroll
     for (int j = 0; j < C::FN; ++j) acc[i][j] = Acc{};
 
-  const int xa0 = wm * C::WTM, xb0 = wn * C::WTN;
+  // (Two B: fragments 0 .. FN / 2 - 1 of the one sub-tile, then the same columns of the other.)
+  const int xa0 = wm * C::WTM, xb0 = wn * (C::WTN / C::NSUB);
+  constexpr int FSUB = C::FN / C::NSUB;
 
   Frag fa[2][C::FM], fb[2][C::FN];
   // one fragment of an operand: 8 E4M3 bytes as they are, or what the MFMA takes
@@ -273,6 +286,13 @@ __global__ __launch_bounds__(C::THREADS) void gemm_dma_kernel(KernelArgs a) {
         return *LDS_PTR(i32x2, base, o);
       else
         return __builtin_amdgcn_ds_read_tr8_b64_v2i32(LDS_PTR(i32x2, base, o));
+    } else if constexpr (C::I8) {
+      const uint32_t o = pp_frag_off<C, KC, RB>(x0, kbase, lane, 0);
+      if constexpr (KC)
+        return *LDS_PTR(bf16x8, base, o);
+      else
+        return pp_read_tr<C>((uint32_t)(uintptr_t)base + o,
+                             (uint32_t)(uintptr_t)base + pp_frag_off<C, KC, RB>(x0, kbase, lane, 1));
     } else {
       return load_frag<C, KC, RB>(base, x0, kbase, lane, sw_on);
     }
@@ -280,7 +300,7 @@ __global__ __launch_bounds__(C::THREADS) void gemm_dma_kernel(KernelArgs a) {
   constexpr std::bool_constant<C::A_KC> akc{};
   constexpr std::bool_constant<C::B_KC> bkc{};
   constexpr std::integral_constant<int, C::A_RB> arb{};
-  constexpr std::integral_constant<int, C::B_RB> brb{};
+  constexpr std::integral_constant<int, C::SUB_RB> brb{};
   // Fragment r of K step kk, in the order the MFMAs first use them (the MFMAs run
   // A-fragment-major): A0, B0 .. B(FN-1), then A1 .. A(FM-1).
   auto read_one = [&](const lds_char* sb, int kk, Frag* xa, Frag* xb, auto rc) {
@@ -290,14 +310,15 @@ __global__ __launch_bounds__(C::THREADS) void gemm_dma_kernel(KernelArgs a) {
     if constexpr (!is_b)
       xa[idx] = frag(akc, arb, sb, xa0 + idx * C::MT, kk * C::KT);
     else
-      xb[idx] = frag(bkc, brb, sb + C::A_BYTES, xb0 + idx * C::MT, kk * C::KT);
+      xb[idx] = frag(bkc, brb, sb + C::A_BYTES + idx / FSUB * C::SUB_BYTES, xb0 + idx % FSUB * C::MT, kk * C::KT);
   };
   auto read_step = [&](const lds_char* sb, int kk, Frag* xa, Frag* xb) {
 #pragma unroll
     for (int i = 0; i < C::FM; ++i)
       xa[i] = frag(akc, arb, sb, xa0 + i * C::MT, kk * C::KT);
 #pragma unroll
-    for (int j = 0; j < C::FN; ++j) xb[j] = frag(bkc, brb, sb + C::A_BYTES, xb0 + j * C::MT, kk * C::KT);
+    for (int j = 0; j < C::FN; ++j)
+      xb[j] = frag(bkc, brb, sb + C::A_BYTES + j / FSUB * C::SUB_BYTES, xb0 + j % FSUB * C::MT, kk * C::KT);
   };
 
   // Scaled native E4M3: the scale bytes this lane's MFMAs take, one register per two
@@ -390,7 +411,7 @@ __global__ __launch_bounds__(C::THREADS) void gemm_dma_kernel(KernelArgs a) {
           else if constexpr (D::E8)
             mma(acc[i / C::FN][i % C::FN], wb[i % C::FN], wa[i / C::FN]);
           else
-            mma(acc[i / C::FN][i % C::FN], fb[kk & 1][i % C::FN], fa[kk & 1][i / C::FN]);
+            mma_of<C>(acc[i / C::FN][i % C::FN], fb[kk & 1][i % C::FN], fa[kk & 1][i / C::FN]);
           if constexpr (i >= RD0) {
             constexpr int r0 = NRF * (i - RD0) / (NMF - RD0), r1 = NRF * (i + 1 - RD0) / (NMF - RD0);
             static_for<r1 - r0>([&](auto jc) {
@@ -417,6 +438,9 @@ __global__ __launch_bounds__(C::THREADS) void gemm_dma_kernel(KernelArgs a) {
 #ifdef DBGEMM_EPILOGUE
   ep_tile<C, C::STAGE_BYTES, false>(a, acc, m0 + xa0, n0 + xb0, tm * C::WM + wm, wave, lane,
                                     (uint32_t)(uintptr_t)slot(std::integral_constant<int, 0>{}));
+#elif defined(DBGEMM_GATED)
+  gt_tile<C, OP, C::STAGE_BYTES, false>(a, acc, m0 + xa0, n0 + xb0, tm * C::WM + wm, wave, lane,
+                                        (uint32_t)(uintptr_t)slot(std::integral_constant<int, 0>{}));
 #else
   store_tile<C>(a, acc, m0 + xa0, n0 + xb0, lane);
 #endif
@@ -435,7 +459,16 @@ struct Reduce {
   static_assert(NP % CH == 0, "whole chunks");
 };
 
-#ifdef DBGEMM_EPILOGUE
+#if defined(DBGEMM_GATED)
+
+// The same for the gated operators (gt_strip): workgroup (tile, i) adds the partials of fragment
+// row i of every row of waves.
+template <class C, int OP>
+__global__ __launch_bounds__(C::THREADS) void split_reduce_gt_kernel(GatedArgs a) {
+  gt_strip<C, OP>(a, blockIdx.x / C::FM, blockIdx.x % C::FM, threadIdx.x);
+}
+
+#elif defined(DBGEMM_EPILOGUE)
 
 // The same with an epilogue: workgroup (tile, i) adds the partials of fragment row i of every
 // row of waves, puts the WM x 16 rows together in LDS and runs the epilogue over them.
@@ -520,15 +553,17 @@ __global__ __launch_bounds__(C::THREADS) void split_reduce_kernel(GemmArgs a) {
 
 #endif
 
-template <class C>
+template <class C, int OP = 0>
 hipError_t launch_cfg(const KernelArgs& a, hipStream_t s) {
   const int ntiles = a.tiles_m * a.tiles_n;
   const unsigned by = a.batch_y > 1 ? (unsigned)a.batch_y : 1u, bz = a.batch_z > 1 ? (unsigned)a.batch_z : 1u;
-  hipLaunchKernelGGL(gemm_dma_kernel<C>, dim3(grid_tiles(a), by, bz), dim3(C::THREADS), 0, s, a);
+  hipLaunchKernelGGL((gemm_dma_kernel<C, OP>), dim3(grid_tiles(a), by, bz), dim3(C::THREADS), 0, s, a);
   if (a.splits > 1) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-#ifdef DBGEMM_EPILOGUE
+#if defined(DBGEMM_GATED)
+    hipLaunchKernelGGL((split_reduce_gt_kernel<C, OP>), dim3(ntiles * C::FM), dim3(C::THREADS), 0, s, a);
+#elif defined(DBGEMM_EPILOGUE)
     hipLaunchKernelGGL(split_reduce_ep_kernel<C>, dim3(ntiles * C::FM), dim3(C::THREADS), 0, s, a);
 #else
     hipLaunchKernelGGL(split_reduce_kernel<C>, dim3(ntiles * Reduce<C>::CHUNKS), dim3(C::THREADS), 0, s, a);
@@ -540,15 +575,41 @@ hipError_t launch_cfg(const KernelArgs& a, hipStream_t s) {
 // This file is compiled once per transpose case (DBGEMM_DMA_TA, DBGEMM_DMA_TB) and half of
 // the policy table (DBGEMM_DMA_PART: the entries on even or odd lines of policies.inc), so
 // the eight groups of kernel instantiations build in parallel.
-// With DBGEMM_EPILOGUE once per transpose case (few entries).
+// With DBGEMM_EPILOGUE or DBGEMM_GATED once per transpose case (few entries).
 #if !defined(DBGEMM_DMA_TA) || !defined(DBGEMM_DMA_TB) || \
-    (!defined(DBGEMM_DMA_PART) && !defined(DBGEMM_EPILOGUE))
+    (!defined(DBGEMM_DMA_PART) && !defined(DBGEMM_EPILOGUE) && !defined(DBGEMM_GATED))
 #error "compile with -DDBGEMM_DMA_TA=0|1 -DDBGEMM_DMA_TB=0|1 -DDBGEMM_DMA_PART=0|1"
 #endif
 
 }  // namespace
 
-#ifdef DBGEMM_EPILOGUE
+#if defined(DBGEMM_GATED)
+
+#define DBGEMM_DMA_CAT2(in, b) launch_mfma_dma_gt_##in##b
+#define DBGEMM_DMA_CAT(a, b) DBGEMM_DMA_CAT2(a, b)
+
+hipError_t DBGEMM_DMA_CAT(DBGEMM_GATED, DBGEMM_DMA_TB)(const Policy& p, const GatedArgs& a, int* parts,
+                                                       hipStream_t s) {
+  constexpr int KIND = DBGEMM_GATED;
+  // partial rows: one per row of waves, or per strip of the second launch
+  *parts = a.tiles_m * (a.splits > 1 ? p.BM / p.WM / 16 : p.WM);
+#define DBGEMM_SIMT(name, eff)
+#define DBGEMM_MFMA(name_, pipe_, in_, bm_, bn_, bk_, wm_, wn_, mt_, st_, grp_, rn_, xcd_, sw_, eff_)      \
+  if constexpr (pipe_ == 1 && in_ == gt_policy_in(KIND) &&                                                 \
+                has_epilogue(pipe_, in_, bm_, bn_, bk_, mt_, ((sw_) >> 3) & 1, eff_))                      \
+    if (p.in_mode == in_ && p.BM == bm_ && p.BN == bn_ && p.BK == bk_ && p.WM == wm_ && p.WN == wn_ && p.stages == st_) { \
+      using C = Cfg<bm_, bn_, gt_bk(KIND, bk_), wm_, wn_, mt_, st_, gt_in(KIND), false, DBGEMM_DMA_TB != 0>;       \
+      using D = Cfg<bm_, bn_, gt_bk(KIND, bk_), wm_, wn_, mt_, st_, gt_in(KIND), false, DBGEMM_DMA_TB != 0, 1, true>; \
+      if (a.op == GT_GATED) return launch_cfg<D, GT_GATED>(a, s);                                          \
+      if (a.op == (KIND == GT_I8 ? GT_LINEAR : GT_GRAD)) return launch_cfg<C, KIND == GT_I8 ? GT_LINEAR : GT_GRAD>(a, s); \
+    }
+#include "policies.inc"
+#undef DBGEMM_SIMT
+#undef DBGEMM_MFMA
+  return hipErrorInvalidConfiguration;
+}
+
+#elif defined(DBGEMM_EPILOGUE)
 
 #define DBGEMM_DMA_CAT2(a, b) launch_mfma_dma_ep_##a##b
 #define DBGEMM_DMA_CAT(a, b) DBGEMM_DMA_CAT2(a, b)

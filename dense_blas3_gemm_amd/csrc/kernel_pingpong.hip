@@ -45,12 +45,17 @@
 #ifdef DBGEMM_EPILOGUE  // the kernels of products with an epilogue
 #include "epilogue_tile.h"
 #endif
+#ifdef DBGEMM_GATED  // the kernels of the gated operators
+#include "gated_tile.h"
+#endif
 
 namespace dbgemm {
 namespace {
 
 #ifdef DBGEMM_EPILOGUE
 using KernelArgs = GemmEpArgs;
+#elif defined(DBGEMM_GATED)
+using KernelArgs = GatedArgs;
 #else
 using KernelArgs = GemmArgs;
 #endif
@@ -92,8 +97,8 @@ template <class C>
 struct PingPong {
   static_assert(C::THREADS == 512 && C::WM == 2 && C::WN == 4, "two groups of four waves");
   static_assert(C::STAGES >= 2 && C::STAGES <= 5, "two to five LDS slots");
-  static_assert((C::IN == IN_BF16 || pp_e8<C>) && C::GES == C::ES,
-                "bf16 or E4M3 operands, LDS holds the global format");
+  static_assert((C::IN == IN_BF16 || C::I8 || pp_e8<C>) && C::GES == C::ES,
+                "bf16, E4M3 or 8-bit integer operands, LDS holds the global format");
   static_assert(!pp_e8<C> || C::MT == 16, "E4M3 tiles feed the 16x16x32 fragment map");
   static constexpr bool E8 = pp_e8<C>;
   // block scales: per K tile, one dword per operand row (its four UE8M0 bytes, one per K
@@ -330,7 +335,8 @@ __device__ __forceinline__ void pp_store_tile_lds(const GemmArgs& a, const typen
 // grid of GemmArgs (sk_dp whole tiles, then sk_grid workgroups sharing the K loops of the
 // other sk_tiles tiles).  Each workgroup runs its segments (a tile and a range [k0, k1) of
 // its K tiles) one after the other, each through the same two-group pipeline.
-template <class C, bool SK>
+// OP: what a gated operator's kernel does with its sums.
+template <class C, bool SK, int OP = 0>
 __global__ __launch_bounds__(512) void gemm_pp_kernel(KernelArgs a) {
   using P = PingPong<C>;
   constexpr int S = P::S;
@@ -371,13 +377,16 @@ __global__ __launch_bounds__(512) void gemm_pp_kernel(KernelArgs a) {
     tile_of(blockIdx.x, a, tm0, tn0, split_unused);
   }
 
+  // two B: the first four waves copy the one's sub-tile, the others the other's
+  const void* const b_ptr = C::DUAL && grp ? a.B2 : a.B;
+  const int64_t ldb = C::DUAL && grp ? a.ldb2 : a.ldb;
   const uint32_t a_rows = C::A_KC ? a.M : a.K;
   const uint32_t b_rows = C::B_KC ? a.N : a.K;
   // 32-bit offsets: every operand spans less than 2^31 bytes with 256 rows (of K for an
   // M/N-contiguous operand) to spare, more than the S tiles issued past the end
   const uint32_t a_kstep = C::A_KC ? C::BK * C::ES : (uint32_t)(C::BK * a.lda * C::ES);
-  const uint32_t b_kstep = C::B_KC ? C::BK * C::ES : (uint32_t)(C::BK * a.ldb * C::ES);
-  const uint32_t a_total = (uint32_t)(a_rows * a.lda * C::ES), b_total = (uint32_t)(b_rows * a.ldb * C::ES);
+  const uint32_t b_kstep = C::B_KC ? C::BK * C::ES : (uint32_t)(C::BK * ldb * C::ES);
+  const uint32_t a_total = (uint32_t)(a_rows * a.lda * C::ES), b_total = (uint32_t)(b_rows * ldb * C::ES);
   const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_char*)lds;
 
   for (;;) {
@@ -389,7 +398,7 @@ __global__ __launch_bounds__(512) void gemm_pp_kernel(KernelArgs a) {
       k1 = min(nk, k0 + (it_end - it));
       raster_tile(a.sk_dp + ts, a, tm, tn);
     }
-    const int m0 = tm * C::BM, n0 = tn * C::BN;
+    const int m0 = tm * C::BM, n0 = tn * C::SUB_BN;
     // The thread index through an opaque copy: everything derived from it below (fragment
     // addresses, copy offsets, partial-tile offsets) is computed again for each segment
     // instead of being hoisted out of the segment loop and held in registers across the
@@ -405,7 +414,10 @@ __global__ __launch_bounds__(512) void gemm_pp_kernel(KernelArgs a) {
     // transposing read only add whole rows (the swizzle depends on bits 0, 1 and 3 of the
     // row, which neither touches), so it sits at base[f] + (kk*KT + h*4) rows.  A slot
     // adds its offset; all of these constants become the reads' immediate offsets.
-    const int xa0 = wm * C::WTM, xb0 = wn * C::WTN;
+    // (Two B: fragments 0 .. FN / 2 - 1 of the one sub-tile, then the same columns of the other.)
+    const int xa0 = wm * C::WTM, xb0 = wn * (C::WTN / C::NSUB);
+    constexpr int FSUB = C::FN / C::NSUB;
+    constexpr int TRH = C::I8 ? 8 : 4;  // rows from a fragment's first transposing read to its second
     constexpr int A_NB = C::A_KC ? C::KSTEPS : C::FM, B_NB = C::B_KC ? C::KSTEPS : C::FN;
     uint32_t a_base[A_NB], b_base[B_NB];
   #pragma unroll
@@ -417,15 +429,16 @@ __global__ __launch_bounds__(512) void gemm_pp_kernel(KernelArgs a) {
     for (int v = 0; v < B_NB; ++v)
       b_base[v] = lds0 + P::B_OFF +
                   (C::B_KC ? pp_frag_off<C, true, C::B_RB>(xb0, v * C::KT, lane, 0)
-                           : pp_frag_off<C, false, C::B_RB>(xb0 + v * C::MT, 0, lane, 0));
+                           : (v / FSUB) * C::SUB_BYTES +
+                                 pp_frag_off<C, false, C::SUB_RB>(xb0 + (v % FSUB) * C::MT, 0, lane, 0));
     // LDS address of read h of fragment f (K step kk) of an operand in slot u
     auto a_addr = [&](int u, int kk, int f, int h) -> uint32_t {
       return C::A_KC ? a_base[kk] + (uint32_t)(u * C::A_BYTES + f * C::MT * C::A_RB)
-                     : a_base[f] + (uint32_t)(u * C::A_BYTES + (kk * C::KT + h * 4) * C::A_RB);
+                     : a_base[f] + (uint32_t)(u * C::A_BYTES + (kk * C::KT + h * TRH) * C::A_RB);
     };
     auto b_addr = [&](int u, int kk, int f, int h) -> uint32_t {
-      return C::B_KC ? b_base[kk] + (uint32_t)(u * C::B_BYTES + f * C::MT * C::B_RB)
-                     : b_base[f] + (uint32_t)(u * C::B_BYTES + (kk * C::KT + h * 4) * C::B_RB);
+      return C::B_KC ? b_base[kk] + (uint32_t)(u * C::B_BYTES + (f / FSUB) * C::SUB_BYTES + f % FSUB * C::MT * C::B_RB)
+                     : b_base[f] + (uint32_t)(u * C::B_BYTES + (kk * C::KT + h * TRH) * C::SUB_RB);
     };
 
     bf16x8 fa[C::FM], fb[C::FN];
@@ -519,10 +532,6 @@ __global__ __launch_bounds__(512) void gemm_pp_kernel(KernelArgs a) {
       for (int e = 0; e < 4; ++e) *(__attribute__((address_space(3))) uint32_t*)(uintptr_t)(d + e * P::SC_TABLE) = w[e];
     };
 
-    auto rd = [&](uint32_t addr) -> u16x4 {
-      return __builtin_bit_cast(u16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                                           (__attribute__((address_space(3))) s16x4*)(uintptr_t)addr));
-    };
     // (The plain 8-byte reads are volatile so that the compiler does not pair the reads of
     // two fragments 16 rows apart into one ds_read2st64_b64: the two addresses of a lane
     // then fall in the same banks; the LDS read probe's paired form, kind 5, runs 2.3x the
@@ -573,8 +582,7 @@ __global__ __launch_bounds__(512) void gemm_pp_kernel(KernelArgs a) {
         if constexpr (C::A_KC) {
           fa[i] = *(__attribute__((address_space(3))) bf16x8*)(uintptr_t)a_addr(u, kk, i, 0);
         } else {
-          const u16x4 lo = rd(a_addr(u, kk, i, 0)), hi = rd(a_addr(u, kk, i, 1));
-          fa[i] = __builtin_bit_cast(bf16x8, (u16x8){lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
+          fa[i] = pp_read_tr<C>(a_addr(u, kk, i, 0), a_addr(u, kk, i, 1));
         }
       }
   #pragma unroll
@@ -582,8 +590,7 @@ __global__ __launch_bounds__(512) void gemm_pp_kernel(KernelArgs a) {
         if constexpr (C::B_KC) {
           fb[j] = *(__attribute__((address_space(3))) bf16x8*)(uintptr_t)b_addr(u, kk, j, 0);
         } else {
-          const u16x4 lo = rd(b_addr(u, kk, j, 0)), hi = rd(b_addr(u, kk, j, 1));
-          fb[j] = __builtin_bit_cast(bf16x8, (u16x8){lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
+          fb[j] = pp_read_tr<C>(b_addr(u, kk, j, 0), b_addr(u, kk, j, 1));
         }
       }
     };
@@ -597,7 +604,7 @@ __global__ __launch_bounds__(512) void gemm_pp_kernel(KernelArgs a) {
       static_for<C::FM * C::FN>([&](auto ic) {
         constexpr int i = decltype(ic)::value;
         constexpr int row = i / C::FN, col = i % C::FN;
-        mma(acc[row][col], fb[col], fa[row]);
+        mma_of<C>(acc[row][col], fb[col], fa[row]);
         if constexpr (P::E8 && row + 1 < C::FM) {
           const float sc = P::MXS ? soa[P::MXS ? row + 1 : 0] : 1.0f;
           wpart[col] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(ra8[row + 1][col >> 1], sc,
@@ -642,19 +649,20 @@ __global__ __launch_bounds__(512) void gemm_pp_kernel(KernelArgs a) {
     }
 #pragma unroll
     for (int i = 0; i < P::B_IPW; ++i) {
-      const int p = (wave * P::B_IPW + i) * 64 + lane;
-      const int r = p / C::B_CPR;
-      const int c = (p % C::B_CPR) ^ pp_swz<C, C::B_KC, C::B_CPR>(r);
+      // (a chunk of its sub-tile)
+      const int p = (wave % (P::NW / C::NSUB) * P::B_IPW + i) * 64 + lane;
+      const int r = p / C::SUB_CPR;
+      const int c = (p % C::SUB_CPR) ^ pp_swz<C, C::B_KC, C::SUB_CPR>(r);
       if constexpr (C::B_KC)
-        b_off[i] = (n0 + r) < a.N ? (uint32_t)((n0 + r) * a.ldb + c * C::VEC) * C::ES : kOOB;
+        b_off[i] = (n0 + r) < a.N ? (uint32_t)((n0 + r) * ldb + c * C::VEC) * C::ES : kOOB;
       else
-        b_off[i] = (n0 + c * C::VEC) < a.N ? (uint32_t)(r * a.ldb + n0 + c * C::VEC) * C::ES : kOOB;
+        b_off[i] = (n0 + c * C::VEC) < a.N ? (uint32_t)(r * ldb + n0 + c * C::VEC) * C::ES : kOOB;
     }
     // the segment's end in K (elements), and the bytes of each operand before it: all of
     // a K-contiguous operand, the rows before it of an M/N-contiguous one
     const int kend = min(a.K, k1 * C::BK);
     const uint32_t a_lim = C::A_KC || !SK ? a_total : min(a_total, (uint32_t)(kend * a.lda * C::ES));
-    const uint32_t b_lim = C::B_KC || !SK ? b_total : min(b_total, (uint32_t)(kend * a.ldb * C::ES));
+    const uint32_t b_lim = C::B_KC || !SK ? b_total : min(b_total, (uint32_t)(kend * ldb * C::ES));
 
     // Copies of K tile kt into slot u: A blocks first, then B.  Tiles past the segment are
     // still issued (all their chunks read zeros), so that every wave has the same number
@@ -667,7 +675,7 @@ __global__ __launch_bounds__(512) void gemm_pp_kernel(KernelArgs a) {
       const uint32_t an = __builtin_amdgcn_readfirstlane(a_lim - min(ao, a_lim));
       const uint32_t bn = __builtin_amdgcn_readfirstlane(b_lim - min(bo, b_lim));
       const __amdgpu_buffer_rsrc_t rta = make_rsrc((const char*)a.A + ao, an);
-      const __amdgpu_buffer_rsrc_t rtb = make_rsrc((const char*)a.B + bo, bn);
+      const __amdgpu_buffer_rsrc_t rtb = make_rsrc((const char*)b_ptr + bo, bn);
       // this wave's first LDS block of each operand tile (its blocks are consecutive)
       const uint32_t la = lds0 + P::A_OFF + u * C::A_BYTES + (uint32_t)(wave * P::A_IPW) * 1024u;
       const uint32_t lb = lds0 + P::B_OFF + u * C::B_BYTES + (uint32_t)(wave * P::B_IPW) * 1024u;
@@ -683,7 +691,7 @@ __global__ __launch_bounds__(512) void gemm_pp_kernel(KernelArgs a) {
                                       [](int r) { return pp_swz<C, true, C::A_CPR>(r); }) < kleft ? a_off[q] : kOOB;
 #pragma unroll
         for (int q = 0; q < P::B_IPW; ++q)
-          ob[q] = !C::B_KC || chunk_k(wave * P::B_IPW + q, C::B_CPR, C::VEC,
+          ob[q] = !C::B_KC || chunk_k(wave % (P::NW / C::NSUB) * P::B_IPW + q, C::B_CPR, C::VEC,
                                       [](int r) { return pp_swz<C, true, C::B_CPR>(r); }) < kleft ? b_off[q] : kOOB;
         pp_copies<P::A_IPW, true>(la, oa, rta);
         pp_copies<P::B_IPW, true>(lb, ob, rtb);
@@ -850,6 +858,8 @@ __global__ __launch_bounds__(512) void gemm_pp_kernel(KernelArgs a) {
     } else {
 #ifdef DBGEMM_EPILOGUE
       ep_tile<C, P::LDS_BYTES, true>(a, acc, m0 + xa0, n0 + xb0, tm * C::WM + wm, wave, lane, lds0);
+#elif defined(DBGEMM_GATED)
+      gt_tile<C, OP, P::LDS_BYTES, true>(a, acc, m0 + xa0, n0 + xb0, tm * C::WM + wm, wave, lane, lds0);
 #else
       pp_store_tile_lds<C>(a, acc, m0, n0, grp, xb0, lane, t, lds0);
 #endif
@@ -858,7 +868,14 @@ __global__ __launch_bounds__(512) void gemm_pp_kernel(KernelArgs a) {
   }
 }
 
-#ifdef DBGEMM_EPILOGUE
+#if defined(DBGEMM_GATED)
+template <class C, int OP>
+hipError_t launch_pp(const KernelArgs& a, hipStream_t s) {
+  if (a.splits != 1 || a.sk_tiles > 0) return hipErrorInvalidConfiguration;
+  hipLaunchKernelGGL((gemm_pp_kernel<C, false, OP>), dim3(grid_tiles(a)), dim3(C::THREADS), 0, s, a);
+  return hipGetLastError();
+}
+#elif defined(DBGEMM_EPILOGUE)
 template <class C>
 hipError_t launch_pp(const KernelArgs& a, hipStream_t s) {
   if (a.splits != 1 || a.sk_tiles > 0) return hipErrorInvalidConfiguration;
@@ -900,14 +917,38 @@ hipError_t launch_pp(const KernelArgs& a, hipStream_t s) {
 
 }  // namespace
 
-#ifdef DBGEMM_EPILOGUE
+#if defined(DBGEMM_GATED)
+#define DBGEMM_PP_CAT2(in, b) launch_mfma_pp_gt_##in##b
+#elif defined(DBGEMM_EPILOGUE)
 #define DBGEMM_PP_CAT2(a, b) launch_mfma_pp_ep_##a##b
 #else
 #define DBGEMM_PP_CAT2(a, b) launch_mfma_pp_##a##b
 #endif
 #define DBGEMM_PP_CAT(a, b) DBGEMM_PP_CAT2(a, b)
 
-#ifdef DBGEMM_EPILOGUE
+#if defined(DBGEMM_GATED)
+
+hipError_t DBGEMM_PP_CAT(DBGEMM_GATED, DBGEMM_DMA_TB)(const Policy& p, const GatedArgs& a, int* parts,
+                                                      hipStream_t s) {
+  constexpr int KIND = DBGEMM_GATED;
+  *parts = a.tiles_m * p.WM;  // one partial row per row of waves
+#define DBGEMM_SIMT(name, eff)
+#define DBGEMM_MFMA(name_, pipe_, in_, bm_, bn_, bk_, wm_, wn_, mt_, st_, grp_, rn_, xcd_, sw_, eff_)              \
+  if constexpr (pipe_ == 2 && in_ == gt_policy_in(KIND) &&                                                         \
+                has_epilogue(pipe_, in_, bm_, bn_, bk_, mt_, ((sw_) >> 3) & 1, eff_))                              \
+    if (p.BM == bm_ && p.BN == bn_ && p.BK == bk_ && p.in_mode == in_) {                                          \
+      using C = Cfg<bm_, bn_, gt_bk(KIND, bk_), wm_, wn_, mt_, st_, gt_in(KIND), false, DBGEMM_DMA_TB != 0>;       \
+      using D = Cfg<bm_, bn_, gt_bk(KIND, bk_), wm_, wn_, mt_, st_, gt_in(KIND), false, DBGEMM_DMA_TB != 0, 1, true>; \
+      if (a.op == GT_GATED) return launch_pp<D, GT_GATED>(a, s);                                                  \
+      if (a.op == (KIND == GT_I8 ? GT_LINEAR : GT_GRAD)) return launch_pp<C, KIND == GT_I8 ? GT_LINEAR : GT_GRAD>(a, s); \
+    }
+#include "policies_pp.inc"
+#undef DBGEMM_SIMT
+#undef DBGEMM_MFMA
+  return hipErrorInvalidConfiguration;
+}
+
+#elif defined(DBGEMM_EPILOGUE)
 
 hipError_t DBGEMM_PP_CAT(DBGEMM_DMA_TA, DBGEMM_DMA_TB)(const Policy& p, const GemmEpArgs& a, int* parts,
                                                        hipStream_t s) {

@@ -12,19 +12,32 @@
 //   * eight neighbouring lanes fetch one line of 128 bytes.  (B [N][K] straight into registers,
 //     in the lanes that the MFMA wants, has neighbouring lanes on 16 different rows: 16.3 us
 //     against 11.1 for the same bytes by lines, 13 x 5120 x 5120.)
+//
+// The gated operators' kernels are built from the same source (DBGEMM_GATED): two B as two
+// sub-tiles of every slot, 8-bit integers whose sums meet as whole numbers.
 #include "epilogue.h"
 #include "mfma_common.h"
+#ifdef DBGEMM_GATED
+#include "gated_tile.h"
+#endif
 
 namespace dbgemm {
 namespace {
 
+#ifdef DBGEMM_GATED
+using KernelArgs = GatedArgs;
+#else
+using KernelArgs = GemmEpArgs;
+#endif
+
 template <class C, int WAVES_>
 struct Skinny {
   static constexpr int WAVES = WAVES_, THREADS = WAVES * 64, S = C::STAGES;
-  static_assert(C::WM == 1 && C::WN == 1 && C::MT == 16 && (C::IN == IN_BF16 || C::IN == IN_E4M3_LDS), "a wave's tile");
+  static_assert(C::WM == 1 && C::WN == 1 && C::MT == 16 && (C::IN == IN_BF16 || C::IN == IN_E4M3_LDS || C::I8),
+                "a wave's tile");
   static constexpr int SLOT = C::A_BYTES + C::B_BYTES;
-  static_assert(C::A_BYTES % 1024 == 0 && C::B_BYTES % 1024 == 0, "whole 1 KiB copies");
-  static constexpr int A_CP = C::A_BYTES / 1024, B_CP = C::B_BYTES / 1024, CP = A_CP + B_CP;
+  static_assert(C::A_BYTES % 1024 == 0 && C::SUB_BYTES % 1024 == 0, "whole 1 KiB copies");
+  static constexpr int A_CP = C::A_BYTES / 1024, SUB_CP = C::SUB_BYTES / 1024, B_CP = SUB_CP * C::NSUB, CP = A_CP + B_CP;
   static_assert(S * CP <= 63, "vmcnt range");
   static constexpr int LDR = C::BN + 4;  // floats per row of a wave's sums
   static constexpr int RING = WAVES * S * SLOT, SUMS = WAVES * C::BM * LDR * 4;
@@ -58,30 +71,39 @@ __device__ __forceinline__ int line_remap(int b, int total) {
   return (2 * ((x >> 1) * (runs / 8) + j / PER) + (x & 1)) * PER + j % PER;
 }
 
-template <class C, int WAVES>
-__global__ __launch_bounds__(WAVES * 64) void gemm_skinny_kernel(GemmEpArgs a) {
+// OP: what a gated operator's kernel does with its sums.
+template <class C, int WAVES, int OP = 0>
+__global__ __launch_bounds__(WAVES * 64) void gemm_skinny_kernel(KernelArgs a) {
   using P = Skinny<C, WAVES>;
   __shared__ __attribute__((aligned(1024))) char lds[P::LDS_BYTES];
   const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
   // (B [N][K]: a run of columns to each XCD)
   const int tn = C::B_KC ? xcd_remap(blockIdx.x, gridDim.x, 8)
-                         : line_remap<(128 > C::BN * C::ES ? 128 / (C::BN * C::ES) : 1)>(blockIdx.x, gridDim.x);
-  const int n0 = tn * C::BN;
+                         : line_remap<(128 > C::SUB_BN * C::ES ? 128 / (C::SUB_BN * C::ES) : 1)>(blockIdx.x, gridDim.x);
+  const int n0 = tn * C::SUB_BN;
 
   // ---- the epilogue's operands: thread t < OUT takes eight columns of a row at the end
-  constexpr int LPR = C::BN / 8, OUT = C::BM * LPR;
-  static_assert(LPR % 4 == 0 && OUT <= P::THREADS, "whole blocks of 32 columns, one step");
+  constexpr int LPR = C::SUB_BN / 8, OUT = C::BM * LPR;
+  static_assert(OUT <= P::THREADS, "one step");
   const int om = t / LPR, on = n0 + (t % LPR) * 8;
   const int nv = t < OUT && om < a.M && on < a.N ? 8 : 0;
+#ifdef DBGEMM_GATED
+  const GtCols<C::I8, OP> cols(a, on, nv);
+  const GtRaw raw = gt_fetch8<C::I8, OP>(a, om, on, nv);
+#else
+  static_assert(LPR % 4 == 0, "whole blocks of 32 columns");
   float bias[8];
   ep_bias8(a, on, nv, bias);
   const EpRaw raw = !a.ep.grad                ? ep_fetch8<EP_FORWARD, false>(a, om, on, nv)
                     : a.ep.z_kind == Z_MX ? ep_fetch8<EP_GRAD_MX, false>(a, om, on, nv)
                                           : ep_fetch8<EP_GRAD_BF16, false>(a, om, on, nv);
+#endif
 
   const __amdgpu_buffer_rsrc_t ra = make_rsrc(a.A, (uint32_t)(a.M * a.lda * C::ES));
   const __amdgpu_buffer_rsrc_t rb =
       make_rsrc(a.B, (uint32_t)((C::B_KC ? (int64_t)a.N : (int64_t)a.K) * a.ldb * C::ES));
+  const __amdgpu_buffer_rsrc_t rb2 =
+      C::DUAL ? make_rsrc(a.B2, (uint32_t)((C::B_KC ? (int64_t)a.N : (int64_t)a.K) * a.ldb2 * C::ES)) : rb;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_char*)lds;
   const uint32_t ring = __builtin_amdgcn_readfirstlane(lds0 + (uint32_t)(wave * P::S * P::SLOT));
 
@@ -89,6 +111,7 @@ __global__ __launch_bounds__(WAVES * 64) void gemm_skinny_kernel(GemmEpArgs a) {
   // p = 64 i + lane being row p / CPR, physical chunk p % CPR, which holds logical chunk
   // (p % CPR) ^ swizzle(row).  Byte offset of it in K tile 0 (past every buffer for a row past
   // M or a column past N), and its K index within a tile.
+  // (A second B has its sub-tile behind the first one's, and other offsets where its stride differs.)
   uint32_t a_off[P::A_CP], b_off[P::B_CP];
   int a_k[P::A_CP], b_k[P::B_CP];
 #pragma unroll
@@ -99,27 +122,37 @@ __global__ __launch_bounds__(WAVES * 64) void gemm_skinny_kernel(GemmEpArgs a) {
   }
 #pragma unroll
   for (int i = 0; i < P::B_CP; ++i) {
-    const int p = i * 64 + lane, r = p / C::B_CPR, c = (p % C::B_CPR) ^ pp_swz<C, C::B_KC, C::B_CPR>(r);
+    const int p = i % P::SUB_CP * 64 + lane, r = p / C::SUB_CPR, c = (p % C::SUB_CPR) ^ pp_swz<C, C::B_KC, C::SUB_CPR>(r);
+    const int64_t ldb = i < P::SUB_CP ? a.ldb : a.ldb2;
     if constexpr (C::B_KC) {
-      b_off[i] = n0 + r < a.N ? (uint32_t)(((n0 + r) * a.ldb + c * C::VEC) * C::ES) : kOOB;
+      b_off[i] = n0 + r < a.N ? (uint32_t)(((n0 + r) * ldb + c * C::VEC) * C::ES) : kOOB;
       b_k[i] = c * C::VEC;
     } else {
-      b_off[i] = n0 + c * C::VEC < a.N ? (uint32_t)((r * a.ldb + n0 + c * C::VEC) * C::ES) : kOOB;
+      b_off[i] = n0 + c * C::VEC < a.N ? (uint32_t)((r * ldb + n0 + c * C::VEC) * C::ES) : kOOB;
       b_k[i] = r;
     }
   }
   const uint32_t b_step = C::B_KC ? C::BK * C::ES : (uint32_t)(C::BK * a.ldb * C::ES);
+  const uint32_t b2_step = C::B_KC ? C::BK * C::ES : (uint32_t)(C::BK * a.ldb2 * C::ES);
   // copies of this wave's tile number it (K tile wave + it * WAVES) into slot u; what lies past K
   // reads zeros and touches no memory
   auto copy_tile = [&](int it, int u) {
     const int kt = wave + it * WAVES, left = a.K - kt * C::BK;
     const uint32_t ao = (uint32_t)(kt * C::BK * C::ES), bo = (uint32_t)kt * b_step;
     const uint32_t l = __builtin_amdgcn_readfirstlane(ring + (uint32_t)(u * P::SLOT));
-    skinny_copies<P::B_CP, 0>(
+    skinny_copies<P::SUB_CP, 0>(
         l + C::A_BYTES, [&](int i) { return b_k[i] < left && b_off[i] != kOOB ? b_off[i] + bo : kOOB; }, rb);
+    if constexpr (C::DUAL) {
+      const uint32_t bo2 = (uint32_t)kt * b2_step;
+      auto o = [&](int i) {
+        return b_k[P::SUB_CP + i] < left && b_off[P::SUB_CP + i] != kOOB ? b_off[P::SUB_CP + i] + bo2 : kOOB;
+      };
+      skinny_copies<P::SUB_CP, 0>(l + C::A_BYTES + C::SUB_BYTES, o, rb2);
+    }
     skinny_copies<P::A_CP, 0>(l, [&](int i) { return a_k[i] < left && a_off[i] != kOOB ? a_off[i] + ao : kOOB; }, ra);
   };
 
+  constexpr int FSUB = C::FN / C::NSUB;
   f32x4 acc[C::FM][C::FN];
 #pragma unroll
   for (int i = 0; i < C::FM; ++i)
@@ -140,12 +173,7 @@ __global__ __launch_bounds__(WAVES * 64) void gemm_skinny_kernel(GemmEpArgs a) {
     } else if constexpr (KC) {
       return *(__attribute__((address_space(3))) bf16x8*)(uintptr_t)o0;
     } else {
-      const uint32_t o1 = base + pp_frag_off<C, KC, RB>(x0, kk * C::KT, lane, 1);
-      const u16x4 lo = __builtin_bit_cast(u16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                                                     (__attribute__((address_space(3))) s16x4*)(uintptr_t)o0));
-      const u16x4 hi = __builtin_bit_cast(u16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                                                     (__attribute__((address_space(3))) s16x4*)(uintptr_t)o1));
-      return __builtin_bit_cast(bf16x8, (ep_u16x8){lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
+      return pp_read_tr<C>(o0, base + pp_frag_off<C, KC, RB>(x0, kk * C::KT, lane, 1));
     }
   };
 
@@ -167,12 +195,12 @@ __global__ __launch_bounds__(WAVES * 64) void gemm_skinny_kernel(GemmEpArgs a) {
             fa[i] = frag(std::true_type{}, std::integral_constant<int, C::A_RB>{}, base, i * 16, kk);
 #pragma unroll
           for (int j = 0; j < C::FN; ++j)
-            fb[j] = frag(std::bool_constant<C::B_KC>{}, std::integral_constant<int, C::B_RB>{}, base + C::A_BYTES,
-                         j * 16, kk);
+            fb[j] = frag(std::bool_constant<C::B_KC>{}, std::integral_constant<int, C::SUB_RB>{},
+                         base + C::A_BYTES + j / FSUB * C::SUB_BYTES, j % FSUB * 16, kk);
 #pragma unroll
           for (int i = 0; i < C::FM; ++i)
 #pragma unroll
-            for (int j = 0; j < C::FN; ++j) mma(acc[i][j], fb[j], fa[i]);
+            for (int j = 0; j < C::FN; ++j) mma_of<C>(acc[i][j], fb[j], fa[i]);
         }
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the slot has been read
         copy_tile(it0 + u + P::S, u);
@@ -184,7 +212,8 @@ __global__ __launch_bounds__(WAVES * 64) void gemm_skinny_kernel(GemmEpArgs a) {
 
   // ---- the waves' sums meet in LDS: a lane holds rows 16 i + lane % 16, columns 16 j +
   // 4 (lane / 16) .. + 3
-  float* sums = (float*)lds;
+  using Sum = std::conditional_t<C::I8, int, float>;
+  Sum* sums = (Sum*)lds;
 #pragma unroll
   for (int i = 0; i < C::FM; ++i)
 #pragma unroll
@@ -193,12 +222,51 @@ __global__ __launch_bounds__(WAVES * 64) void gemm_skinny_kernel(GemmEpArgs a) {
   __syncthreads();
   for (int x = t; x < C::BM * C::BN; x += P::THREADS) {
     const int at = x / C::BN * P::LDR + x % C::BN;
-    float v = sums[at];
+    Sum v = sums[at];
 #pragma unroll
     for (int w = 1; w < WAVES; ++w) v += sums[w * C::BM * P::LDR + at];
     sums[at] = v;
   }
   __syncthreads();
+#ifdef DBGEMM_GATED
+  float cs[8] = {}, cs2[8] = {};
+  if (nv) {
+    float w[8], w2[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const Sum* p = sums + om * P::LDR + (t % LPR) * 8 + i;
+      w[i] = C::I8 ? (float)*p : a.alpha * (float)*p;
+      if constexpr (C::DUAL) w2[i] = C::I8 ? (float)p[C::SUB_BN] : a.alpha * (float)p[C::SUB_BN];
+    }
+    ep_with_act(a.ep.act, [&](auto ac) EP_INLINE {
+      gt_finish8<false, C::I8, OP, decltype(ac)::value>(a, w, w2, raw, cols, om, on, cs, cs2);
+    });
+  }
+  if constexpr (OP == GT_GRAD) {  // every row is here: the column sums themselves
+    constexpr int OW = (OUT + 63) / 64;  // waves that hold rows
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      float* const out = k ? a.ep.sum2 : a.ep.sum1;
+      if (!out) continue;
+      float(&v)[8] = k ? cs2 : cs;
+#pragma unroll
+      for (int o = LPR; o < 64; o <<= 1)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] += __shfl_xor(v[i], o);
+      __syncthreads();
+      if (wave < OW && lane < LPR)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sums[wave * C::BN + lane * 8 + i] = v[i];
+      __syncthreads();
+      if (t < C::BN && n0 + t < a.N) {
+        float sum = sums[t];
+#pragma unroll
+        for (int w = 1; w < OW; ++w) sum += sums[w * C::BN + t];
+        out[n0 + t] = sum;
+      }
+    }
+  }
+#else
   float cs[8] = {};
   if (t < OUT) {
     float w[8];
@@ -226,7 +294,38 @@ __global__ __launch_bounds__(WAVES * 64) void gemm_skinny_kernel(GemmEpArgs a) {
       a.ep.colsum[n0 + t] = v;
     }
   }
+#endif
 }
+
+#ifdef DBGEMM_GATED
+
+// BM rows, SUB columns of each B, K tiles of 128 bytes of A, S slots to a wave
+template <int BM, int SUB, int S, int IN, bool KC, int OP>
+hipError_t launch(const GatedArgs& a, hipStream_t s) {
+  constexpr bool DUAL = OP == GT_GATED;
+  constexpr int WAVES = 4;
+  using C = Cfg<BM, DUAL ? 2 * SUB : SUB, IN == IN_BF16 ? 64 : 128, 1, 1, 16, S, IN, false, KC, 1, DUAL>;
+  hipLaunchKernelGGL((gemm_skinny_kernel<C, WAVES, OP>), dim3((unsigned)((a.N + SUB - 1) / SUB)), dim3(WAVES * 64), 0, s, a);
+  return hipGetLastError();
+}
+
+template <int IN, bool KC, int OP>
+hipError_t launch_rows(const GatedArgs& a, hipStream_t s) {
+  // columns of each B: two of them in the same LDS, and rows of [K][N] at least 64 bytes wide
+  constexpr int SUB = KC ? (OP == GT_GATED ? 16 : 32) : IN == IN_BF16 ? 32 : 64;
+  constexpr int S = OP == GT_GATED && !KC ? 2 : 3;
+  if (a.M <= 16) return launch<16, SUB, S, IN, KC, OP>(a, s);
+  if (a.M <= 32) return launch<32, SUB, S, IN, KC, OP>(a, s);
+  return launch<64, SUB < 32 ? SUB : 32, 2, IN, KC, OP>(a, s);
+}
+
+template <int IN, bool KC>
+hipError_t launch_op(const GatedArgs& a, hipStream_t s) {
+  if (a.op == GT_GATED) return launch_rows<IN, KC, GT_GATED>(a, s);
+  return launch_rows<IN, KC, IN == IN_I8 ? GT_LINEAR : GT_GRAD>(a, s);
+}
+
+#else
 
 // BM rows, BN columns, K tiles of 128 bytes of A, S slots to a wave
 template <int BM, int BN, int S, int WAVES, bool E8, bool KC>
@@ -246,7 +345,29 @@ hipError_t launch_rows(const GemmEpArgs& a, hipStream_t s) {
   return launch<64, 32, 2, 4, E8, KC>(a, s);
 }
 
+#endif
+
 }  // namespace
+
+#ifdef DBGEMM_GATED
+
+bool gated_skinny_serves(int op, int in_kind, int transB, int64_t M, int64_t K) {
+  return skinny_serves(in_kind != GT_BF16, 0, transB, M, K);
+}
+
+hipError_t launch_gated_skinny(const GatedArgs& a, hipStream_t s) {
+  if (a.M < 1 || a.M > 64 || a.N % 8 != 0) return hipErrorInvalidConfiguration;
+  switch (a.in_kind * 2 + (a.transB != 0)) {
+    case GT_BF16 * 2: return launch_op<IN_BF16, false>(a, s);
+    case GT_BF16 * 2 + 1: return launch_op<IN_BF16, true>(a, s);
+    case GT_E4M3 * 2: return launch_op<IN_E4M3_LDS, false>(a, s);
+    case GT_E4M3 * 2 + 1: return launch_op<IN_E4M3_LDS, true>(a, s);
+    case GT_I8 * 2: return launch_op<IN_I8, false>(a, s);
+    default: return launch_op<IN_I8, true>(a, s);
+  }
+}
+
+#else
 
 // Where this kernel is the faster one: up to some K, past which a workgroup's waves walk too
 // long and the tiled kernels' split of K wins.  Measured both ways on 24557 products of 1 to 64
@@ -279,5 +400,7 @@ hipError_t launch_skinny(const GemmEpArgs& a, hipStream_t s) {
   if (a.in_fp8) return a.transB ? launch_rows<true, true>(a, s) : launch_rows<true, false>(a, s);
   return a.transB ? launch_rows<false, true>(a, s) : launch_rows<false, false>(a, s);
 }
+
+#endif
 
 }  // namespace dbgemm

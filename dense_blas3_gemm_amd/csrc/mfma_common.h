@@ -98,29 +98,43 @@ __device__ inline void raster_tile(int L, const GemmArgs& a, int& tm, int& tn) {
 // IN_MX_NATIVE (the same operands on the scaled f8f6f4 MFMA, which applies the scales);
 // IN_E4M3_LDS (E4M3 operands kept as E4M3 bytes in LDS and widened exactly to bf16 in
 // registers after each fragment read, bf16 MFMA: the ping-pong kernel); IN_MX_LDS (the same
-// with a UE8M0 scale per 32 along K, applied by the widening: the ping-pong kernel).
-enum { IN_BF16 = 0, IN_E4M3 = 1, IN_E4M3_NATIVE = 2, IN_MX = 3, IN_MX_NATIVE = 4, IN_E4M3_LDS = 5, IN_MX_LDS = 6 };
+// with a UE8M0 scale per 32 along K, applied by the widening: the ping-pong kernel); IN_I8
+// (8-bit integers on the integer MFMA: the gated operators' kernels).
+enum {
+  IN_BF16 = 0,
+  IN_E4M3 = 1,
+  IN_E4M3_NATIVE = 2,
+  IN_MX = 3,
+  IN_MX_NATIVE = 4,
+  IN_E4M3_LDS = 5,
+  IN_MX_LDS = 6,
+  IN_I8 = 7
+};
 
 // READ_: 1 reads M/N-contiguous fragments with the transposing ds_read_b64_tr_*; 0 reads
 // them one element at a time (ds_read_u16), the plain-load rung of the read ablation.
+// DUAL_: two products of one A at once.  The B tile's BN columns are BN / 2 of each B, as two
+// sub-tiles in LDS one behind the other, and a wave's fragments are the same columns of both.
 template <int BM_, int BN_, int BK_, int WM_, int WN_, int MT_, int STAGES_, int IN_, bool TA_, bool TB_,
-          int READ_ = 1>
+          int READ_ = 1, bool DUAL_ = false>
 struct Cfg {
   static constexpr int BM = BM_, BN = BN_, BK = BK_, WM = WM_, WN = WN_, MT = MT_, STAGES = STAGES_;
   static constexpr int IN = IN_;
   static constexpr int READ = READ_;
   static_assert(READ == 1 || (IN != IN_E4M3_NATIVE && IN != IN_MX_NATIVE), "element-wise reads are for bf16");
   static constexpr bool TA = TA_, TB = TB_;
+  static constexpr bool DUAL = DUAL_;
+  static constexpr bool I8 = IN == IN_I8;
   static constexpr bool MXN = IN == IN_MX_NATIVE;  // block scales ride in LDS next to the tiles
   static constexpr bool FP8 = IN == IN_E4M3_NATIVE || MXN;  // fragments and MFMA are E4M3
   static constexpr int THREADS = WM * WN * 64;
   static constexpr int GES = IN == IN_BF16 ? 2 : 1;  // bytes per element in global memory
-  static constexpr int ES = (FP8 || IN == IN_E4M3_LDS || IN == IN_MX_LDS) ? 1 : 2;  // bytes per element in LDS
+  static constexpr int ES = (FP8 || IN == IN_E4M3_LDS || IN == IN_MX_LDS || I8) ? 1 : 2;  // bytes per element in LDS
   static constexpr int WIDEN = ES / GES;             // LDS chunks per global 16-byte chunk
   static constexpr int VEC = 16 / GES;               // elements per global 16-byte chunk
   static constexpr int WTM = BM / WM, WTN = BN / WN;
-  static constexpr int KT = FP8 ? (MT == 32 ? 64 : 128) : (MT == 32 ? 16 : 32);  // K per MFMA
-  static constexpr int KPL = FP8 ? 32 : 8;                                        // K per lane
+  static constexpr int KT = FP8 ? (MT == 32 ? 64 : 128) : I8 ? 64 : (MT == 32 ? 16 : 32);  // K per MFMA
+  static constexpr int KPL = FP8 ? 32 : I8 ? 16 : 8;                                        // K per lane
   static constexpr int FM = WTM / MT, FN = WTN / MT;
   static constexpr int KSTEPS = BK / KT;
   static constexpr int ACC = MT * MT / 64;  // accumulator floats per lane per block
@@ -132,6 +146,10 @@ struct Cfg {
   static constexpr int A_CPR = A_RB / 16, B_CPR = B_RB / 16;    // LDS chunks per row
   static constexpr int A_GCPR = A_COLS * GES / 16, B_GCPR = B_COLS * GES / 16;  // global chunks per row
   static constexpr int A_BYTES = A_ROWS * A_RB, B_BYTES = B_ROWS * B_RB;
+  // a B sub-tile (the whole tile unless DUAL): its columns, bytes, and the bytes and chunks of a row
+  static constexpr int NSUB = DUAL ? 2 : 1;
+  static constexpr int SUB_BN = BN / NSUB, SUB_BYTES = B_BYTES / NSUB;
+  static constexpr int SUB_RB = B_KC ? B_RB : B_RB / NSUB, SUB_CPR = SUB_RB / 16;
   // scaled native E4M3: one 32-bit word per tile row holding the UE8M0 bytes of the tile's
   // four 32-element K blocks, A rows then B rows
   static constexpr int A_SC_BYTES = MXN ? BM * 4 : 0, B_SC_BYTES = MXN ? BN * 4 : 0;
@@ -145,6 +163,8 @@ struct Cfg {
   static constexpr int DS_READS_PER_STEP = FM * A_FRAG_READS + FN * B_FRAG_READS;
 
   static_assert(WTM % MT == 0 && WTN % MT == 0, "wave tile must hold whole MFMA blocks");
+  static_assert(!DUAL || FN % 2 == 0, "a wave holds as many fragments of either B");
+  static_assert(!I8 || (MT == 16 && !TA), "8-bit integers: 16x16x64 MFMA, A [M][K]");
   static_assert(BK % KT == 0, "BK must hold whole MFMA K steps");
   static_assert(STAGES * STAGE_BYTES <= 160 * 1024, "LDS budget");
   static_assert(!MXN || (BK == 128 && MT == 32 && STAGES == 2 && !TA && TB),
@@ -216,6 +236,18 @@ __device__ inline void mma(f32x16& acc, const i32x8& b, const i32x8& a) {
 }
 __device__ inline void mma(f32x4& acc, const i32x8& b, const i32x8& a) {
   acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, acc, 0, 0, 0, 0, 0, 0);
+}
+
+// One MFMA of configuration C.  8-bit integers keep the registers of the bf16 form, 16 bytes of
+// K to a lane and four sums, whose bits are then whole numbers.
+template <class C, class Acc, class Frag>
+__device__ __forceinline__ void mma_of(Acc& acc, const Frag& b, const Frag& a) {
+  if constexpr (C::I8)
+    acc = __builtin_bit_cast(Acc, __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, b),
+                                                                        __builtin_bit_cast(i32x4, a),
+                                                                        __builtin_bit_cast(i32x4, acc), 0, 0, 0));
+  else
+    mma(acc, b, a);
 }
 
 // Scaled f8f6f4 MFMA: the first operand (the B fragment, rows n) is scaled by byte SELB
@@ -401,6 +433,12 @@ __device__ __forceinline__ int pp_swz(int r) {
       return (r >> (CPR == 4 ? 2 : 1)) & (CPR - 1);
     else
       return r & (CPR - 1);
+  } else if constexpr (C::I8 && !KC) {
+    // ds_read_b64_tr_b8 with the two halves of 16 K values to a lane 8 rows apart (so that the
+    // swizzle leaves out bit 3): a half wave reads rows r .. r + 7 and r + 16 .. r + 23 of one
+    // 16-byte column.  Rows of 256 bytes all start on one bank, shorter ones in turn.
+    constexpr int drop = CPR >= 16 ? 0 : CPR == 8 ? 1 : 2;  // row bits that the banks tell apart
+    return (((r & 7) >> drop) | (((r >> 4) & 1) << (3 - drop))) & (CPR - 1);
   } else {
     return swz<KC, false, CPR, C::MT>(r);
   }
@@ -426,9 +464,15 @@ __device__ __forceinline__ uint32_t pp_frag_off(int x0, int kbase, int lane, int
       const int xb = x0 + (t % 2) * 8;
       return (uint32_t)(k * RB + ((((xb >> 4) ^ pp_swz<C, false, CPR>(k)) << 4) | (xb & 15)));
     }
+  } else if constexpr (C::I8 && !KC) {
+    // as above, K values 16 (l / 16) + 8 h .. + 7
+    const int g = lane >> 4, t = lane & 15;
+    const int k = kbase + g * 16 + h * 8 + t / 2;
+    const int xb = x0 + (t % 2) * 8;
+    return (uint32_t)(k * RB + ((((xb >> 4) ^ pp_swz<C, false, CPR>(k)) << 4) | (xb & 15)));
   } else if constexpr (KC) {
     const int r = x0 + lane % C::MT;
-    const int c = (kbase + (lane / C::MT) * C::KPL) * 2 / 16;
+    const int c = (kbase + (lane / C::MT) * C::KPL) * C::ES / 16;
     return (uint32_t)(r * RB + ((c ^ swz<true, false, CPR, C::MT>(r)) << 4));
   } else {
     const int g = lane >> 4, s = lane & 15;
@@ -452,6 +496,23 @@ __device__ __forceinline__ bf16x8 pp_widen8(i32x2 v, float scale = 1.0f) {
   const int w2 = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[1], scale, false));
   const int w3 = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[1], scale, true));
   return __builtin_bit_cast(bf16x8, (i32x4){w0, w1, w2, w3});
+}
+
+// The fragment that two transposing reads make, 4 K values of bf16 or 8 of 8-bit integers each.
+template <class C>
+__device__ __forceinline__ bf16x8 pp_read_tr(uint32_t lo_at, uint32_t hi_at) {
+  if constexpr (C::I8) {
+    const i32x2 lo = __builtin_amdgcn_ds_read_tr8_b64_v2i32((__attribute__((address_space(3))) i32x2*)(uintptr_t)lo_at);
+    const i32x2 hi = __builtin_amdgcn_ds_read_tr8_b64_v2i32((__attribute__((address_space(3))) i32x2*)(uintptr_t)hi_at);
+    return __builtin_bit_cast(bf16x8, (i32x4){lo[0], lo[1], hi[0], hi[1]});
+  } else {
+    typedef unsigned short u16x8 __attribute__((ext_vector_type(8)));
+    const u16x4 lo = __builtin_bit_cast(u16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                                   (__attribute__((address_space(3))) s16x4*)(uintptr_t)lo_at));
+    const u16x4 hi = __builtin_bit_cast(u16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                                   (__attribute__((address_space(3))) s16x4*)(uintptr_t)hi_at));
+    return __builtin_bit_cast(bf16x8, (u16x8){lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
+  }
 }
 
 // Instruction-scheduling hints for one K step: NMF MFMAs, each followed by its even

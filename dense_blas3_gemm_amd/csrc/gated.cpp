@@ -92,6 +92,7 @@ Problem problem_of(const GatedArgs& a) {
   pr.c_kind = a.c_kind;
   pr.fast_ok = true;
   pr.ep = true;
+  pr.gt = true;
   return pr;
 }
 

@@ -114,6 +114,7 @@ struct Policy {
   int k_contig_only;  // serves only A [M][K] with B [N][K] (transA = 0, transB = 1)
   int a_kc_only;      // serves only A [M][K] (transA = 0)
   int ep_only;        // serves only products with an epilogue
+  int gt_only;        // serves only the gated operators' products
 };
 
 // The table entries whose kernels are also built with an epilogue behind the product
@@ -192,6 +193,7 @@ struct Problem {
   bool square_tiles = false;
   bool kband = false;  // per-tile K band (wave model: longest tiles first)
   bool ep = false;     // an epilogue behind the product (has_epilogue)
+  bool gt = false;     // the gated operators' kernels (with ep)
 };
 // Stream-K plan of a ping-pong policy on a problem (the GemmArgs fields of that name);
 // tiles == 0: none (the grid is whole rounds, or the policy has no stream-K form).

@@ -263,8 +263,8 @@ gemm_status_t gemm_hw_probe(gemm_handle_t h, int kind, int param, int iters, int
                             const void* src, int64_t src_bytes, unsigned long long* cycles);
 
 /* The policy table: count and names (index 0 .. count-1).  Out-of-range -> NULL.  Names that
- * begin with "ep_" are tiles of products with an epilogue only (gemm_run_act, gemm_run_dact, which
- * choose them by themselves): gemm_run under one returns NOT_SUPPORTED. */
+ * begin with "ep_" are tiles of products with an epilogue only (gemm_run_act, gemm_run_dact and the
+ * gated operators, which choose them by themselves): gemm_run under one returns NOT_SUPPORTED. */
 int gemm_policy_count(void);
 const char* gemm_policy_name(int index);
 

@@ -92,7 +92,8 @@ Problem problem_of(const GatedArgs& a) {
   pr.c_kind = a.c_kind;
   pr.fast_ok = true;
   pr.ep = true;
-  pr.gt = true;
+  pr.products = a.op == GT_GATED ? 2 : 1;
+  pr.elem = (int)in_bytes(a);
   return pr;
 }
 
@@ -108,23 +109,41 @@ bool operands_ok(const GatedArgs& a, int64_t cols) {
          (a.op != GT_GATED || fits(a.B2, a.ldb2, b_rows));
 }
 
+// The tile model's cost (2e6 units to about a microsecond) as the time of a call of a few rows,
+// each kind with its own factor: a fit, 9 to 10 % off in the mean square.  Column sums are one more
+// launch.
+double tiles_us(int in_kind, double cost, bool sums) {
+  const double factor = in_kind == GT_BF16 ? 0.77 : in_kind == GT_E4M3 ? 0.64 : 0.79;
+  return 3.6 + factor * cost / 2.0e6 + (sums ? 4.0 : 0.0);
+}
+// (no tile's time is less: the search among them is a microsecond of the host's)
+constexpr double kLeastTilesUs = 5.0;
+
 // a's columns, whole eights of them, on the MFMA kernels; false (nothing launched) where they, or
 // the workspace, cannot.  accumulate: the sums are added to dbias and dbias2.
 bool run_fused(const HandleView& v, GatedArgs a, float* dbias, float* dbias2, int accumulate, hipError_t* e) {
   const bool sums = dbias || dbias2;
-  if (!accumulate && gated_skinny_serves(a.op, a.in_kind, a.transB, a.M, a.K)) {
-    a.ep.sum1 = dbias;
-    a.ep.sum2 = dbias2;
-    *e = launch_gated_skinny(a, v.stream);
-    return true;
-  }
   const int nb = a.op == GT_GATED ? 2 : 1;
   Problem pr = problem_of(a);
   int sp = 1, idx2 = 0, sp2 = 1;
   double cost = 0.0;
   const int64_t split_floats = v.ws ? (int64_t)(kPartBytes / sizeof(float)) : 0;
+  // a few rows: their own kernel where its time by its model is less than any tile's, or than the
+  // chosen ones'
+  int few_cols = 0;
+  const double few = !accumulate && a.M <= kFewRows
+                         ? few_rows_us(a.op, a.in_kind, a.transB, a.M, a.N, a.K, &few_cols)
+                         : 0.0;
+  auto run_few = [&] {
+    a.ep.sum1 = dbias;
+    a.ep.sum2 = dbias2;
+    *e = launch_gated_skinny(a, few_cols, v.stream);
+    return true;
+  };
+  if (few_cols && few < kLeastTilesUs) return run_few();
   int idx = policy_select(pr, v.cu_count, split_floats, &sp, &cost);
   if (policy_at(idx).kind != KIND_MFMA) return false;
+  if (few_cols && few < tiles_us(a.in_kind, cost, sums)) return run_few();
   const Cut cut = policy_cut(pr, v.cu_count, split_floats, cost);
   GatedArgs a1 = a, a2 = a;
   const int64_t at = cut.p < 0 || cut.by_rows ? cut.at : cut.at / nb;

@@ -70,10 +70,12 @@ DBGEMM_GT_DECL(2, 0)
 DBGEMM_GT_DECL(2, 1)
 #undef DBGEMM_GT_DECL
 
-// Products of a few rows, the rest as for launch_mfma_gated; ep.sum1 and ep.sum2 receive the
-// column sums.
-bool gated_skinny_serves(int op, int in_kind, int transB, int64_t M, int64_t K);
-hipError_t launch_gated_skinny(const GatedArgs& a, hipStream_t s);
+// Products of up to kFewRows rows, `cols` columns of each B to a workgroup, the rest as for
+// launch_mfma_gated; ep.sum1 and ep.sum2 receive the column sums.
+constexpr int64_t kFewRows = 64;
+hipError_t launch_gated_skinny(const GatedArgs& a, int cols, hipStream_t s);
+// The columns that take the least time by a model, and that time in us.
+double few_rows_us(int op, int in_kind, int transB, int64_t M, int64_t N, int64_t K, int* cols);
 
 // Any sizes, strides and alignment (op(A) = A).  With ep.colsum set, *parts receives the number
 // of partial rows written (at most max_parts >= 1).

@@ -179,7 +179,7 @@ __device__ __forceinline__ void gt_tile(const GatedArgs& a, const typename AccOf
   constexpr int PASS = gt_pass_rows<C, LDS_BYTES>(RPS);
   constexpr int RB = C::WTN * 4, CPR = C::WTN / 4;  // bytes and 16-byte chunks of an LDS row
   constexpr int STEPS = PASS / RPS, ALL = C::WTM / RPS;
-  constexpr int WANT = OP != GT_GRAD ? 4 : C::STAGES > 2 || C::THREADS < 512 ? 2 : 1, BATCH = STEPS < WANT ? STEPS : WANT;
+  constexpr int WANT = OP == GT_GRAD ? 2 : 4, BATCH = STEPS < WANT ? STEPS : WANT;
   static_assert(PASS * RB * (C::THREADS / 64) <= LDS_BYTES && C::WTM % PASS == 0, "a pass of every wave fits");
   static_assert((CPR & (CPR - 1)) == 0 && PASS % RPS == 0 && STEPS % BATCH == 0, "whole steps and batches");
   const uint32_t mine = lds0 + (uint32_t)(wave * PASS * RB);

@@ -114,7 +114,6 @@ struct Policy {
   int k_contig_only;  // serves only A [M][K] with B [N][K] (transA = 0, transB = 1)
   int a_kc_only;      // serves only A [M][K] (transA = 0)
   int ep_only;        // serves only products with an epilogue
-  int gt_only;        // serves only the gated operators' products
 };
 
 // The table entries whose kernels are also built with an epilogue behind the product
@@ -193,7 +192,12 @@ struct Problem {
   bool square_tiles = false;
   bool kband = false;  // per-tile K band (wave model: longest tiles first)
   bool ep = false;     // an epilogue behind the product (has_epilogue)
-  bool gt = false;     // the gated operators' kernels (with ep)
+  // the gated operators' kernels: how many B share the columns (N is that of both), and the bytes
+  // of an element (8-bit integers are a problem of bf16 with half the K).  Their ping-pong tiles
+  // split K too, any of them 3, 6 or 12 ways, and the model knows what their operands take to be
+  // fetched.
+  int products = 0;
+  int elem = 2;
 };
 // Stream-K plan of a ping-pong policy on a problem (the GemmArgs fields of that name);
 // tiles == 0: none (the grid is whole rounds, or the policy has no stream-K form).

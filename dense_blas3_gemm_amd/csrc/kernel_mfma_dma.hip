@@ -106,16 +106,8 @@ struct Dma {
 };
 
 // OP: what a gated operator's kernel does with its sums.
-//
-// Two-stage tiles leave room for several workgroups on a CU: four waves to a SIMD.
-#ifdef DBGEMM_GATED
-#define DBGEMM_DMA_BOUNDS(C) __launch_bounds__(C::THREADS, C::STAGES == 2 ? 4 : 1)
-#else
-#define DBGEMM_DMA_BOUNDS(C) __launch_bounds__(C::THREADS)
-#endif
-
 template <class C, int OP = 0>
-__global__ DBGEMM_DMA_BOUNDS(C) void gemm_dma_kernel(KernelArgs a) {
+__global__ __launch_bounds__(C::THREADS) void gemm_dma_kernel(KernelArgs a) {
   using D = Dma<C>;
   // One LDS object per ring slot: the compiler tracks the loads into each slot on
   // its own, so its automatic waits before LDS reads wait for that slot only.
@@ -628,8 +620,7 @@ hipError_t DBGEMM_DMA_CAT(DBGEMM_DMA_TA, DBGEMM_DMA_TB)(const Policy& p, const G
   *parts = a.tiles_m * (a.splits > 1 ? p.BM / p.WM / 16 : p.WM);
 #define DBGEMM_SIMT(name, eff)
 #define DBGEMM_MFMA(name_, pipe_, in_, bm_, bn_, bk_, wm_, wn_, mt_, st_, grp_, rn_, xcd_, sw_, eff_)      \
-  if constexpr (pipe_ == 1 && !(((sw_) >> 6) & 1) &&                                                       \
-                has_epilogue(pipe_, in_, bm_, bn_, bk_, mt_, ((sw_) >> 3) & 1, eff_))                      \
+  if constexpr (pipe_ == 1 && has_epilogue(pipe_, in_, bm_, bn_, bk_, mt_, ((sw_) >> 3) & 1, eff_))        \
     if (p.in_mode == in_ && p.BM == bm_ && p.BN == bn_ && p.BK == bk_ && p.WM == wm_ && p.WN == wn_ && p.stages == st_) \
       return launch_cfg<Cfg<bm_, bn_, bk_, wm_, wn_, mt_, st_, in_, DBGEMM_DMA_TA != 0, DBGEMM_DMA_TB != 0>>(a, s);
 #include "policies.inc"

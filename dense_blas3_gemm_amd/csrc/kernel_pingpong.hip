@@ -335,8 +335,10 @@ __device__ __forceinline__ void pp_store_tile_lds(const GemmArgs& a, const typen
 // grid of GemmArgs (sk_dp whole tiles, then sk_grid workgroups sharing the K loops of the
 // other sk_tiles tiles).  Each workgroup runs its segments (a tile and a range [k0, k1) of
 // its K tiles) one after the other, each through the same two-group pipeline.
-// OP: what a gated operator's kernel does with its sums.
-template <class C, bool SK, int OP = 0>
+// OP: what a gated operator's kernel does with its sums.  SPLIT: those kernels' form for a product
+// whose K is split (GemmArgs::splits), which leaves its part of the sums in the workspace (one kernel
+// for both spilled registers in the epilogue: 935 us, so 1010 at 4096 x 13696 x 5120).
+template <class C, bool SK, int OP = 0, bool SPLIT = false>
 __global__ __launch_bounds__(512) void gemm_pp_kernel(KernelArgs a) {
   using P = PingPong<C>;
   constexpr int S = P::S;
@@ -357,7 +359,7 @@ __global__ __launch_bounds__(512) void gemm_pp_kernel(KernelArgs a) {
   // one whole tile.  `slot` is the stream-K workgroup's index: consecutive indices share
   // tiles, and they are grouped by XCD (ids b run on XCD b % xcd) so that a tile's owner
   // and the workgroups that hand it partials mostly share one L2.
-  int it = 0, it_end = nk, slot = 0;
+  int it = 0, it_end = nk, slot = 0, split = 0;
   int tm0 = 0, tn0 = 0;
   bool whole = true;
   if constexpr (SK) {
@@ -373,8 +375,7 @@ __global__ __launch_bounds__(512) void gemm_pp_kernel(KernelArgs a) {
       if (it >= it_end) return;  // an empty range (uniform over the workgroup)
     }
   } else {
-    int split_unused;  // unsplit
-    tile_of(blockIdx.x, a, tm0, tn0, split_unused);
+    tile_of(blockIdx.x, a, tm0, tn0, split);
   }
 
   // two B: the first four waves copy the one's sub-tile, the others the other's
@@ -397,6 +398,10 @@ __global__ __launch_bounds__(512) void gemm_pp_kernel(KernelArgs a) {
       k0 = it - ts * nk;
       k1 = min(nk, k0 + (it_end - it));
       raster_tile(a.sk_dp + ts, a, tm, tn);
+    }
+    if constexpr (SPLIT) {
+      k0 = split * a.kt_per_split;
+      k1 = min(nk, k0 + a.kt_per_split);
     }
     const int m0 = tm * C::BM, n0 = tn * C::SUB_BN;
     // The thread index through an opaque copy: everything derived from it below (fragment
@@ -661,8 +666,8 @@ __global__ __launch_bounds__(512) void gemm_pp_kernel(KernelArgs a) {
     // the segment's end in K (elements), and the bytes of each operand before it: all of
     // a K-contiguous operand, the rows before it of an M/N-contiguous one
     const int kend = min(a.K, k1 * C::BK);
-    const uint32_t a_lim = C::A_KC || !SK ? a_total : min(a_total, (uint32_t)(kend * a.lda * C::ES));
-    const uint32_t b_lim = C::B_KC || !SK ? b_total : min(b_total, (uint32_t)(kend * ldb * C::ES));
+    const uint32_t a_lim = C::A_KC || !(SK || SPLIT) ? a_total : min(a_total, (uint32_t)(kend * a.lda * C::ES));
+    const uint32_t b_lim = C::B_KC || !(SK || SPLIT) ? b_total : min(b_total, (uint32_t)(kend * ldb * C::ES));
 
     // Copies of K tile kt into slot u: A blocks first, then B.  Tiles past the segment are
     // still issued (all their chunks read zeros), so that every wave has the same number
@@ -859,7 +864,11 @@ __global__ __launch_bounds__(512) void gemm_pp_kernel(KernelArgs a) {
 #ifdef DBGEMM_EPILOGUE
       ep_tile<C, P::LDS_BYTES, true>(a, acc, m0 + xa0, n0 + xb0, tm * C::WM + wm, wave, lane, lds0);
 #elif defined(DBGEMM_GATED)
-      gt_tile<C, OP, P::LDS_BYTES, true>(a, acc, m0 + xa0, n0 + xb0, tm * C::WM + wm, wave, lane, lds0);
+      if constexpr (SPLIT)  // in register order, for the second launch
+        pp_store_partial<C>(a.ws + ((size_t)(tm * a.tiles_n + tn) * a.splits + split) * (C::BM * C::BN), acc,
+                            (uint32_t)lane_t * 16u);
+      else
+        gt_tile<C, OP, P::LDS_BYTES, true>(a, acc, m0 + xa0, n0 + xb0, tm * C::WM + wm, wave, lane, lds0);
 #else
       pp_store_tile_lds<C>(a, acc, m0, n0, grp, xb0, lane, t, lds0);
 #endif
@@ -869,10 +878,25 @@ __global__ __launch_bounds__(512) void gemm_pp_kernel(KernelArgs a) {
 }
 
 #if defined(DBGEMM_GATED)
+// A split product's second launch: workgroup (tile, i) adds the partials of fragment row i of every
+// row of waves and finishes them.  (The partials of 361 x 7360 x 19232 are 58 tiles of 256 x 256 in
+// four parts: one round of the CUs where the whole tiles fill a quarter of one.)
+template <class C, int OP>
+__global__ __launch_bounds__(C::THREADS) void pp_split_reduce_kernel(GatedArgs a) {
+  gt_strip<C, OP>(a, blockIdx.x / C::FM, blockIdx.x % C::FM, threadIdx.x);
+}
+
 template <class C, int OP>
 hipError_t launch_pp(const KernelArgs& a, hipStream_t s) {
-  if (a.splits != 1 || a.sk_tiles > 0) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL((gemm_pp_kernel<C, false, OP>), dim3(grid_tiles(a)), dim3(C::THREADS), 0, s, a);
+  if (a.splits < 1 || (a.splits > 1 && !a.ws) || a.sk_tiles > 0) return hipErrorInvalidConfiguration;
+  if (a.splits == 1) {
+    hipLaunchKernelGGL((gemm_pp_kernel<C, false, OP>), dim3(grid_tiles(a)), dim3(C::THREADS), 0, s, a);
+  } else {
+    hipLaunchKernelGGL((gemm_pp_kernel<C, false, OP, true>), dim3(grid_tiles(a)), dim3(C::THREADS), 0, s, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((pp_split_reduce_kernel<C, OP>), dim3(a.tiles_m * a.tiles_n * C::FM), dim3(C::THREADS), 0, s, a);
+  }
   return hipGetLastError();
 }
 #elif defined(DBGEMM_EPILOGUE)
@@ -931,7 +955,8 @@ hipError_t launch_pp(const KernelArgs& a, hipStream_t s) {
 hipError_t DBGEMM_PP_CAT(DBGEMM_GATED, DBGEMM_DMA_TB)(const Policy& p, const GatedArgs& a, int* parts,
                                                       hipStream_t s) {
   constexpr int KIND = DBGEMM_GATED;
-  *parts = a.tiles_m * p.WM;  // one partial row per row of waves
+  // partial rows: one per row of waves, or per strip of the second launch
+  *parts = a.tiles_m * (a.splits > 1 ? p.BM / p.WM / 16 : p.WM);
 #define DBGEMM_SIMT(name, eff)
 #define DBGEMM_MFMA(name_, pipe_, in_, bm_, bn_, bk_, wm_, wn_, mt_, st_, grp_, rn_, xcd_, sw_, eff_)              \
   if constexpr (pipe_ == 2 && in_ == gt_policy_in(KIND) &&                                                         \

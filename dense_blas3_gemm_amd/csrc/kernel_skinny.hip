@@ -18,6 +18,8 @@
 #include "epilogue.h"
 #include "mfma_common.h"
 #ifdef DBGEMM_GATED
+#include <cmath>
+
 #include "gated_tile.h"
 #endif
 
@@ -299,30 +301,45 @@ __global__ __launch_bounds__(WAVES * 64) void gemm_skinny_kernel(KernelArgs a) {
 
 #ifdef DBGEMM_GATED
 
-// BM rows, SUB columns of each B, K tiles of 128 bytes of A, S slots to a wave
-template <int BM, int SUB, int S, int IN, bool KC, int OP>
+// The least columns of each B to a workgroup are the best where there are few workgroups or B is
+// [N][K]; rows of B [K][N] are asked for in pieces of that many columns, and a line costs the same
+// whatever is taken of it.
+constexpr int kFewCols[] = {16, 32, 64};
+constexpr int few_bm(int64_t M) { return M <= 16 ? 16 : M <= 32 ? 32 : 64; }
+constexpr bool few_fits(int bm, int sub) { return bm * sub / 8 <= 256; }  // (the epilogue's one step)
+
+// BM rows, SUB columns of each B, K tiles of 128 bytes of A, four waves of two slots each (three
+// slots, or eight waves, measured alike or slower by up to 30 %)
+template <int BM, int SUB, int IN, bool KC, int OP>
 hipError_t launch(const GatedArgs& a, hipStream_t s) {
-  constexpr bool DUAL = OP == GT_GATED;
-  constexpr int WAVES = 4;
-  using C = Cfg<BM, DUAL ? 2 * SUB : SUB, IN == IN_BF16 ? 64 : 128, 1, 1, 16, S, IN, false, KC, 1, DUAL>;
-  hipLaunchKernelGGL((gemm_skinny_kernel<C, WAVES, OP>), dim3((unsigned)((a.N + SUB - 1) / SUB)), dim3(WAVES * 64), 0, s, a);
-  return hipGetLastError();
+  if constexpr (few_fits(BM, SUB)) {
+    constexpr bool DUAL = OP == GT_GATED;
+    using C = Cfg<BM, DUAL ? 2 * SUB : SUB, IN == IN_BF16 ? 64 : 128, 1, 1, 16, 2, IN, false, KC, 1, DUAL>;
+    hipLaunchKernelGGL((gemm_skinny_kernel<C, 4, OP>), dim3((unsigned)((a.N + SUB - 1) / SUB)), dim3(256), 0, s, a);
+    return hipGetLastError();
+  } else {
+    return hipErrorInvalidConfiguration;
+  }
+}
+
+template <int SUB, int IN, bool KC, int OP>
+hipError_t launch_bm(const GatedArgs& a, hipStream_t s) {
+  if (a.M <= 16) return launch<16, SUB, IN, KC, OP>(a, s);
+  if (a.M <= 32) return launch<32, SUB, IN, KC, OP>(a, s);
+  return launch<64, SUB, IN, KC, OP>(a, s);
 }
 
 template <int IN, bool KC, int OP>
-hipError_t launch_rows(const GatedArgs& a, hipStream_t s) {
-  // columns of each B: two of them in the same LDS, and rows of [K][N] at least 64 bytes wide
-  constexpr int SUB = KC ? (OP == GT_GATED ? 16 : 32) : IN == IN_BF16 ? 32 : 64;
-  constexpr int S = OP == GT_GATED && !KC ? 2 : 3;
-  if (a.M <= 16) return launch<16, SUB, S, IN, KC, OP>(a, s);
-  if (a.M <= 32) return launch<32, SUB, S, IN, KC, OP>(a, s);
-  return launch<64, SUB < 32 ? SUB : 32, 2, IN, KC, OP>(a, s);
+hipError_t launch_rows(const GatedArgs& a, int cols, hipStream_t s) {
+  if (cols == 16) return launch_bm<16, IN, KC, OP>(a, s);
+  if (cols == 32) return launch_bm<32, IN, KC, OP>(a, s);
+  return launch_bm<64, IN, KC, OP>(a, s);
 }
 
 template <int IN, bool KC>
-hipError_t launch_op(const GatedArgs& a, hipStream_t s) {
-  if (a.op == GT_GATED) return launch_rows<IN, KC, GT_GATED>(a, s);
-  return launch_rows<IN, KC, IN == IN_I8 ? GT_LINEAR : GT_GRAD>(a, s);
+hipError_t launch_op(const GatedArgs& a, int cols, hipStream_t s) {
+  if (a.op == GT_GATED) return launch_rows<IN, KC, GT_GATED>(a, cols, s);
+  return launch_rows<IN, KC, IN == IN_I8 ? GT_LINEAR : GT_GRAD>(a, cols, s);
 }
 
 #else
@@ -351,19 +368,42 @@ hipError_t launch_rows(const GemmEpArgs& a, hipStream_t s) {
 
 #ifdef DBGEMM_GATED
 
-bool gated_skinny_serves(int op, int in_kind, int transB, int64_t M, int64_t K) {
-  return skinny_serves(in_kind != GT_BF16, 0, transB, M, K);
+// A workgroup's wave takes every fourth of the K tiles (128 bytes of K).  A K tile costs a wave what
+// its lines (128 bytes, or the piece of one that a row of B [K][N] has in these columns) and its
+// bytes take to be asked for; and all workgroups together need the CU's share of the memory's rate
+// and of its line requests.  Fitted to 9000 products of 1 to 64 rows, N and K from 256 to 20480, in
+// all kinds, layouts and the three widths: 15 % off in the mean square.  The faster of this formula's
+// best width and the tiles by their model was 3 % slower than the fastest of the four in the mean.
+double few_rows_us(int op, int in_kind, int transB, int64_t M, int64_t N, int64_t K, int* cols) {
+  const int bm = few_bm(M), nb = op == GT_GATED ? 2 : 1, es = in_kind == GT_BF16 ? 2 : 1;
+  const double its = (double)((K * es + 127) / 128) / 4.0;
+  double best = 0.0;
+  *cols = 0;
+  for (int sub : kFewCols) {
+    if (!few_fits(bm, sub)) continue;
+    const double groups = (double)((N + sub - 1) / sub) / 256.0;
+    const double lines = nb * (transB ? sub : 128 / es) + bm, kb = nb * sub / 8.0;
+    double wave = 0.00435 * lines + 0.0222 * kb;
+    if (in_kind == GT_E4M3 && transB) wave *= 1.39;  // (the widening, where the lines do not hide it)
+    const double all = 4.0 * (0.00141 * lines + 0.0401 * kb) * groups;
+    const double us = 2.69 + 0.777 * bm * sub * nb / 1024.0 + its * std::sqrt(std::sqrt(wave * wave * wave * wave + all * all * all * all));
+    if (*cols == 0 || us < best) {
+      best = us;
+      *cols = sub;
+    }
+  }
+  return best;
 }
 
-hipError_t launch_gated_skinny(const GatedArgs& a, hipStream_t s) {
+hipError_t launch_gated_skinny(const GatedArgs& a, int cols, hipStream_t s) {
   if (a.M < 1 || a.M > 64 || a.N % 8 != 0) return hipErrorInvalidConfiguration;
   switch (a.in_kind * 2 + (a.transB != 0)) {
-    case GT_BF16 * 2: return launch_op<IN_BF16, false>(a, s);
-    case GT_BF16 * 2 + 1: return launch_op<IN_BF16, true>(a, s);
-    case GT_E4M3 * 2: return launch_op<IN_E4M3_LDS, false>(a, s);
-    case GT_E4M3 * 2 + 1: return launch_op<IN_E4M3_LDS, true>(a, s);
-    case GT_I8 * 2: return launch_op<IN_I8, false>(a, s);
-    default: return launch_op<IN_I8, true>(a, s);
+    case GT_BF16 * 2: return launch_op<IN_BF16, false>(a, cols, s);
+    case GT_BF16 * 2 + 1: return launch_op<IN_BF16, true>(a, cols, s);
+    case GT_E4M3 * 2: return launch_op<IN_E4M3_LDS, false>(a, cols, s);
+    case GT_E4M3 * 2 + 1: return launch_op<IN_E4M3_LDS, true>(a, cols, s);
+    case GT_I8 * 2: return launch_op<IN_I8, false>(a, cols, s);
+    default: return launch_op<IN_I8, true>(a, cols, s);
   }
 }
 

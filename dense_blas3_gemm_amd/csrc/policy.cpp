@@ -6,6 +6,7 @@
 // ablation) are the model here.  On MI355X a "wave" is one round of workgroups over
 // the 256 CUs: a grid of T tiles with `occ` resident workgroups per CU takes
 // ceil(T / (CUs * occ)) rounds, each as long as one CU needs for `occ` tiles.
+#include <cmath>
 #include <cstring>
 
 #include "gemm_internal.h"
@@ -14,10 +15,10 @@ namespace dbgemm {
 namespace {
 
 const Policy kTable[] = {
-#define DBGEMM_SIMT(name_, eff_) {name_, KIND_SIMT, 0, -1, 64, 64, 16, 1, 1, 0, 1, 1, 0, 1, 0, 0, 1, 256, eff_, 0, 0, 0, 0},
+#define DBGEMM_SIMT(name_, eff_) {name_, KIND_SIMT, 0, -1, 64, 64, 16, 1, 1, 0, 1, 1, 0, 1, 0, 0, 1, 256, eff_, 0, 0, 0},
 #define DBGEMM_MFMA(name_, pipe_, in_, bm_, bn_, bk_, wm_, wn_, mt_, st_, grp_, rn_, xcd_, sw_, eff_) \
   {name_, KIND_MFMA, pipe_, in_, bm_, bn_, bk_, wm_, wn_, mt_, st_, grp_, rn_, xcd_, (sw_) & 1,        \
-   ((sw_) >> 1) & 1, ((sw_) >> 2) & 1 ? 0 : 1, (wm_) * (wn_) * 64, eff_, ((sw_) >> 3) & 1, ((sw_) >> 4) & 1, ((sw_) >> 5) & 1, ((sw_) >> 6) & 1},
+   ((sw_) >> 1) & 1, ((sw_) >> 2) & 1 ? 0 : 1, (wm_) * (wn_) * 64, eff_, ((sw_) >> 3) & 1, ((sw_) >> 4) & 1, ((sw_) >> 5) & 1},
 #include "policies.inc"
 #include "policies_pp.inc"
 #undef DBGEMM_SIMT
@@ -58,7 +59,7 @@ int policy_find(const char* name) {
 bool policy_serves(const Policy& p, const Problem& pr) {
   if (p.kind == KIND_SIMT) return true;
   if (p.kind != KIND_MFMA || !pr.fast_ok) return false;
-  if ((p.ep_only && !pr.ep) || (p.gt_only && !pr.gt)) return false;
+  if (p.ep_only && !pr.ep) return false;
   if (pr.ep && !has_epilogue(p.pipe, p.in_mode, p.BM, p.BN, p.BK, p.MT, p.k_contig_only, p.efficiency)) return false;
   if (p.k_contig_only && (pr.transA != 0 || pr.transB != 1)) return false;
   if (p.a_kc_only && pr.transA != 0) return false;
@@ -85,7 +86,8 @@ int64_t split_kt(const Policy& p, int64_t K, int splits) {
 
 bool split_allowed(const Policy& p, const Problem& pr, int splits, int64_t ws_floats) {
   if (splits == 1) return true;
-  if (p.pipe != 1 || split_kt(p, pr.K, splits) == 0) return false;  // direct-to-LDS ring kernels
+  // direct-to-LDS ring kernels (and the gated operators' ping-pong ones)
+  if ((p.pipe != 1 && !(p.pipe == 2 && pr.products)) || split_kt(p, pr.K, splits) == 0) return false;
   return split_ws_floats(p, pr, splits) <= ws_floats;
 }
 
@@ -124,6 +126,22 @@ constexpr double K0 = 256.0;  // prologue + epilogue cost of a tile, in K-equiva
 // The model's unit is BM*BN*K/efficiency per CU; one us is about 2e6 of them (a 64 x 64
 // tile at efficiency 0.5 advances about 265 K per us).
 constexpr double kUnitsPerUs = 2.0e6;
+
+// What the operands of a gated operator's grid take to be fetched, in us on 256 CUs: a CU asks for
+// so many lines (128 bytes, or the piece of one that a tile takes of a row of B [K][N]) and moves so
+// many bytes (the rates of the few-row kernel's model, less a tenth).  It decides where there are
+// few rows of A, or few columns of 1-byte elements to a tile: 19 x 9824 x 8432 of 8-bit integers,
+// both B [K][N], 80 us on 64 x 64 tiles, 32 bytes of a row each, and 42 on 128 x 128.  Over 1500 drawn
+// products the choice was 4.4 % behind the fastest for up to 64 rows and 2.3 % for more; with this
+// 3.0 and 1.7.
+double fetch_us(const Policy& p, const Problem& pr) {
+  const double tiles = (double)((pr.M + p.BM - 1) / p.BM) * (double)((pr.N + p.BN - 1) / p.BN);
+  const double kt = (double)((pr.K * (pr.in_fp8 ? 1 : 2) + 127) / 128);  // K tiles of 128 bytes
+  const double cols = (double)p.BN / pr.products;                        // of each B
+  const double pieces = cols * pr.elem > 128 ? cols * pr.elem / 128 : 1.0;
+  const double lines = pr.products * (pr.transB ? cols : 128.0 / pr.elem * pieces) + p.BM;
+  return 0.9 * tiles / 256.0 * kt * (0.00141 * lines + 0.0401 * p.BN / 8.0);
+}
 }  // namespace
 
 int policy_select(const Problem& pr, int cu_count, int64_t ws_floats, int* splits, double* cost) {
@@ -144,7 +162,9 @@ int policy_select(const Problem& pr, int cu_count, int64_t ws_floats, int* split
       tiles = t * (t + 1) / 2;
     }
     const double slots = (double)cu_count * occ;
-    for (int sp = 1; sp <= 16; sp *= 2) {
+    constexpr int ways[] = {1, 2, 4, 8, 16, 3, 6, 12};
+    for (int w = 0; w < (pr.products ? 8 : 5); ++w) {
+      const int sp = ways[w];
       if (!split_allowed(p, pr, sp, ws_floats)) continue;
       const double wgs = tiles * sp;
       const double k_eff = (double)split_kt(p, pr.K, sp) * p.BK;
@@ -163,6 +183,11 @@ int policy_select(const Problem& pr, int cu_count, int64_t ws_floats, int* split
       // choice is between tiles that write C once, it decides (512 x 5120 x 5120: 256 x 128
       // tiles split in two 52 us, 128 x 128 unsplit 39)
       if (sp > 1 && pr.ep) t += tiles * sp * p.BM * p.BN * 8.0 / 4.0e6 * kUnitsPerUs;
+      if (pr.products) {
+        const double f = fetch_us(p, pr) * kUnitsPerUs;
+        if (have && (t >= best_t || f >= best_t)) continue;  // (the root is not for nothing)
+        t = std::sqrt(std::sqrt(t * t * t * t + f * f * f * f));
+      }
       if (!have || t < best_t * 0.999) {
         best = i;
         best_t = t;
@@ -203,7 +228,7 @@ Cut policy_cut(const Problem& pr, int cu_count, int64_t ws_floats, double whole)
       (rows ? rest.M : rest.N) -= at;
       int sp = 1;
       double t = 0.0;
-      if (kTable[policy_select(rest, cu_count, ws_floats, &sp, &t)].pipe == 2) continue;
+      if (kTable[policy_select(rest, cu_count, ws_floats, &sp, &t)].pipe == 2 && sp == 1) continue;
       t += head + 3.0 * kUnitsPerUs;  // the second launch
       if (t < kCutGain * whole) {
         whole = t / kCutGain;

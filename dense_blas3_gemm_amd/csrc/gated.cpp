@@ -195,8 +195,13 @@ gemm_status_t run(gemm_handle_t h, GatedArgs a, float* dbias = nullptr, float* d
   // kernel has the rest
   const int64_t step = a.transB ? 8 : 16 / in_bytes(a), N1 = a.K > 0 ? a.N / step * step : 0;
   if (N1 == 0) return run_simt(v, a, dbias, dbias2);
-  // rows that 32-bit offsets into A cover, 256 at a time
-  const int64_t most = (int64_t)(2147483647.0 / ((double)a.lda * (double)in_bytes(a))) / 256 * 256 - 512;
+  // rows that 32-bit offsets into A cover, and whose partial column sums (at most one row of them
+  // to 32 rows) the workspace holds; whole tiles of them
+  int64_t most = (int64_t)(2147483647.0 / ((double)a.lda * (double)in_bytes(a))) / 256 * 256 - 512;
+  if ((dbias || dbias2) && v.ws) {
+    const int64_t fit = (int64_t)((v.ws_bytes - kPartBytes) / sizeof(float)) / (2 * N1) * 32 / 256 * 256 - 512;
+    if (fit >= 1 && fit < most) most = fit;
+  }
   const int64_t rows = most >= a.M ? a.M : most;
   if (rows < 1 || !operands_ok(part_of(a, 0, 0, rows, a.N), N1)) return run_simt(v, a, dbias, dbias2);
   for (int64_t m0 = 0; m0 < a.M; m0 += rows) {

@@ -38,7 +38,8 @@ struct GtCols {
 };
 
 // What a row brings for columns [n, n + 8): a residual (8 bf16 in lo, or fp32 in both), or G and U;
-// and the row's factor.
+// and the row's factor.  It is read once, past the caches: the gradient of 8192 x 10240 x 1024 290
+// -> 275 us, 8-bit integers with a residual at 8192 x 8192 x 1024 125 -> 111.
 struct GtRaw {
   ep_u32x4 lo, hi;
   float s;
@@ -53,15 +54,15 @@ __device__ __forceinline__ GtRaw gt_fetch8(const GatedArgs& a, int64_t m, int n,
   if (nv == 0) return r;
   if constexpr (I8) r.s = e.sa[m];
   if constexpr (OP == GT_GRAD) {
-    r.lo = *(const ep_u32x4_2*)((const uint16_t*)e.G + m * e.ldg + n);
-    r.hi = *(const ep_u32x4_2*)((const uint16_t*)e.U + m * e.ldu + n);
+    r.lo = __builtin_nontemporal_load((const ep_u32x4_2*)((const uint16_t*)e.G + m * e.ldg + n));
+    r.hi = __builtin_nontemporal_load((const ep_u32x4_2*)((const uint16_t*)e.U + m * e.ldu + n));
   } else if constexpr (OP == GT_LINEAR) {
     if (e.R && a.c_kind == C_F32) {
       const float* p = (const float*)e.R + m * e.ldr + n;
-      r.lo = *(const ep_u32x4_4*)p;
-      r.hi = *(const ep_u32x4_4*)(p + 4);
+      r.lo = __builtin_nontemporal_load((const ep_u32x4_4*)p);
+      r.hi = __builtin_nontemporal_load((const ep_u32x4_4*)(p + 4));
     } else if (e.R) {
-      r.lo = *(const ep_u32x4_2*)((const uint16_t*)e.R + m * e.ldr + n);
+      r.lo = __builtin_nontemporal_load((const ep_u32x4_2*)((const uint16_t*)e.R + m * e.ldr + n));
     }
   }
   return r;

@@ -371,9 +371,10 @@ hipError_t launch_rows(const GemmEpArgs& a, hipStream_t s) {
 // A workgroup's wave takes every fourth of the K tiles (128 bytes of K).  A K tile costs a wave what
 // its lines (128 bytes, or the piece of one that a row of B [K][N] has in these columns) and its
 // bytes take to be asked for; and all workgroups together need the CU's share of the memory's rate
-// and of its line requests.  Fitted to 9000 products of 1 to 64 rows, N and K from 256 to 20480, in
-// all kinds, layouts and the three widths: 15 % off in the mean square.  The faster of this formula's
-// best width and the tiles by their model was 3 % slower than the fastest of the four in the mean.
+// and of its line requests, whole workgroups to a CU (1 x 10944 x 4096, both B [N][K]: 33 us at 16
+// columns, 684 workgroups, 37.5 at 32, 342 of them, and 34 at 64).  Fitted to 9000 products of 1 to 64
+// rows, N and K from 256 to 20480, in all kinds, layouts and the three widths: 15 % off in the mean
+// square, its width 1.5 % behind the best of them in the mean.
 double few_rows_us(int op, int in_kind, int transB, int64_t M, int64_t N, int64_t K, int* cols) {
   const int bm = few_bm(M), nb = op == GT_GATED ? 2 : 1, es = in_kind == GT_BF16 ? 2 : 1;
   const double its = (double)((K * es + 127) / 128) / 4.0;
@@ -381,12 +382,15 @@ double few_rows_us(int op, int in_kind, int transB, int64_t M, int64_t N, int64_
   *cols = 0;
   for (int sub : kFewCols) {
     if (!few_fits(bm, sub)) continue;
-    const double groups = (double)((N + sub - 1) / sub) / 256.0;
+    const int64_t wgs = (N + sub - 1) / sub;
+    const double whole = 0.85 * (double)((wgs + 255) / 256), share = (double)wgs / 256.0;
+    const double groups = wgs >= 256 && whole > share ? whole : share;
     const double lines = nb * (transB ? sub : 128 / es) + bm, kb = nb * sub / 8.0;
-    double wave = 0.00435 * lines + 0.0222 * kb;
+    double wave = 0.00437 * lines + 0.0230 * kb;
     if (in_kind == GT_E4M3 && transB) wave *= 1.39;  // (the widening, where the lines do not hide it)
-    const double all = 4.0 * (0.00141 * lines + 0.0401 * kb) * groups;
-    const double us = 2.69 + 0.777 * bm * sub * nb / 1024.0 + its * std::sqrt(std::sqrt(wave * wave * wave * wave + all * all * all * all));
+    const double all = 4.0 * (0.00127 * lines + 0.0362 * kb) * groups;
+    const double us = 2.70 + 0.768 * bm * sub * nb / 1024.0 +
+                      its * std::sqrt(std::sqrt(wave * wave * wave * wave + all * all * all * all));
     if (*cols == 0 || us < best) {
       best = us;
       *cols = sub;

@@ -13,6 +13,9 @@ using namespace dbgemm;
 
 namespace {
 
+// What an epilogue reads past the caches (GatedEp::past): where it would fill half of them.
+constexpr double kPastBytes = (double)(128 << 20);
+
 // Longest sum of products of two 8-bit integers (at most 2^14 each) that 32 bits hold.
 constexpr int64_t kMaxK8 = 131071;
 
@@ -191,6 +194,7 @@ gemm_status_t run(gemm_handle_t h, GatedArgs a, float* dbias = nullptr, float* d
     return status(launch_colsum(nullptr, 0, 2 * whole8(a.N), a.N, dbias, dbias2, 0, v.stream));
   }
   if (a.alpha == 0.f) a.K = 0;
+  a.ep.past = (double)a.M * a.N * (a.op == GT_GRAD ? 4 : a.ep.R ? (double)c_bytes(a) : 0) >= kPastBytes;
   // the columns of the MFMA kernels: whole eights, of [K][N] operands whole 16 bytes; the generic
   // kernel has the rest
   const int64_t step = a.transB ? 8 : 16 / in_bytes(a), N1 = a.K > 0 ? a.N / step * step : 0;

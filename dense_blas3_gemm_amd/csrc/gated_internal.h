@@ -36,6 +36,11 @@ struct GatedEp {
   int64_t ldd2;
   void* H;  // bf16, or null
   int64_t ldh;
+  // What the epilogue reads, the residual or G and U, does not fit the caches (256 MB): the 256 x 256
+  // tiles read it past them.  The gradient of 8192 x 10240 x 1024 290 -> 275 us, 8-bit integers with
+  // a residual at 8192 x 8192 x 1024 125 -> 111.  A smaller one may still be there from whoever wrote
+  // it (1078 x 7888 x 2240 with an fp32 residual, 34 MB, 39 us, past the caches 52).
+  int past;
   float* colsum;  // fp32 partial sums, [part][2][whole8(N)], or null
   float* sum1;    // the kernels of a few rows: the sums themselves, each or null
   float* sum2;

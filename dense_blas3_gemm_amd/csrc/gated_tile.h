@@ -38,14 +38,21 @@ struct GtCols {
 };
 
 // What a row brings for columns [n, n + 8): a residual (8 bf16 in lo, or fp32 in both), or G and U;
-// and the row's factor.  It is read once, past the caches: the gradient of 8192 x 10240 x 1024 290
-// -> 275 us, 8-bit integers with a residual at 8192 x 8192 x 1024 125 -> 111.
+// and the row's factor.  NT: past the caches, for what does not fit them anyway (GatedEp::past).
 struct GtRaw {
   ep_u32x4 lo, hi;
   float s;
 };
 
-template <bool I8, int OP>
+template <bool NT, class V>
+__device__ __forceinline__ ep_u32x4 gt_load(const V* p) {
+  if constexpr (NT)
+    return __builtin_nontemporal_load(p);
+  else
+    return *p;
+}
+
+template <bool NT, bool I8, int OP>
 __device__ __forceinline__ GtRaw gt_fetch8(const GatedArgs& a, int64_t m, int n, int nv) {
   const GatedEp& e = a.ep;
   GtRaw r;
@@ -54,15 +61,15 @@ __device__ __forceinline__ GtRaw gt_fetch8(const GatedArgs& a, int64_t m, int n,
   if (nv == 0) return r;
   if constexpr (I8) r.s = e.sa[m];
   if constexpr (OP == GT_GRAD) {
-    r.lo = __builtin_nontemporal_load((const ep_u32x4_2*)((const uint16_t*)e.G + m * e.ldg + n));
-    r.hi = __builtin_nontemporal_load((const ep_u32x4_2*)((const uint16_t*)e.U + m * e.ldu + n));
+    r.lo = gt_load<NT>((const ep_u32x4_2*)((const uint16_t*)e.G + m * e.ldg + n));
+    r.hi = gt_load<NT>((const ep_u32x4_2*)((const uint16_t*)e.U + m * e.ldu + n));
   } else if constexpr (OP == GT_LINEAR) {
     if (e.R && a.c_kind == C_F32) {
       const float* p = (const float*)e.R + m * e.ldr + n;
-      r.lo = __builtin_nontemporal_load((const ep_u32x4_4*)p);
-      r.hi = __builtin_nontemporal_load((const ep_u32x4_4*)(p + 4));
+      r.lo = gt_load<NT>((const ep_u32x4_4*)p);
+      r.hi = gt_load<NT>((const ep_u32x4_4*)(p + 4));
     } else if (e.R) {
-      r.lo = __builtin_nontemporal_load((const ep_u32x4_2*)((const uint16_t*)e.R + m * e.ldr + n));
+      r.lo = gt_load<NT>((const ep_u32x4_2*)((const uint16_t*)e.R + m * e.ldr + n));
     }
   }
   return r;
@@ -170,8 +177,9 @@ constexpr int gt_pass_rows(int step) {
 // acc: the 16x16 fragments of this wave, whose results start at row m0, column n0 (of both
 // products).  lds0: LDS_BYTES of LDS, free once every wave has passed the barrier here.  The
 // 16-byte chunks of an LDS row are XOR-swizzled by the row.  What the rows bring from memory is
-// asked for ahead, up to BATCH steps of rows at a time.
-template <class C, int OP, int LDS_BYTES, bool NT>
+// asked for ahead, up to BATCH steps of rows at a time.  NT: the outputs go past the caches; NTL: so do
+// the rows that are read.
+template <class C, int OP, int LDS_BYTES, bool NT, bool NTL>
 __device__ __forceinline__ void gt_tile(const GatedArgs& a, const typename AccOf<C::MT>::T (&acc)[C::FM][C::FN], int m0,
                                         int n0, int part, int wave, int lane, uint32_t lds0) {
   static_assert(C::MT == 16 && C::ACC == 4 && C::DUAL == (OP == GT_GATED), "16x16 fragments");
@@ -194,7 +202,7 @@ __device__ __forceinline__ void gt_tile(const GatedArgs& a, const typename AccOf
     GtRaw raw[BATCH];
     auto fetch = [&](int step) EP_INLINE {
       const int m = m0 + row + step * RPS;
-      return gt_fetch8<C::I8, OP>(a, m, n, step < ALL && m < a.M ? nvc : 0);
+      return gt_fetch8<NTL, C::I8, OP>(a, m, n, step < ALL && m < a.M ? nvc : 0);
     };
 #pragma unroll
     for (int s = 0; s < BATCH; ++s) raw[s] = fetch(s);
@@ -273,7 +281,7 @@ __device__ __forceinline__ void gt_strip(const GatedArgs& a, int tile, int i, in
 #pragma unroll
     for (int s = 0; s < STEPS; ++s) {
       const int m = row_of(s * RPS + row);
-      raw[s] = gt_fetch8<C::I8, OP>(a, m, n, m < a.M ? nvc : 0);
+      raw[s] = gt_fetch8<false, C::I8, OP>(a, m, n, m < a.M ? nvc : 0);
     }
     if (row_of(wm * 16) < a.M) {  // (this wave's rows past M hold no sums)
       f32x4 v[C::FN];

@@ -439,8 +439,8 @@ __global__ __launch_bounds__(C::THREADS) void gemm_dma_kernel(KernelArgs a) {
   ep_tile<C, C::STAGE_BYTES, false>(a, acc, m0 + xa0, n0 + xb0, tm * C::WM + wm, wave, lane,
                                     (uint32_t)(uintptr_t)slot(std::integral_constant<int, 0>{}));
 #elif defined(DBGEMM_GATED)
-  gt_tile<C, OP, C::STAGE_BYTES, false>(a, acc, m0 + xa0, n0 + xb0, tm * C::WM + wm, wave, lane,
-                                        (uint32_t)(uintptr_t)slot(std::integral_constant<int, 0>{}));
+  gt_tile<C, OP, C::STAGE_BYTES, false, false>(a, acc, m0 + xa0, n0 + xb0, tm * C::WM + wm, wave, lane,
+                                               (uint32_t)(uintptr_t)slot(std::integral_constant<int, 0>{}));
 #else
   store_tile<C>(a, acc, m0 + xa0, n0 + xb0, lane);
 #endif

@@ -337,8 +337,9 @@ __device__ __forceinline__ void pp_store_tile_lds(const GemmArgs& a, const typen
 // its K tiles) one after the other, each through the same two-group pipeline.
 // OP: what a gated operator's kernel does with its sums.  SPLIT: those kernels' form for a product
 // whose K is split (GemmArgs::splits), which leaves its part of the sums in the workspace (one kernel
-// for both spilled registers in the epilogue: 935 us, so 1010 at 4096 x 13696 x 5120).
-template <class C, bool SK, int OP = 0, bool SPLIT = false>
+// for both spilled registers in the epilogue: 935 us, so 1010 at 4096 x 13696 x 5120).  NTL: the rows
+// that the epilogue reads come past the caches.
+template <class C, bool SK, int OP = 0, bool SPLIT = false, bool NTL = false>
 __global__ __launch_bounds__(512) void gemm_pp_kernel(KernelArgs a) {
   using P = PingPong<C>;
   constexpr int S = P::S;
@@ -868,7 +869,7 @@ __global__ __launch_bounds__(512) void gemm_pp_kernel(KernelArgs a) {
         pp_store_partial<C>(a.ws + ((size_t)(tm * a.tiles_n + tn) * a.splits + split) * (C::BM * C::BN), acc,
                             (uint32_t)lane_t * 16u);
       else
-        gt_tile<C, OP, P::LDS_BYTES, true>(a, acc, m0 + xa0, n0 + xb0, tm * C::WM + wm, wave, lane, lds0);
+        gt_tile<C, OP, P::LDS_BYTES, true, NTL>(a, acc, m0 + xa0, n0 + xb0, tm * C::WM + wm, wave, lane, lds0);
 #else
       pp_store_tile_lds<C>(a, acc, m0, n0, grp, xb0, lane, t, lds0);
 #endif
@@ -889,7 +890,9 @@ __global__ __launch_bounds__(C::THREADS) void pp_split_reduce_kernel(GatedArgs a
 template <class C, int OP>
 hipError_t launch_pp(const KernelArgs& a, hipStream_t s) {
   if (a.splits < 1 || (a.splits > 1 && !a.ws) || a.sk_tiles > 0) return hipErrorInvalidConfiguration;
-  if (a.splits == 1) {
+  if (a.splits == 1 && OP != GT_GATED && a.ep.past) {
+    hipLaunchKernelGGL((gemm_pp_kernel<C, false, OP, false, OP != GT_GATED>), dim3(grid_tiles(a)), dim3(C::THREADS), 0, s, a);
+  } else if (a.splits == 1) {
     hipLaunchKernelGGL((gemm_pp_kernel<C, false, OP>), dim3(grid_tiles(a)), dim3(C::THREADS), 0, s, a);
   } else {
     hipLaunchKernelGGL((gemm_pp_kernel<C, false, OP, true>), dim3(grid_tiles(a)), dim3(C::THREADS), 0, s, a);

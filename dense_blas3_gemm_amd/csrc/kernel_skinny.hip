@@ -91,7 +91,7 @@ __global__ __launch_bounds__(WAVES * 64) void gemm_skinny_kernel(KernelArgs a) {
   const int nv = t < OUT && om < a.M && on < a.N ? 8 : 0;
 #ifdef DBGEMM_GATED
   const GtCols<C::I8, OP> cols(a, on, nv);
-  const GtRaw raw = gt_fetch8<C::I8, OP>(a, om, on, nv);
+  const GtRaw raw = gt_fetch8<false, C::I8, OP>(a, om, on, nv);
 #else
   static_assert(LPR % 4 == 0, "whole blocks of 32 columns");
   float bias[8];

@@ -880,8 +880,9 @@ __global__ __launch_bounds__(512) void gemm_pp_kernel(KernelArgs a) {
 
 #if defined(DBGEMM_GATED)
 // A split product's second launch: workgroup (tile, i) adds the partials of fragment row i of every
-// row of waves and finishes them.  (The partials of 361 x 7360 x 19232 are 58 tiles of 256 x 256 in
-// four parts: one round of the CUs where the whole tiles fill a quarter of one.)
+// row of waves and finishes them.  361 x 7360 x 19232 are 58 tiles in four parts, one
+// round of the CUs where the whole tiles fill a quarter of one: 8-bit integers, B [K][N], 93 us, whole
+// 260, 256 x 128 tiles in two parts 107; the bf16 gradient 146, 420 and 176.
 template <class C, int OP>
 __global__ __launch_bounds__(C::THREADS) void pp_split_reduce_kernel(GatedArgs a) {
   gt_strip<C, OP>(a, blockIdx.x / C::FM, blockIdx.x % C::FM, threadIdx.x);

@@ -130,8 +130,8 @@ constexpr double kUnitsPerUs = 2.0e6;
 // What the operands of a gated operator's grid take to be fetched, in us on 256 CUs: a CU asks for
 // so many lines (128 bytes, or the piece of one that a tile takes of a row of B [K][N]) and moves so
 // many bytes (the rates of the few-row kernel's model, less a tenth).  It decides where there are
-// few rows of A, or few columns of 1-byte elements to a tile: 19 x 9824 x 8432 of 8-bit integers,
-// both B [K][N], 80 us on 64 x 64 tiles, 32 bytes of a row each, and 42 on 128 x 128.  Over 1500 drawn
+// few rows of A, or few columns of 1-byte elements to a tile: 37 x 10944 x 6368 of 8-bit integers,
+// both B [K][N], 62 us on 64 x 64 tiles, 32 bytes of a row each, and 42 on 128 x 128.  Over 1500 drawn
 // products the choice was 4.4 % behind the fastest for up to 64 rows and 2.3 % for more; with this
 // 3.0 and 1.7.
 double fetch_us(const Policy& p, const Problem& pr) {

@@ -116,3 +116,63 @@ def test_gradients_of_many_megabytes(gpu):
     gpu.run_dgated(A, B, g, u, g, u, transB=1, act="relu")
     torch.cuda.synchronize()
     assert torch.equal(g, x) and torch.equal(u, y)
+
+
+def test_two_handles_on_two_streams():
+    """Split products and column sums side by side: each handle has its own workspace."""
+    import torch
+    import dense_blas3_gemm_amd as d
+    hs = [d.Gemm(0), d.Gemm(0)]
+    try:
+        M, N, K = 255, 1040, 8208
+        A, B = [whole(M, K, 2, i) for i in (0, 1)], [whole(N, K, 2, i) for i in (2, 3)]
+        g, u = [whole(M, N, 2, i) for i in (4, 5)], [whole(M, N, 2, i) for i in (6, 7)]
+        out = [[torch.empty(M, N, device="cuda") for _ in range(3)] + [torch.empty(N, device="cuda") for _ in range(2)]
+               for _ in range(2)]
+        streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+        torch.cuda.synchronize()
+        for _ in range(20):
+            for h, s, a, b, gg, uu, o in zip(hs, streams, A, B, g, u, out):
+                with torch.cuda.stream(s):
+                    h.run_gated(a, b, b, o[0], transB=1, act="relu")
+                    h.run_dgated(a, b, gg, uu, o[1], o[2], transB=1, act="relu", dbias_g=o[3], dbias_u=o[4])
+        torch.cuda.synchronize()
+        for a, b, gg, uu, o in zip(A, B, g, u, out):
+            p, on = product(a, b, 1), (gg > 0).float()
+            x, y = p * uu.float() * on, p * gg.float() * on
+            assert torch.equal(o[0], p.clamp(min=0) * p) and torch.equal(o[1], x) and torch.equal(o[2], y)
+            assert torch.equal(o[3], x.sum(0)) and torch.equal(o[4], y.sum(0))
+    finally:
+        for h in hs:
+            h.close()
+
+
+def test_captured_odd_and_split(gpu):
+    """Split tiles, left columns and column sums replayed between eager calls of the same handle."""
+    import torch
+    M, N, K = 255, 1045, 8208
+    A, B = whole(M, K, 2, 0), whole(N, K, 2, 1)
+    g, u = whole(M, N, 2, 2), whole(M, N, 2, 3)
+    mk = lambda: [torch.empty(M, N, device="cuda") for _ in range(3)] + [torch.empty(N, device="cuda") for _ in range(2)]  # noqa: E731
+    out, want = mk(), mk()
+
+    def run(o):
+        gpu.run_gated(A, B, B, o[0], transB=1, act="relu")
+        gpu.run_dgated(A, B, g, u, o[1], o[2], transB=1, act="relu", dbias_g=o[3], dbias_u=o[4])
+    run(want)
+    torch.cuda.synchronize()
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        run(out)
+    for i in range(4):
+        A.copy_(whole(M, K, 2, 10 + i))
+        for t in out:
+            t.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        run(want)
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(out, want)), i
+    p = product(A, B, 1)
+    assert torch.equal(out[0], p.clamp(min=0) * p)

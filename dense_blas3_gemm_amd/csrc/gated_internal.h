@@ -8,7 +8,8 @@
 namespace dbgemm {
 
 // What a product's results go through, element (m, n); w is alpha * (A op(B)), or for 8-bit
-// integers (the exact sum * sa[m]) * sb[n], w2 the same of the second B:
+// integers (the exact sum * sa[m]) * sb[n] (or the factors the other way round, kFarFactor), w2 the
+// same of the second B:
 //   GT_LINEAR: C <- act(w + bias) + beta * R
 //   GT_GATED:  g = w + bias, u = w2 + bias2; G <- g, U <- u (where kept); C <- act(g) * u
 //   GT_GRAD:   C <- w * U * act'(G); D2 <- w * act(G); H <- act(G) * U; the column sums of the
@@ -45,6 +46,13 @@ struct GatedEp {
   float* sum1;    // the kernels of a few rows: the sums themselves, each or null
   float* sum2;
 };
+
+// Past this magnitude of a row's factor its columns' factors come first: sum * sa[m] could leave fp32's
+// range (a row that holds bf16's lowest value has a factor of 2.7e36) where sum * sa[m] * sb[n] does
+// not.  A sum is a whole number of at most 2^31, so neither order loses anything else: up to here its
+// product with sa[m] is at most 2^95; past here one with sb[n] overflows from |sb[n]| = 2^97 on only,
+// where the result does too; and times a subnormal factor it is a whole number of 2^-149, exact.
+constexpr float kFarFactor = 0x1p64f;
 
 // (B2 and ldb2 of GemmArgs hold the second B.)
 struct GatedArgs : GemmArgs {

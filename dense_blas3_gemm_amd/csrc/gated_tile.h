@@ -90,6 +90,18 @@ __device__ __forceinline__ void gt_bf16(const ep_u32x4& r, float (&v)[8]) {
   }
 }
 
+// Eight sums of a row times its factor s and their columns' c (kFarFactor).
+__device__ __forceinline__ void gt_scale8(float (&w)[8], float s, const float (&c)[8]) {
+  const bool far = __builtin_fabsf(s) > kFarFactor;
+  if (__any(far)) {  // (a branch of the whole wave, and next to never taken)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = w[i] * (far ? c[i] : s) * (far ? s : c[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = w[i] * s * c[i];
+  }
+}
+
 // Eight columns of row m: w, w2 the products (w2 of the second B), alpha applied, or the whole
 // numbers as floats.  A gradient's unrounded results are added to cs and cs2.
 template <bool NT, bool I8, int OP, int ACT>
@@ -113,14 +125,14 @@ __device__ __forceinline__ void gt_finish8(const GatedArgs& a, float (&w)[8], fl
     ep_store8<NT, EP_NONE>(e.D2, m * e.ldd2 + n, f32, 8, du);
     if (e.H) ep_store8<NT, EP_NONE>((uint16_t*)e.H + m * e.ldh + n, 8, h);
   } else {
+    if constexpr (I8) {
+      gt_scale8(w, r.s, c.s);
+      if constexpr (OP == GT_GATED) gt_scale8(w2, r.s, c.s2);
+    }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      if constexpr (I8) w[i] = w[i] * r.s * c.s[i];
       w[i] += c.b[i];
-      if constexpr (OP == GT_GATED) {
-        if constexpr (I8) w2[i] = w2[i] * r.s * c.s2[i];
-        w2[i] += c.b2[i];
-      }
+      if constexpr (OP == GT_GATED) w2[i] += c.b2[i];
     }
     if constexpr (OP == GT_GATED) {
       if (e.G) ep_store8<NT, EP_NONE>((uint16_t*)e.G + m * e.ldg + n, 8, w);

@@ -40,16 +40,25 @@ __device__ __forceinline__ void gs_store(void* p, int64_t i, int f32, float v) {
     ((uint16_t*)p)[i] = ep_f32bf(v);
 }
 
+// A sum times alpha, or times the factors of its row and its column (kFarFactor).
+template <int IN>
+__device__ __forceinline__ float gs_scale(const GatedArgs& a, float w, int64_t m, const float* sb, int64_t n) {
+  if constexpr (IN != GT_I8) {
+    return w * a.alpha;
+  } else {
+    const float s = a.ep.sa[m], c = sb[n];
+    const bool far = __builtin_fabsf(s) > kFarFactor;
+    return w * (far ? c : s) * (far ? s : c);
+  }
+}
+
 // Element (m, n) from its sums (w2 of the second B); a gradient's results are added to cs.
 template <int IN, int OP, int ACT>
 __device__ __forceinline__ void gs_finish(const GatedArgs& a, int64_t m, int64_t n, float w, float w2, float& cs,
                                           float& cs2) {
-  constexpr bool INT = IN == GT_I8;
   const GatedEp& e = a.ep;
   const bool f32 = a.c_kind == C_F32;
-  const float sa = INT ? e.sa[m] : a.alpha;
-  w *= sa;
-  if constexpr (INT) w *= e.sb[n];
+  w = gs_scale<IN>(a, w, m, e.sb, n);
   if constexpr (OP == GT_GRAD) {
     const float g = ep_bf16f(((const uint16_t*)e.G)[m * e.ldg + n]);
     const float u = ep_bf16f(((const uint16_t*)e.U)[m * e.ldu + n]);
@@ -63,8 +72,7 @@ __device__ __forceinline__ void gs_finish(const GatedArgs& a, int64_t m, int64_t
     if (e.bias) w += gs_value(e.bias, n, e.bias_f32);
     float c = ep_act<ACT>(w);
     if constexpr (OP == GT_GATED) {
-      w2 *= sa;
-      if constexpr (INT) w2 *= e.sb2[n];
+      w2 = gs_scale<IN>(a, w2, m, e.sb2, n);
       if (e.bias2) w2 += gs_value(e.bias2, n, e.bias_f32);
       if (e.G) gs_store(e.G, m * e.ldg + n, 0, w);
       if (e.U) gs_store(e.U, m * e.ldu + n, 0, w2);

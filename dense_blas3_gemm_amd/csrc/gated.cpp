@@ -16,21 +16,12 @@ namespace {
 // What an epilogue reads past the caches (GatedEp::past): where it would fill half of them.
 constexpr double kPastBytes = (double)(128 << 20);
 
+// Columns that the generic kernels take in a launch: a launch ends at 2^32 threads, the one for few
+// elements (8 columns to 256 threads) at 2^27 columns.
+constexpr int64_t kSimtCols = (int64_t)1 << 26;
+
 // Longest sum of products of two 8-bit integers (at most 2^14 each) that 32 bits hold.
 constexpr int64_t kMaxK8 = 131071;
-
-// The generic kernel over all of a; dbias: fp32 column sums, the second set from dbias2.
-gemm_status_t run_simt(const HandleView& v, GatedArgs a, float* dbias, float* dbias2) {
-  const bool sums = dbias || dbias2;
-  const int mp = sums ? max_parts(v, 2 * whole8(a.N)) : 1;
-  if (mp < 1) return GEMM_STATUS_NOT_SUPPORTED;
-  a.ep.colsum = sums ? (float*)v.ws : nullptr;
-  int parts = 0;
-  hipError_t e = launch_gated_simt(a, mp, &parts, v.stream);
-  if (e == hipSuccess && sums)
-    e = launch_colsum((const float*)v.ws, parts, 2 * whole8(a.N), a.N, dbias, dbias2, 0, v.stream);
-  return status(e);
-}
 
 // bytes per element of the operands, of C
 int64_t in_bytes(const GatedArgs& a) { return a.in_kind == GT_BF16 ? 2 : 1; }
@@ -60,6 +51,25 @@ GatedArgs part_of(const GatedArgs& a, int64_t m0, int64_t n0, int64_t M, int64_t
   at(r.ep.D2, (m0 * a.ep.ldd2 + n0) * ce);
   at(r.ep.H, (m0 * a.ep.ldh + n0) * 2);
   return r;
+}
+
+// The generic kernel over all of a; dbias: fp32 column sums, the second set from dbias2.
+gemm_status_t run_simt(const HandleView& v, const GatedArgs& all, float* dbias, float* dbias2) {
+  const bool sums = dbias || dbias2;
+  const int mp = sums ? max_parts(v, 2 * whole8(all.N)) : 1;
+  if (mp < 1) return GEMM_STATUS_NOT_SUPPORTED;
+  for (int64_t n0 = 0; n0 < all.N; n0 += kSimtCols) {
+    const int64_t N = all.N - n0 < kSimtCols ? all.N - n0 : kSimtCols;
+    GatedArgs a = part_of(all, 0, n0, all.M, N);
+    a.ep.colsum = sums ? (float*)v.ws : nullptr;
+    int parts = 0;
+    hipError_t e = launch_gated_simt(a, mp, &parts, v.stream);
+    if (e == hipSuccess && sums)
+      e = launch_colsum((const float*)v.ws, parts, 2 * whole8(N), N, dbias ? dbias + n0 : nullptr,
+                        dbias2 ? dbias2 + n0 : nullptr, 0, v.stream);
+    if (e != hipSuccess) return status(e);
+  }
+  return GEMM_STATUS_SUCCESS;
 }
 
 // One launch on policy p with sp splits; partial column sums into ep.colsum, *parts rows of them.

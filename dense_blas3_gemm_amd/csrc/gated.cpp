@@ -19,6 +19,8 @@ constexpr double kPastBytes = (double)(128 << 20);
 // Columns that the generic kernels take in a launch: a launch ends at 2^32 threads, the one for few
 // elements (8 columns to 256 threads) at 2^27 columns.
 constexpr int64_t kSimtCols = (int64_t)1 << 26;
+// and where a partial row of column sums of all of them does not fit the workspace (from 2^23 on): two do
+constexpr int64_t kSimtSumCols = (int64_t)1 << 22;
 
 // Longest sum of products of two 8-bit integers (at most 2^14 each) that 32 bits hold.
 constexpr int64_t kMaxK8 = 131071;
@@ -56,10 +58,12 @@ GatedArgs part_of(const GatedArgs& a, int64_t m0, int64_t n0, int64_t M, int64_t
 // The generic kernel over all of a; dbias: fp32 column sums, the second set from dbias2.
 gemm_status_t run_simt(const HandleView& v, const GatedArgs& all, float* dbias, float* dbias2) {
   const bool sums = dbias || dbias2;
-  const int mp = sums ? max_parts(v, 2 * whole8(all.N)) : 1;
+  int64_t most = all.N < kSimtCols ? all.N : kSimtCols;
+  if (sums && max_parts(v, 2 * whole8(most)) < 1 && most > kSimtSumCols) most = kSimtSumCols;
+  const int mp = sums ? max_parts(v, 2 * whole8(most)) : 1;
   if (mp < 1) return GEMM_STATUS_NOT_SUPPORTED;
-  for (int64_t n0 = 0; n0 < all.N; n0 += kSimtCols) {
-    const int64_t N = all.N - n0 < kSimtCols ? all.N - n0 : kSimtCols;
+  for (int64_t n0 = 0; n0 < all.N; n0 += most) {
+    const int64_t N = all.N - n0 < most ? all.N - n0 : most;
     GatedArgs a = part_of(all, 0, n0, all.M, N);
     a.ep.colsum = sums ? (float*)v.ws : nullptr;
     int parts = 0;

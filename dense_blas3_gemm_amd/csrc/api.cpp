@@ -18,9 +18,6 @@ namespace {
 
 constexpr const char* kVersion = "dbgemm 0.1.0 policy-table 1";
 
-// Device workspace, allocated once per handle at creation: split-K's fp32 partial tiles,
-// and the BLAS3 calls' expanded, packed or transposed operands.
-constexpr size_t kWorkspaceBytes = (size_t)256 << 20;
 // Split-K partials use at most this much of it: the wave-time model's split costs were fitted
 // with this bound (a larger one lets it split grids whose reduction costs more than it saves).
 constexpr size_t kSplitBytes = (size_t)64 << 20;

@@ -13,6 +13,10 @@ namespace dbgemm {
 constexpr int kTrsmNB = 128;
 constexpr int kTrsmLeaf = 2 * kTrsmNB;
 
+// Device workspace, allocated once per handle at creation: split-K's fp32 partial tiles,
+// and the BLAS3 calls' expanded, packed or transposed operands.
+constexpr size_t kWorkspaceBytes = (size_t)256 << 20;
+
 // What the BLAS3 code needs of a live handle.
 struct HandleView {
   int device;

@@ -4,6 +4,8 @@
 
 #include <cmath>
 #include <cstdint>
+#include <cstdio>
+#include <string>
 #include <type_traits>
 
 #include "gated_internal.h"
@@ -55,11 +57,16 @@ GatedArgs part_of(const GatedArgs& a, int64_t m0, int64_t n0, int64_t M, int64_t
   return r;
 }
 
-// The generic kernel over all of a; dbias: fp32 column sums, the second set from dbias2.
+// The columns of a launch of the generic kernels over all of a.
+int64_t simt_cols(const HandleView& v, const GatedArgs& a, bool sums) {
+  const int64_t most = a.N < kSimtCols ? a.N : kSimtCols;
+  return sums && max_parts(v, 2 * whole8(most)) < 1 && most > kSimtSumCols ? kSimtSumCols : most;
+}
+
+// The generic kernels over all of a; dbias: fp32 column sums, the second set from dbias2.
 gemm_status_t run_simt(const HandleView& v, const GatedArgs& all, float* dbias, float* dbias2) {
   const bool sums = dbias || dbias2;
-  int64_t most = all.N < kSimtCols ? all.N : kSimtCols;
-  if (sums && max_parts(v, 2 * whole8(most)) < 1 && most > kSimtSumCols) most = kSimtSumCols;
+  const int64_t most = simt_cols(v, all, sums);
   const int mp = sums ? max_parts(v, 2 * whole8(most)) : 1;
   if (mp < 1) return GEMM_STATUS_NOT_SUPPORTED;
   for (int64_t n0 = 0; n0 < all.N; n0 += most) {
@@ -136,13 +143,21 @@ double tiles_us(int in_kind, double cost, bool sums) {
 // (no tile's time is less: the search among them is a microsecond of the host's)
 constexpr double kLeastTilesUs = 5.0;
 
-// a's columns, whole eights of them, on the MFMA kernels; false (nothing launched) where they, or
-// the workspace, cannot.  accumulate: the sums are added to dbias and dbias2.
-bool run_fused(const HandleView& v, GatedArgs a, float* dbias, float* dbias2, int accumulate, hipError_t* e) {
-  const bool sums = dbias || dbias2;
+// How a product of whole eights of columns is run on the MFMA kernels.
+struct Choice {
+  bool ok = false;   // not: they, or the workspace, cannot
+  int few_cols = 0;  // the few-row kernel at this width, or
+  int idx = 0, sp = 1;
+  Cut cut;  // two launches, the second one's
+  int idx2 = 0, sp2 = 1;
+  GatedArgs a1, a2;
+  int64_t floats1 = 0, floats2 = 0;  // of partial column sums
+};
+
+// accumulate: the sums are added to those of other rows.
+Choice choose(const HandleView& v, const GatedArgs& a, bool sums, bool accumulate) {
+  Choice c;
   const int nb = a.op == GT_GATED ? 2 : 1;
-  Problem pr = problem_of(a);
-  int sp = 1, idx2 = 0, sp2 = 1;
   double cost = 0.0;
   const int64_t split_floats = v.ws ? (int64_t)(kPartBytes / sizeof(float)) : 0;
   // a few rows: their own kernel where its time by its model is less than any tile's, or than the
@@ -151,51 +166,87 @@ bool run_fused(const HandleView& v, GatedArgs a, float* dbias, float* dbias2, in
   const double few = !accumulate && a.M <= kFewRows
                          ? few_rows_us(a.op, a.in_kind, a.transB, a.M, a.N, a.K, &few_cols)
                          : 0.0;
-  auto run_few = [&] {
-    a.ep.sum1 = dbias;
-    a.ep.sum2 = dbias2;
-    *e = launch_gated_skinny(a, few_cols, v.stream);
-    return true;
-  };
-  if (few_cols && few < kLeastTilesUs) return run_few();
-  int idx = policy_select(pr, v.cu_count, split_floats, &sp, &cost);
-  if (policy_at(idx).kind != KIND_MFMA) return false;
-  if (few_cols && few < tiles_us(a.in_kind, cost, sums)) return run_few();
-  const Cut cut = policy_cut(pr, v.cu_count, split_floats, cost);
-  GatedArgs a1 = a, a2 = a;
-  const int64_t at = cut.p < 0 || cut.by_rows ? cut.at : cut.at / nb;
-  if (cut.p >= 0) {
-    a1 = cut.by_rows ? part_of(a, 0, 0, at, a.N) : part_of(a, 0, 0, a.M, at);
-    a2 = cut.by_rows ? part_of(a, at, 0, a.M - at, a.N) : part_of(a, 0, at, a.M, a.N - at);
-    idx = cut.p;
-    sp = 1;
-    pr.M = a2.M;
-    pr.N = (int64_t)a2.N * nb;
-    idx2 = policy_select(pr, v.cu_count, split_floats, &sp2);
-    if (policy_at(idx2).kind != KIND_MFMA) return false;
+  if (few_cols && few < kLeastTilesUs) {
+    c.ok = true;
+    c.few_cols = few_cols;
+    return c;
+  }
+  Problem pr = problem_of(a);
+  c.idx = policy_select(pr, v.cu_count, split_floats, &c.sp, &cost);
+  if (policy_at(c.idx).kind != KIND_MFMA) return c;
+  if (few_cols && few < tiles_us(a.in_kind, cost, sums)) {
+    c.ok = true;
+    c.few_cols = few_cols;
+    return c;
+  }
+  c.cut = policy_cut(pr, v.cu_count, split_floats, cost);
+  c.a1 = a;
+  if (c.cut.p >= 0) {
+    const int64_t at = c.cut.at = c.cut.by_rows ? c.cut.at : c.cut.at / nb;
+    c.a1 = c.cut.by_rows ? part_of(a, 0, 0, at, a.N) : part_of(a, 0, 0, a.M, at);
+    c.a2 = c.cut.by_rows ? part_of(a, at, 0, a.M - at, a.N) : part_of(a, 0, at, a.M, a.N - at);
+    c.idx = c.cut.p;
+    c.sp = 1;
+    pr.M = c.a2.M;
+    pr.N = (int64_t)c.a2.N * nb;
+    c.idx2 = policy_select(pr, v.cu_count, split_floats, &c.sp2);
+    if (policy_at(c.idx2).kind != KIND_MFMA) return c;
   }
   if (sums) {
-    const int64_t f1 = partial_rows(policy_at(idx), a1.M, sp) * 2 * a1.N;
-    const int64_t f2 = cut.p >= 0 ? partial_rows(policy_at(idx2), a2.M, sp2) * 2 * a2.N : 0;
-    if (!v.ws || v.ws_bytes < kPartBytes + (size_t)(f1 + f2) * sizeof(float)) return false;
-    a1.ep.colsum = (float*)((char*)v.ws + kPartBytes);
-    a2.ep.colsum = a1.ep.colsum + f1;
+    c.floats1 = partial_rows(policy_at(c.idx), c.a1.M, c.sp) * 2 * c.a1.N;
+    if (c.cut.p >= 0) c.floats2 = partial_rows(policy_at(c.idx2), c.a2.M, c.sp2) * 2 * c.a2.N;
+    if (!v.ws || v.ws_bytes < kPartBytes + (size_t)(c.floats1 + c.floats2) * sizeof(float)) return c;
+  }
+  c.ok = true;
+  return c;
+}
+
+// c's launches; accumulate: the sums are added to dbias and dbias2.
+hipError_t run_choice(const HandleView& v, GatedArgs a, Choice& c, float* dbias, float* dbias2, int accumulate) {
+  if (c.few_cols) {
+    a.ep.sum1 = dbias;
+    a.ep.sum2 = dbias2;
+    return launch_gated_skinny(a, c.few_cols, v.stream);
+  }
+  const bool sums = dbias || dbias2;
+  if (sums) {
+    c.a1.ep.colsum = (float*)((char*)v.ws + kPartBytes);
+    c.a2.ep.colsum = c.a1.ep.colsum + c.floats1;
   }
   auto add_up = [&](const GatedArgs& p, int parts, int64_t n0) {
     return launch_colsum(p.ep.colsum, parts, 2 * (int64_t)p.N, p.N, dbias ? dbias + n0 : nullptr,
                          dbias2 ? dbias2 + n0 : nullptr, accumulate, v.stream);
   };
+  const bool two = c.cut.p >= 0;
   int parts = 0, parts2 = 0;
-  *e = run_tiles(v, a1, policy_at(idx), sp, &parts);
-  if (cut.p >= 0 && *e == hipSuccess) *e = run_tiles(v, a2, policy_at(idx2), sp2, &parts2);
-  if (!sums || *e != hipSuccess) return true;
-  if (cut.p >= 0 && cut.by_rows) {  // (the rows of partial sums of both follow each other)
-    *e = add_up(a1, parts + parts2, 0);
-  } else {
-    *e = add_up(a1, parts, 0);
-    if (cut.p >= 0 && *e == hipSuccess) *e = add_up(a2, parts2, at);
+  hipError_t e = run_tiles(v, c.a1, policy_at(c.idx), c.sp, &parts);
+  if (two && e == hipSuccess) e = run_tiles(v, c.a2, policy_at(c.idx2), c.sp2, &parts2);
+  if (!sums || e != hipSuccess) return e;
+  if (two && c.cut.by_rows) return add_up(c.a1, parts + parts2, 0);  // (the rows of both follow each other)
+  e = add_up(c.a1, parts, 0);
+  if (two && e == hipSuccess) e = add_up(c.a2, parts2, c.cut.at);
+  return e;
+}
+
+// The columns of the MFMA kernels, whole eights (of [K][N] operands whole 16 bytes; the generic kernels
+// have the rest), and the rows of a call on them that 32-bit offsets into A cover and whose partial column
+// sums (at most one row of them to 32 rows) the workspace holds, whole tiles of them; no columns where
+// those kernels do not take the operands.
+struct Blocks {
+  int64_t cols = 0, rows = 0;
+};
+Blocks blocks_of(const HandleView& v, const GatedArgs& a, bool sums) {
+  Blocks b;
+  const int64_t step = a.transB ? 8 : 16 / in_bytes(a), N1 = a.K > 0 ? a.N / step * step : 0;
+  if (N1 == 0) return b;
+  int64_t most = (int64_t)(2147483647.0 / ((double)a.lda * (double)in_bytes(a))) / 256 * 256 - 512;
+  if (sums && v.ws) {
+    const int64_t fit = (int64_t)((v.ws_bytes - kPartBytes) / sizeof(float)) / (2 * N1) * 32 / 256 * 256 - 512;
+    if (fit >= 1 && fit < most) most = fit;
   }
-  return true;
+  b.rows = most >= a.M ? a.M : most;
+  if (b.rows >= 1 && operands_ok(part_of(a, 0, 0, b.rows, a.N), N1)) b.cols = N1;
+  return b;
 }
 
 gemm_status_t run(gemm_handle_t h, GatedArgs a, float* dbias = nullptr, float* dbias2 = nullptr) {
@@ -203,36 +254,28 @@ gemm_status_t run(gemm_handle_t h, GatedArgs a, float* dbias = nullptr, float* d
   if (!handle_view(h, &v)) return GEMM_STATUS_NOT_INITIALIZED;
   OnDevice on(v.device);
   if (!on.ok) return GEMM_STATUS_INTERNAL;
+  const bool sums = dbias || dbias2;
   if (a.M == 0 || a.N == 0) {  // no element; the sums over no rows are zeros
-    if ((!dbias && !dbias2) || a.N == 0) return GEMM_STATUS_SUCCESS;
+    if (!sums || a.N == 0) return GEMM_STATUS_SUCCESS;
     return status(launch_colsum(nullptr, 0, 2 * whole8(a.N), a.N, dbias, dbias2, 0, v.stream));
   }
   if (a.alpha == 0.f) a.K = 0;
   a.ep.past = (double)a.M * a.N * (a.op == GT_GRAD ? 4 : a.ep.R ? (double)c_bytes(a) : 0) >= kPastBytes;
-  // the columns of the MFMA kernels: whole eights, of [K][N] operands whole 16 bytes; the generic
-  // kernel has the rest
-  const int64_t step = a.transB ? 8 : 16 / in_bytes(a), N1 = a.K > 0 ? a.N / step * step : 0;
-  if (N1 == 0) return run_simt(v, a, dbias, dbias2);
-  // rows that 32-bit offsets into A cover, and whose partial column sums (at most one row of them
-  // to 32 rows) the workspace holds; whole tiles of them
-  int64_t most = (int64_t)(2147483647.0 / ((double)a.lda * (double)in_bytes(a))) / 256 * 256 - 512;
-  if ((dbias || dbias2) && v.ws) {
-    const int64_t fit = (int64_t)((v.ws_bytes - kPartBytes) / sizeof(float)) / (2 * N1) * 32 / 256 * 256 - 512;
-    if (fit >= 1 && fit < most) most = fit;
-  }
-  const int64_t rows = most >= a.M ? a.M : most;
-  if (rows < 1 || !operands_ok(part_of(a, 0, 0, rows, a.N), N1)) return run_simt(v, a, dbias, dbias2);
-  for (int64_t m0 = 0; m0 < a.M; m0 += rows) {
-    const int64_t M = a.M - m0 < rows ? a.M - m0 : rows;
-    hipError_t e;
-    if (!run_fused(v, part_of(a, m0, 0, M, N1), dbias, dbias2, m0 > 0, &e)) {
+  const Blocks b = blocks_of(v, a, sums);
+  if (b.cols == 0) return run_simt(v, a, dbias, dbias2);
+  for (int64_t m0 = 0; m0 < a.M; m0 += b.rows) {
+    const GatedArgs part = part_of(a, m0, 0, a.M - m0 < b.rows ? a.M - m0 : b.rows, b.cols);
+    Choice c = choose(v, part, sums, m0 > 0);
+    if (!c.ok) {
       if (m0 > 0) return GEMM_STATUS_INTERNAL;
       return run_simt(v, a, dbias, dbias2);
     }
+    const hipError_t e = run_choice(v, part, c, dbias, dbias2, m0 > 0);
     if (e != hipSuccess) return status(e);
   }
-  if (N1 == a.N) return GEMM_STATUS_SUCCESS;
-  return run_simt(v, part_of(a, 0, N1, a.M, a.N - N1), dbias ? dbias + N1 : nullptr, dbias2 ? dbias2 + N1 : nullptr);
+  if (b.cols == a.N) return GEMM_STATUS_SUCCESS;
+  return run_simt(v, part_of(a, 0, b.cols, a.M, a.N - b.cols), dbias ? dbias + b.cols : nullptr,
+                  dbias2 ? dbias2 + b.cols : nullptr);
 }
 
 // Operands (the second B is checked by the same rules) and C of one call.
@@ -324,6 +367,58 @@ hipError_t launch_mfma_gated(const Policy& p, const GatedArgs& a, int* parts, hi
 }  // namespace dbgemm
 
 extern "C" {
+
+int dbgemm_gated_plan(int op, int in_kind, int transB, int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb,
+                      int64_t ldb2, int sums, int cu_count, char* text, size_t len) {
+  if (!text || len == 0 || M < 1 || N < 1 || K < 0) return 1;
+  HandleView v{};
+  v.cu_count = cu_count;
+  v.ws = (void*)0x1000;  // (never dereferenced, as the operands')
+  v.ws_bytes = kWorkspaceBytes;
+  GatedArgs a{};
+  a.A = a.B = a.B2 = a.C = (void*)0x1000;
+  a.lda = lda;
+  a.ldb = ldb;
+  a.ldb2 = ldb2;
+  a.ldc = N;
+  a.M = (int)M;
+  a.N = (int)N;
+  a.K = (int)K;
+  a.transB = transB;
+  a.op = op;
+  a.in_kind = in_kind;
+  std::string s;
+  auto add = [&](const std::string& kernel, const GatedArgs& p) {
+    s += (s.empty() ? "" : "; ") + kernel + " " + std::to_string(p.M) + "x" + std::to_string(p.N);
+  };
+  auto tiles = [](int idx, int sp) { return std::string(policy_at(idx).name) + (sp > 1 ? "+sk" + std::to_string(sp) : ""); };
+  auto simt = [&](const GatedArgs& all) {
+    const int64_t most = simt_cols(v, all, sums);
+    for (int64_t n0 = 0; n0 < all.N; n0 += most) {
+      const GatedArgs p = part_of(all, 0, n0, all.M, all.N - n0 < most ? all.N - n0 : most);
+      add(gated_simt_thin(p) ? "simt_thin" : "simt_tiles", p);
+    }
+  };
+  const Blocks b = blocks_of(v, a, sums);
+  bool ok = b.cols > 0;
+  for (int64_t m0 = 0; ok && m0 < M; m0 += b.rows) {
+    const GatedArgs part = part_of(a, m0, 0, M - m0 < b.rows ? M - m0 : b.rows, b.cols);
+    const Choice c = choose(v, part, sums, m0 > 0);
+    ok = c.ok;
+    if (!ok) break;
+    if (c.few_cols)
+      add("few_rows_n" + std::to_string(c.few_cols), part);
+    else
+      add(tiles(c.idx, c.sp), c.a1);
+    if (!c.few_cols && c.cut.p >= 0) add(tiles(c.idx2, c.sp2), c.a2);
+  }
+  if (!ok)
+    simt(a);
+  else if (b.cols < N)
+    simt(part_of(a, 0, b.cols, M, N - b.cols));
+  std::snprintf(text, len, "%s", s.c_str());
+  return s.size() < len ? 0 : 1;
+}
 
 gemm_status_t gemm_run_gated(gemm_handle_t h, int transB, int64_t M, int64_t N, int64_t K, float alpha, const void* A,
                              int64_t lda, const void* Bg, int64_t ldbg, const void* Bu, int64_t ldbu,

@@ -93,9 +93,17 @@ double few_rows_us(int op, int in_kind, int transB, int64_t M, int64_t N, int64_
 // Any sizes, strides and alignment (op(A) = A).  With ep.colsum set, *parts receives the number
 // of partial rows written (at most max_parts >= 1).
 hipError_t launch_gated_simt(const GatedArgs& a, int max_parts, int* parts, hipStream_t s);
+bool gated_simt_thin(const GatedArgs& a);  // whether on the kernel for few elements
 
 // Rows of bf16 or fp32 -> 8-bit integers and a factor each.
 hipError_t launch_quantize_i8(int64_t rows, int64_t cols, const void* src, int64_t ld_src, int src_kind, int8_t* dst,
                               int64_t ld_dst, float* scales, hipStream_t s);
 
 }  // namespace dbgemm
+
+// For tests: the launches of a call on a device of cu_count CUs, by the code that makes them, as
+// "kernel[+sk<splits>] rowsxcolumns; ..." in their order (without the launches that add up splits and
+// partial column sums).  op and in_kind as above, the operands' pointers taken as aligned, the workspace a
+// handle's.  0, or 1 where the arguments or the text's length do not do.  Pure host code.
+extern "C" int dbgemm_gated_plan(int op, int in_kind, int transB, int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb,
+                                 int64_t ldb2, int sums, int cu_count, char* text, size_t len);

@@ -295,8 +295,12 @@ void launch_simt(const GatedArgs& a, bool thin, dim3 grid, hipStream_t s) {
 
 }  // namespace
 
+bool gated_simt_thin(const GatedArgs& a) {
+  return a.transB ? (int64_t)a.M * a.N <= kThin : a.N <= kThinCols || a.M <= kThinRows;
+}
+
 hipError_t launch_gated_simt(const GatedArgs& a, int max_parts, int* parts, hipStream_t s) {
-  const bool thin = a.transB ? (int64_t)a.M * a.N <= kThin : a.N <= kThinCols || a.M <= kThinRows;
+  const bool thin = gated_simt_thin(a);
   const int64_t mb = thin ? TR : TS, nb = thin ? TC : TS;
   const int64_t tm = ((int64_t)a.M + mb - 1) / mb, tn = ((int64_t)a.N + nb - 1) / nb;
   int64_t gy = tm < 65535 ? tm : 65535;

@@ -164,7 +164,7 @@ Choice choose(const HandleView& v, const GatedArgs& a, bool sums, bool accumulat
   // chosen ones'
   int few_cols = 0;
   const double few = !accumulate && a.M <= kFewRows
-                         ? few_rows_us(a.op, a.in_kind, a.transB, a.M, a.N, a.K, &few_cols)
+                         ? few_rows_us(a.op, a.in_kind, a.transB, a.M, a.N, a.K, v.cu_count, &few_cols)
                          : 0.0;
   if (few_cols && few < kLeastTilesUs) {
     c.ok = true;

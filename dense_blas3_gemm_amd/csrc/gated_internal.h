@@ -88,7 +88,7 @@ DBGEMM_GT_DECL(2, 1)
 constexpr int64_t kFewRows = 64;
 hipError_t launch_gated_skinny(const GatedArgs& a, int cols, hipStream_t s);
 // The columns that take the least time by a model, and that time in us.
-double few_rows_us(int op, int in_kind, int transB, int64_t M, int64_t N, int64_t K, int* cols);
+double few_rows_us(int op, int in_kind, int transB, int64_t M, int64_t N, int64_t K, int cu_count, int* cols);
 
 // Any sizes, strides and alignment (op(A) = A).  With ep.colsum set, *parts receives the number
 // of partial rows written (at most max_parts >= 1).

@@ -377,9 +377,10 @@ hipError_t launch_rows(const GemmEpArgs& a, hipStream_t s) {
 // of 64 rows to a CU, 16.7 us in five rounds; 8.3 on the tiles), and under half the CUs do not draw the memory's rate (13 x 8864 x 9056, both
 // B [K][N], 8-bit: 57 us at 64 columns, 139 workgroups; 15 x 7760 x 8608 58, 122 of them, and 47 at 32
 // columns).  Fitted to 10500 products of 1 to 64
-// rows, N and K from 256 to 20480, in all kinds, layouts and the three widths: 14 % off in the mean
-// square, its width 1.0 % behind the best of them in the mean.
-double few_rows_us(int op, int in_kind, int transB, int64_t M, int64_t N, int64_t K, int* cols) {
+// rows, N and K from 256 to 20480, in all kinds, layouts and the three widths, on 256 CUs: 14 % off in the
+// mean square, its width 1.0 % behind the best of them in the mean.
+double few_rows_us(int op, int in_kind, int transB, int64_t M, int64_t N, int64_t K, int cu_count, int* cols) {
+  if (cu_count <= 0) cu_count = 256;
   const int bm = few_bm(M), nb = op == GT_GATED ? 2 : 1, es = in_kind == GT_BF16 ? 2 : 1;
   const double its = (double)((K * es + 127) / 128) / 4.0;
   double best = 0.0;
@@ -387,18 +388,18 @@ double few_rows_us(int op, int in_kind, int transB, int64_t M, int64_t N, int64_
   for (int sub : kFewCols) {
     if (!few_fits(bm, sub)) continue;
     const int64_t wgs = (N + sub - 1) / sub;
-    const double whole = 0.85 * (double)((wgs + 255) / 256), share = (double)wgs / 256.0;
-    const double groups = wgs >= 256 && whole > share ? whole : share;
+    const double whole = 0.85 * (double)((wgs + cu_count - 1) / cu_count), share = (double)wgs / cu_count;
+    const double groups = wgs >= cu_count && whole > share ? whole : share;
     const double lines = nb * (transB ? sub : 128 / es) + bm, kb = nb * sub / 8.0;
     double wave = 0.00443 * lines + 0.0240 * kb;
     if (in_kind == GT_E4M3 && transB) wave *= 1.39;  // (the widening, where the lines do not hide it)
     const double all = 4.0 * (0.00114 * lines + 0.0349 * kb) * groups;
     const int held = 160 / (bm + nb * sub);  // workgroups that the LDS of a CU holds, 1 KiB to a row of A or B
-    const int64_t at_once = 256 * (held < 1 ? 1 : held > 8 ? 8 : held);
+    const int64_t at_once = (int64_t)cu_count * (held < 1 ? 1 : held > 8 ? 8 : held);
     const double more = (double)((wgs + at_once - 1) / at_once - 1), results = bm * sub * nb / 1024.0;
     double us = 2.75 + 0.696 * results + more * (0.874 + 0.689 * results) +
                 its * std::sqrt(std::sqrt(wave * wave * wave * wave + all * all * all * all));
-    if (sub == 64 && wgs < 128) us *= 1.2;
+    if (sub == 64 && 2 * wgs < cu_count) us *= 1.2;
     if (*cols == 0 || us < best) {
       best = us;
       *cols = sub;

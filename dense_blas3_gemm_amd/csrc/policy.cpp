@@ -127,20 +127,20 @@ constexpr double K0 = 256.0;  // prologue + epilogue cost of a tile, in K-equiva
 // tile at efficiency 0.5 advances about 265 K per us).
 constexpr double kUnitsPerUs = 2.0e6;
 
-// What the operands of a gated operator's grid take to be fetched, in us on 256 CUs: a CU asks for
+// What the operands of a gated operator's grid take to be fetched, in us: a CU asks for
 // so many lines (128 bytes, or the piece of one that a tile takes of a row of B [K][N]) and moves so
 // many bytes (the rates of the few-row kernel's model, less a tenth).  It decides where there are
 // few rows of A, or few columns of 1-byte elements to a tile: 37 x 10944 x 6368 of 8-bit integers,
 // both B [K][N], 62 us on 64 x 64 tiles, 32 bytes of a row each, and 42 on 128 x 128.  Over 1500 drawn
 // products the choice was 4.4 % behind the fastest for up to 64 rows and 2.3 % for more; with this
 // 3.0 and 1.7.
-double fetch_us(const Policy& p, const Problem& pr) {
+double fetch_us(const Policy& p, const Problem& pr, int cu_count) {
   const double tiles = (double)((pr.M + p.BM - 1) / p.BM) * (double)((pr.N + p.BN - 1) / p.BN);
   const double kt = (double)((pr.K * (pr.in_fp8 ? 1 : 2) + 127) / 128);  // K tiles of 128 bytes
   const double cols = (double)p.BN / pr.products;                        // of each B
   const double pieces = cols * pr.elem > 128 ? cols * pr.elem / 128 : 1.0;
   const double lines = pr.products * (pr.transB ? cols : 128.0 / pr.elem * pieces) + p.BM;
-  return 0.9 * tiles / 256.0 * kt * (0.00141 * lines + 0.0401 * p.BN / 8.0);
+  return 0.9 * tiles / cu_count * kt * (0.00141 * lines + 0.0401 * p.BN / 8.0);
 }
 }  // namespace
 
@@ -184,7 +184,7 @@ int policy_select(const Problem& pr, int cu_count, int64_t ws_floats, int* split
       // tiles split in two 52 us, 128 x 128 unsplit 39)
       if (sp > 1 && pr.ep) t += tiles * sp * p.BM * p.BN * 8.0 / 4.0e6 * kUnitsPerUs;
       if (pr.products) {
-        const double f = fetch_us(p, pr) * kUnitsPerUs;
+        const double f = fetch_us(p, pr, cu_count) * kUnitsPerUs;
         if (have && (t >= best_t || f >= best_t)) continue;  // (the root is not for nothing)
         t = std::sqrt(std::sqrt(t * t * t * t + f * f * f * f));
       }

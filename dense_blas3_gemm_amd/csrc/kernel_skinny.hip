@@ -306,14 +306,19 @@ __global__ __launch_bounds__(WAVES * 64) void gemm_skinny_kernel(KernelArgs a) {
 // whatever is taken of it.
 constexpr int kFewCols[] = {16, 32, 64};
 constexpr int few_bm(int64_t M) { return M <= 16 ? 16 : M <= 32 ? 32 : 64; }
-constexpr bool few_fits(int bm, int sub) { return bm * sub / 8 <= 256; }  // (the epilogue's one step)
+// The epilogue's one step; and for 64 rows of two B the least columns only, but for E4M3 B [N][K] (widens):
+// of 200000 drawn products of 33 to 64 rows none was given more, since where more would be the better width
+// the tiles take less time still.
+constexpr bool few_fits(int bm, int sub, int nb, bool widens) {
+  return bm * sub / 8 <= 256 && (bm < 64 || nb == 1 || sub == kFewCols[0] || widens);
+}
 
 // BM rows, SUB columns of each B, K tiles of 128 bytes of A, four waves of two slots each (three
 // slots, or eight waves, measured alike or slower by up to 30 %)
 template <int BM, int SUB, int IN, bool KC, int OP>
 hipError_t launch(const GatedArgs& a, hipStream_t s) {
-  if constexpr (few_fits(BM, SUB)) {
-    constexpr bool DUAL = OP == GT_GATED;
+  constexpr bool DUAL = OP == GT_GATED;
+  if constexpr (few_fits(BM, SUB, DUAL ? 2 : 1, IN == IN_E4M3_LDS && KC)) {
     using C = Cfg<BM, DUAL ? 2 * SUB : SUB, IN == IN_BF16 ? 64 : 128, 1, 1, 16, 2, IN, false, KC, 1, DUAL>;
     hipLaunchKernelGGL((gemm_skinny_kernel<C, 4, OP>), dim3((unsigned)((a.N + SUB - 1) / SUB)), dim3(256), 0, s, a);
     return hipGetLastError();
@@ -386,7 +391,7 @@ double few_rows_us(int op, int in_kind, int transB, int64_t M, int64_t N, int64_
   double best = 0.0;
   *cols = 0;
   for (int sub : kFewCols) {
-    if (!few_fits(bm, sub)) continue;
+    if (!few_fits(bm, sub, nb, in_kind == GT_E4M3 && transB)) continue;
     const int64_t wgs = (N + sub - 1) / sub;
     const double whole = 0.85 * (double)((wgs + cu_count - 1) / cu_count), share = (double)wgs / cu_count;
     const double groups = wgs >= cu_count && whole > share ? whole : share;

@@ -4,7 +4,7 @@ whole, products in two launches along either side.  Whole numbers with every sum
 of additions gives the exact sum, and what follows it is compared bit by bit."""
 import pytest
 
-from gated_plan import FORMS, PAD, SHAPES
+from gated_plan import FORMS, PAD, SHAPES, plan
 from test_gpu_gated_split import product, whole
 
 pytestmark = pytest.mark.gpu
@@ -57,3 +57,29 @@ def test_whole_numbers(gpu, shape, form):
         torch.cuda.synchronize()
         assert torch.equal(C, (x.clamp(min=0) + 2.0 * R.float()).bfloat16())
     assert all((t[:, N:] == -7).all() for _, t in bufs)
+
+
+@pytest.mark.parametrize("form", [f for f in FORMS if f[0] != "gated"])
+def test_operands_of_many_megabytes(gpu, form):
+    """G and U, or an fp32 residual, of more than 128 MB: 256 x 256 tiles read them past the caches."""
+    import torch
+    (op, kind, tB), (M, N, K) = form, (5003, 7696, 272)
+    assert any(p.splits == 1 and "_pp_m256n256" in p.kernel for p in plan(*form, M, N, K, sums=op == "dgated", pad=PAD))
+    A, B = whole(M, K, 2, 0, kind, PAD), whole(*((N, K) if tB else (K, N)), 2, 1, kind, PAD)
+    x = product(A, B, tB)
+    if op == "dgated":
+        g, u = whole(M, N, 2, 3, pad=8), whole(M, N, 2, 4, pad=1)
+        (dg, dgb), (du, dub), s = out(M, N, 1, "float32"), out(M, N, 3, "float32"), torch.empty(2, N, device="cuda")
+        gpu.run_dgated(A, B, g, u, dg, du, transB=tB, act="relu", dbias_g=s[0], dbias_u=s[1])
+        on = (g > 0).float()
+        wg, wu = x * u.float() * on, x * g.float() * on
+        torch.cuda.synchronize()
+        assert torch.equal(dg, wg) and torch.equal(du, wu)
+        assert torch.equal(s[0].double(), wg.double().sum(0)) and torch.equal(s[1].double(), wu.double().sum(0))
+        assert (dgb[:, N:] == -7).all() and (dub[:, N:] == -7).all()
+    else:
+        one, R = torch.ones(max(M, N), device="cuda"), whole(M, N, 100, 2, pad=1).float()
+        C, buf = out(M, N, 8, "float32")
+        gpu.run_i8(A, one[:M], B, one[:N], C, transB=tB, act="relu", residual=R[:, :N], beta=2.0)
+        torch.cuda.synchronize()
+        assert torch.equal(C, x.clamp(min=0) + 2.0 * R[:, :N]) and (buf[:, N:] == -7).all()

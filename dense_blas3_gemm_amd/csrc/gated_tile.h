@@ -90,16 +90,10 @@ __device__ __forceinline__ void gt_bf16(const ep_u32x4& r, float (&v)[8]) {
   }
 }
 
-// Eight sums of a row times its factor s and their columns' c (kFarFactor).
-__device__ __forceinline__ void gt_scale8(float (&w)[8], float s, const float (&c)[8]) {
-  const bool far = __builtin_fabsf(s) > kFarFactor;
-  if (__any(far)) {  // (a branch of the whole wave, and next to never taken)
+// Eight sums of a row times its factor s and their columns' c, plus b (kFarFactor).
+__device__ __forceinline__ void gt_scale8(float (&w)[8], float s, const float (&c)[8], const float (&b)[8], bool far) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = w[i] * (far ? c[i] : s) * (far ? s : c[i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = w[i] * s * c[i];
-  }
+  for (int i = 0; i < 8; ++i) w[i] = __builtin_fmaf(w[i] * (far ? c[i] : s), far ? s : c[i], b[i]);
 }
 
 // Eight columns of row m: w, w2 the products (w2 of the second B), alpha applied, or the whole
@@ -126,13 +120,20 @@ __device__ __forceinline__ void gt_finish8(const GatedArgs& a, float (&w)[8], fl
     if (e.H) ep_store8<NT, EP_NONE>((uint16_t*)e.H + m * e.ldh + n, 8, h);
   } else {
     if constexpr (I8) {
-      gt_scale8(w, r.s, c.s);
-      if constexpr (OP == GT_GATED) gt_scale8(w2, r.s, c.s2);
-    }
+      const bool far = __builtin_fabsf(r.s) > kFarFactor;
+      if (__builtin_expect(__any(far), 0)) {  // (a branch of the whole wave: selects would be two an element)
+        gt_scale8(w, r.s, c.s, c.b, far);
+        if constexpr (OP == GT_GATED) gt_scale8(w2, r.s, c.s2, c.b2, far);
+      } else {
+        gt_scale8(w, r.s, c.s, c.b, false);
+        if constexpr (OP == GT_GATED) gt_scale8(w2, r.s, c.s2, c.b2, false);
+      }
+    } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      w[i] += c.b[i];
-      if constexpr (OP == GT_GATED) w2[i] += c.b2[i];
+      for (int i = 0; i < 8; ++i) {
+        w[i] += c.b[i];
+        if constexpr (OP == GT_GATED) w2[i] += c.b2[i];
+      }
     }
     if constexpr (OP == GT_GATED) {
       if (e.G) ep_store8<NT, EP_NONE>((uint16_t*)e.G + m * e.ldg + n, 8, w);

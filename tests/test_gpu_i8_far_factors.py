@@ -70,13 +70,13 @@ def test_gated_products(gpu, shape, tB):
 
 
 def test_the_lowest_value_in_a_row(gpu):
-    """Quantised with bf16's lowest value among its elements, times weights; its neighbours keep the bits
-    that they have beside an ordinary row."""
+    """Quantised with bf16's lowest value among its elements, times weights, and a bias; its neighbours keep
+    the bits that they have beside an ordinary row (the bias's rounding is one more)."""
     import torch
     for M, N, K in ((5, 64, 272), (300, 512, 96), (65, 129, 71)):
         r = torch.Generator().manual_seed(M)
         x = torch.randn(M, K, generator=r).bfloat16()
-        w = torch.randn(N, K, generator=r) * 1e-3
+        w, bias = torch.randn(N, K, generator=r) * 1e-3, torch.randn(N, generator=r)
         low = x.clone()
         low[1, 3] = torch.finfo(torch.bfloat16).min
         out = []
@@ -86,10 +86,10 @@ def test_the_lowest_value_in_a_row(gpu):
             gpu.quantize_i8(v.cuda(), q, s)
             gpu.quantize_i8(w.cuda(), b, sb)
             C = torch.empty(M, N, device="cuda")
-            gpu.run_i8(q, s, b, sb, C, transB=1)
+            gpu.run_i8(q, s, b, sb, C, transB=1, bias=bias.cuda())
             torch.cuda.synchronize()
             P = gated.product_i8(q.cpu().numpy(), s.cpu().numpy(), b.cpu().numpy(), sb.cpu().numpy(), 1)[0]
-            near(host(C), P, 4 * U * np.abs(P) + 2.0 ** -149, (M, N, K))
+            near(host(C), P + bias.numpy(), 4 * U * np.abs(P) + U * np.abs(P + bias.numpy()) + 2.0 ** -149, (M, N, K))
             out.append(C)
         rest = [i for i in range(M) if i != 1]
         assert torch.equal(out[0][rest], out[1][rest])

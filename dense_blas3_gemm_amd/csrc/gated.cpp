@@ -15,7 +15,7 @@ using namespace dbgemm;
 
 namespace {
 
-// What an epilogue reads past the caches (GatedEp::past): where it would fill half of them.
+// What an epilogue reads past the caches (GatedEp::past, with both sides measured): half of them.
 constexpr double kPastBytes = (double)(128 << 20);
 
 // Columns that the generic kernels take in a launch: a launch ends at 2^32 threads, the one for few
@@ -134,8 +134,9 @@ bool operands_ok(const GatedArgs& a, int64_t cols) {
 }
 
 // The tile model's cost (2e6 units to about a microsecond) as the time of a call of a few rows,
-// each kind with its own factor: a fit, 9 to 10 % off in the mean square.  Column sums are one more
-// launch.
+// each kind with its own factor: a fit, 9 to 10 % off in the mean square, so that near ties may go to the
+// slower side (24 x 13696 x 5120 of 8-bit integers, both B [N][K]: 32.5 us on the tiles that are chosen,
+// 29.5 on the few-row kernel).  Column sums are one more launch.
 double tiles_us(int in_kind, double cost, bool sums) {
   const double factor = in_kind == GT_BF16 ? 0.77 : in_kind == GT_E4M3 ? 0.64 : 0.79;
   return 3.6 + factor * cost / 2.0e6 + (sums ? 4.0 : 0.0);

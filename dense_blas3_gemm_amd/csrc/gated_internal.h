@@ -37,9 +37,13 @@ struct GatedEp {
   int64_t ldd2;
   void* H;  // bf16, or null
   int64_t ldh;
-  // What the epilogue reads, the residual or G and U, does not fit the caches (256 MB): the 256 x 256
-  // tiles read it past them.  The gradient of 8192 x 10240 x 1024 290 -> 275 us, 8-bit integers with
-  // a residual at 8192 x 8192 x 1024 125 -> 111.  A smaller one may still be there from whoever wrote
+  // What the epilogue reads, the residual or G and U, would fill half of the caches (128 of 256 MB) or
+  // more: the 256 x 256 tiles read it past them.  us through them and past, three sets of buffers in
+  // turn: 8-bit integers with a bf16 residual, K = 1024, 2048 x 8192 (32 MB) 28.5 and 31.7, 4096 x 8192
+  // (64) 56.6 and 61.0, 4096 x 12288 (96) 81.9 and 81.1, 8192 x 8192 (128) 129 and 113, 8192 x 12288 (192)
+  // 167 and 153; with K = 4096 62 and 64.5, 135 and 127, 194 and 183, 269 and 244, 382 and 359; a gradient,
+  // K = 1024, 64 MB of G and U 48.6 and 53.2, 128 106 and 102, 256 210 and 196.  So past them is the faster
+  // from 128 MB on throughout, and from 64 to 96 by K; a smaller one may still be there from whoever wrote
   // it (1078 x 7888 x 2240 with an fp32 residual, 34 MB, 39 us, past the caches 52).
   int past;
   float* colsum;  // fp32 partial sums, [part][2][whole8(N)], or null

@@ -8,9 +8,9 @@
 // neither product exists outside the registers.
 //
 // The K loops around it are bound by the MFMA at large sizes (4096 x 13696 x 5120 with G and U kept
-// 935 us, 1229 TFLOP/s; 8192 x 13696 x 5120 of 8-bit integers 960 us, 2390 T op/s).  The epilogue is
+// 935 us, 1229 TFLOP/s; 8192 x 13696 x 5120 of 8-bit integers 938 us, 2450 T op/s).  The epilogue is
 // bound by memory, and by the VALU for GELU (erf), and nothing of it runs beside the next tile's
-// products: a gradient at 4096 x 13696 x 5120, 561 MB in and out of its epilogue, 540 us where its
+// products: a gradient at 4096 x 13696 x 5120, 561 MB in and out of its epilogue, 521 us where its
 // products alone take 430.  (Asking for four steps of G and U ahead instead of two, staggering the
 // workgroups' starts and leaving out the partial sums changed nothing.)
 #pragma once
@@ -197,8 +197,10 @@ constexpr int gt_pass_rows(int step) {
 // acc: the 16x16 fragments of this wave, whose results start at row m0, column n0 (of both
 // products).  lds0: LDS_BYTES of LDS, free once every wave has passed the barrier here.  The
 // 16-byte chunks of an LDS row are XOR-swizzled by the row.  What the rows bring from memory is
-// asked for ahead, up to BATCH steps of rows at a time.  NT: the outputs go past the caches; NTL: so do
-// the rows that are read.
+// asked for ahead, up to BATCH steps of rows at a time.  NT: the outputs go past the caches (the 256 x 256
+// tiles, whatever their size: a gated product alone up to 13 % faster than with cached stores at 8 to 107 MB of H,
+// 2048 x 8192 x 2048 104 us and 118; with the product that reads H behind it 0.4 to 2 %, but for the
+// smallest, 1531 x 2736 x 1000 with 8 MB, where the two take 62.1 and 58.1).  NTL: so do the rows that are read.
 template <class C, int OP, int LDS_BYTES, bool NT, bool NTL>
 __device__ __forceinline__ void gt_tile(const GatedArgs& a, const typename AccOf<C::MT>::T (&acc)[C::FM][C::FN], int m0,
                                         int n0, int part, int wave, int lane, uint32_t lds0) {

@@ -376,14 +376,15 @@ hipError_t launch_rows(const GemmEpArgs& a, hipStream_t s) {
 // A workgroup's wave takes every fourth of the K tiles (128 bytes of K).  A K tile costs a wave what
 // its lines (128 bytes, or the piece of one that a row of B [K][N] has in these columns) and its
 // bytes take to be asked for; and all workgroups together need the CU's share of the memory's rate
-// and of its line requests, whole workgroups to a CU (1 x 10944 x 4096, both B [N][K]: 33 us at 16
-// columns, 684 workgroups, 37.5 at 32, 342 of them, and 34 at 64).  Past what the CUs hold at once
-// every further round starts and ends on its own (55 x 17840 x 272 of 8-bit integers, one workgroup
-// of 64 rows to a CU, 16.7 us in five rounds; 8.3 on the tiles), and under half the CUs do not draw the memory's rate (13 x 8864 x 9056, both
-// B [K][N], 8-bit: 57 us at 64 columns, 139 workgroups; 15 x 7760 x 8608 58, 122 of them, and 47 at 32
-// columns).  Fitted to 10500 products of 1 to 64
-// rows, N and K from 256 to 20480, in all kinds, layouts and the three widths, on 256 CUs: 14 % off in the
-// mean square, its width 1.0 % behind the best of them in the mean.
+// and of its line requests, whole workgroups to a CU (1 x 10944 x 4096, both B [N][K]: 39.3 us at 32
+// columns, 342 workgroups, and 34.4 at 16, 684 of them).  Past what the CUs hold at once every further
+// round starts and ends on its own (55 x 17840 x 272 of 8-bit integers, one workgroup of 64 rows to a CU,
+// 16.7 us in five rounds; 8.3 on the tiles), and under half the CUs do not draw the memory's rate
+// (13 x 8864 x 9056, both B [K][N], 8-bit: 57 us at 64 columns, 139 workgroups; 15 x 7760 x 8608 58, 122 of
+// them, and 47 at 32 columns).  Fitted to 10500 products of 1 to 64 rows, N and K from 256 to 20480, in all
+// kinds, layouts and the three widths, on 256 CUs: 14 % off in the mean square, its width 1.0 % behind the
+// best of them in the mean.  Near ties it misses: 1 x 10944 x 4096 is given 64 columns, 35.6 us by the model
+// and 36.3 at 16, and measures 37.4 there with its weights out of the caches.
 double few_rows_us(int op, int in_kind, int transB, int64_t M, int64_t N, int64_t K, int cu_count, int* cols) {
   if (cu_count <= 0) cu_count = 256;
   const int bm = few_bm(M), nb = op == GT_GATED ? 2 : 1, es = in_kind == GT_BF16 ? 2 : 1;
